@@ -280,6 +280,113 @@ typedef struct {
 wl_status wl_describe_nvfp4_plan(int M, int K, const wl_proj_nvfp4 *projs, int P, int num_sms,
                                  wl_nvfp4_plan *out);
 
+/* ------------------------------------------------------- 8-bit weights ----
+ * A matrix in 8 bits ("fp8 matrix"): E4M3 codes and one power-of-two scale 2^E
+ * per block of block_rows x 128 elements, block_rows 1 (activations, blocks
+ * along a row) or 128 (weights).
+ *   codes  : rows x cols bytes, row-major, 16-byte aligned, cols % 16 == 0
+ *   scales : ceil(rows / block_rows) rows of WL_FP8_SCALE_PITCH(cols) bytes,
+ *            4-byte aligned; byte b of a row is E + 127 (E8M0) of columns
+ *            128 b .. 128 b + 127, bytes behind the last block hold 127
+ * E is the smallest integer with 448 * 2^E >= max|a| over the block's finite
+ * elements, at least -127, and 0 for a block whose finite elements are all 0.
+ * The code is a * 2^-E (exact) rounded to nearest-even E4M3; an element that
+ * is not finite gets the NaN code 0x7F.  The scales being powers of two, the
+ * tensor cores apply them themselves (block-scaled MMA) and the codes do not
+ * depend on the precision in which the quotient is formed. */
+#define WL_FP8_SCALE_PITCH(cols) (4 * (((cols) + 511) / 512))
+
+typedef enum { WL_BF16 = 0, WL_F32 = 1 } wl_type;
+
+/* Codes and scales of a rows x cols matrix `a` (device, row-major, 16-byte
+ * aligned, bf16 or fp32).  block_rows is 1 or 128.  rows, cols >= 0.
+ * Asynchronous on `stream`.  WL_ERR_INVALID_ARG for null pointers, negative
+ * sizes, another type or block_rows; WL_ERR_ALIGNMENT for cols % 16 != 0 or
+ * pointers that are not aligned as above. */
+wl_status wl_quantize_fp8(const void *a, wl_type type, int rows, int cols, int block_rows,
+                          uint8_t *codes, uint8_t *scales, void *stream);
+
+/* y = A B^T for two fp8 matrices: A M x K with 1 x 128 blocks, B N x K with
+ * 128 x 128 blocks, y M x N bf16 row-major (2-byte aligned).  fp32
+ * accumulation, one rounding.  `workspace` (16-byte aligned) holds at least
+ * wl_matmul_fp8_workspace(M, N, K) bytes; its contents need no preparation.
+ * Asynchronous on `stream`; M, N, K >= 0 (K == 0 writes zeros).
+ * WL_ERR_INVALID_ARG for null pointers, negative sizes or a workspace that is
+ * too small, WL_ERR_ALIGNMENT for K % 16 != 0 or misaligned pointers. */
+wl_status wl_matmul_fp8(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *b_codes,
+                        const uint8_t *b_scales, wl_bf16 *y, int M, int N, int K,
+                        void *workspace, size_t workspace_bytes, void *stream);
+size_t wl_matmul_fp8_workspace(int M, int N, int K);
+
+/* One projection of an 8-bit call: W0 as an fp8 matrix with 128 x 128 blocks. */
+typedef struct {
+    const uint8_t *codes;  /* N x K                                            */
+    const uint8_t *scales; /* ceil(N / 128) x WL_FP8_SCALE_PITCH(K)            */
+    const float *s;        /* N                                                */
+    const wl_bf16 *U;      /* N x r row-major, 16-byte aligned (NULL iff r == 0) */
+    const wl_bf16 *V;      /* K x r row-major, 16-byte aligned (NULL iff r == 0) */
+    wl_bf16 *y;            /* M x N row-major (output)                         */
+    wl_bf16 *T;            /* M x r row-major, 16-byte aligned (output: x V rounded
+                              to bf16), or NULL when it is not wanted          */
+    int N;                 /* output rows, >= 0                                */
+    int r;                 /* rank, 0 <= r <= WL_MAX_RANK, r % 8 == 0          */
+} wl_proj_fp8;
+
+/* The stacked forward with 8-bit shared blocks and 8-bit activations: x is
+ * quantised in blocks of 1 x 128 (x^), and for each projection
+ *   T_p = x V_p,   y_p = s_p (.) (x^ W0_p^T) + T_p U_p^T,
+ * with fp32 accumulation; T is formed from x itself (bf16) and rounded to
+ * bf16 as an operand of the second product; y is rounded once to bf16.
+ *   x_codes, x_scales : where the quantised x is left (M x K codes and
+ *     M x WL_FP8_SCALE_PITCH(K) scales), or both NULL.  Together with the
+ *     projections' T they are the 8-bit checkpoint that
+ *     wl_stacked_backward_fp8 reads in place of x.
+ *   workspace : at least wl_stacked_forward_fp8_workspace(M, K, projs, P)
+ *     bytes, 16-byte aligned, contents arbitrary; calls that overlap on the
+ *     GPU need one each, and a captured graph keeps using the one it was
+ *     captured with.
+ * Any M >= 0.  Unlike the bf16 calls it may directly follow the kernel that
+ * writes its weights.  Errors: those of wl_stacked_forward;
+ * WL_ERR_ALIGNMENT for K % 16 != 0, r % 8 != 0 or misaligned pointers;
+ * WL_ERR_INVALID_ARG for a workspace that is too small or only one of
+ * x_codes and x_scales. */
+wl_status wl_stacked_forward_fp8(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, int P,
+                                 uint8_t *x_codes, uint8_t *x_scales, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+/* Depends on the sizes alone (the pointers are not read); 0 for sizes that
+ * the forward refuses. */
+size_t wl_stacked_forward_fp8_workspace(int M, int K, const wl_proj_fp8 *projs, int P);
+
+/* One projection of a backward call.  ds, dU, dV may be NULL (not wanted). */
+typedef struct {
+    const uint8_t *codes, *scales; /* W0 as in wl_proj_fp8                      */
+    const float *s;
+    const wl_bf16 *U, *V;  /* as in wl_proj_fp8                                 */
+    const wl_bf16 *T;      /* M x r, as the forward left it (NULL iff r == 0)   */
+    const wl_bf16 *dy;     /* M x N row-major, 2-byte aligned                   */
+    float *ds;             /* N (output)                                        */
+    wl_bf16 *dU;           /* N x r (output), 16-byte aligned                   */
+    wl_bf16 *dV;           /* K x r (output), 16-byte aligned                   */
+    int N, r;
+} wl_grad_fp8;
+
+/* Gradients of wl_stacked_forward_fp8 with respect to x and to each layer's
+ * own parameters, from the checkpoint (x^ as x_codes / x_scales, and T_p):
+ *   E_p  = dy_p U_p
+ *   g_p  = s_p (.) dy_p quantised in blocks of 1 x 128 along N
+ *   dx   = sum_p g_p W0_p + E_p V_p^T                   (M x K bf16; or NULL)
+ *   ds_p = sum_m dy_p (.) (x^ W0_p^T)                   (fp32)
+ *   dU_p = dy_p^T T_p,  dV_p = (x^)^T E_p               (bf16)
+ * The quantisation of x counts as the identity.  W0 has no gradient: the
+ * layers of a band share it.  E is rounded to bf16 as an operand; all sums
+ * are fp32, in an order fixed by the sizes, so results are reproducible.  dx
+ * must not overlap the inputs.  M == 0 writes zero ds, dU, dV.  Workspace,
+ * errors and ordering as in wl_stacked_forward_fp8. */
+wl_status wl_stacked_backward_fp8(const uint8_t *x_codes, const uint8_t *x_scales, int M, int K,
+                                  const wl_grad_fp8 *projs, int P, wl_bf16 *dx, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+size_t wl_stacked_backward_fp8_workspace(int M, int K, const wl_grad_fp8 *projs, int P);
+
 /* Host-side decomposition of L dense layer weights into theta bundles
  * ("Quality", "Why sharing fails": band-mean W0, per-row scale s, low-rank
  * residual; "Add a new model architecture", "Decompose HF weights" step 4).

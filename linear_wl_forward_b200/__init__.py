@@ -7,6 +7,7 @@ missing or was built for another device, calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -16,6 +17,8 @@ __all__ = [
     "materialize_weight", "describe_decode_plan", "DecodePlan", "describe_rows_plan", "RowsPlan",
     "describe_nvfp4_plan", "Nvfp4Plan",
     "quantize_nvfp4",
+    "quantize_fp8", "matmul_fp8", "stacked_forward_fp8", "prepare_stacked_fp8", "PreparedForwardFp8",
+    "Fp8Checkpoint", "stacked_backward_fp8", "fp8_scale_pitch",
     "decompose",
     "relative_frobenius_error", "last_device_status", "wait_probe", "set_wait_limit", "PATHS",
     "DECODE_MAX_M", "MAX_RANK", "MAX_PROJ", "STATUS",
@@ -55,6 +58,16 @@ class _ProjNvfp4(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("tensor_scale", ctypes.c_float),
                 ("s", ctypes.c_void_p), ("U", ctypes.c_void_p), ("V", ctypes.c_void_p), ("y", ctypes.c_void_p),
                 ("N", ctypes.c_int), ("r", ctypes.c_int)]
+
+
+class _ProjFp8(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "scales", "s", "U", "V", "y", "T")] + \
+               [("N", ctypes.c_int), ("r", ctypes.c_int)]
+
+
+class _GradFp8(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "scales", "s", "U", "V", "T", "dy", "ds", "dU", "dV")] + \
+               [("N", ctypes.c_int), ("r", ctypes.c_int)]
 
 
 class RowsPlan(ctypes.Structure):
@@ -105,6 +118,17 @@ def lib():
         L.wl_describe_rows_plan.argtypes = [ci, ci, ctypes.POINTER(_Proj), ci, ci, ctypes.POINTER(RowsPlan)]
         L.wl_describe_nvfp4_plan.argtypes = [ci, ci, ctypes.POINTER(_ProjNvfp4), ci, ci, ctypes.POINTER(Nvfp4Plan)]
         L.wl_quantize_nvfp4.argtypes = [vp, ci, ci, ctypes.c_float, vp, vp, ctypes.POINTER(ctypes.c_float)]
+        sz = ctypes.c_size_t
+        L.wl_quantize_fp8.argtypes = [vp, ci, ci, ci, ci, vp, vp, vp]
+        L.wl_matmul_fp8.argtypes = [vp] * 5 + [ci] * 3 + [vp, sz, vp]
+        L.wl_matmul_fp8_workspace.argtypes = [ci] * 3
+        L.wl_stacked_forward_fp8.argtypes = [vp, ci, ci, ctypes.POINTER(_ProjFp8), ci, vp, vp, vp, sz, vp]
+        L.wl_stacked_forward_fp8_workspace.argtypes = [ci, ci, ctypes.POINTER(_ProjFp8), ci]
+        L.wl_stacked_backward_fp8.argtypes = [vp, vp, ci, ci, ctypes.POINTER(_GradFp8), ci, vp, vp, sz, vp]
+        L.wl_stacked_backward_fp8_workspace.argtypes = [ci, ci, ctypes.POINTER(_GradFp8), ci]
+        for name in ("wl_matmul_fp8_workspace", "wl_stacked_forward_fp8_workspace",
+                     "wl_stacked_backward_fp8_workspace"):
+            getattr(L, name).restype = sz
         L.wl_relative_frobenius_error.argtypes = [vp] * 5 + [ci] * 3
         L.wl_relative_frobenius_error.restype = ctypes.c_double
         L.wl_status_string.argtypes = [ci]
@@ -119,7 +143,8 @@ def lib():
                      "wl_decompose", "wl_decompose_als",
                      "wl_materialize_weight", "wl_describe_decode_plan", "wl_describe_rows_plan",
                      "wl_describe_nvfp4_plan",
-                     "wl_quantize_nvfp4",
+                     "wl_quantize_nvfp4", "wl_quantize_fp8", "wl_matmul_fp8", "wl_stacked_forward_fp8",
+                     "wl_stacked_backward_fp8",
                      "wl_last_device_status", "wl_wait_probe", "wl_set_wait_limit", "wl_noalloc_last_status"):
             getattr(L, name).restype = ci
         _lib = L
@@ -199,6 +224,260 @@ def stacked_forward_nvfp4(x, projs, ys=None, stream=None):
     _check(lib().wl_stacked_forward_nvfp4(_dev_ptr(x, torch.bfloat16, "x", (M, K)), M, K, arr, len(projs),
                                           _stream_handle(stream)), "wl_stacked_forward_nvfp4")
     return ys
+
+
+def fp8_scale_pitch(cols: int) -> int:
+    """Bytes per row of the scales of an 8-bit matrix with `cols` columns
+    (include/wl.h, WL_FP8_SCALE_PITCH)."""
+    return 4 * ((cols + 511) // 512)
+
+
+@contextlib.contextmanager
+def _launch_on(device, stream):
+    """Makes `device` current and, when a stream (torch stream or raw handle)
+    is given, that stream too, so that what the call allocates belongs to the
+    stream it runs on.  Yields the stream's handle."""
+    import torch
+
+    with contextlib.ExitStack() as stack:
+        if device.index != torch.cuda.current_device():
+            stack.enter_context(torch.cuda.device(device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            elif stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+            stack.enter_context(torch.cuda.stream(stream))
+        yield torch.cuda.current_stream().cuda_stream
+
+
+def _dev_ptrs(device, *checks):
+    """_dev_ptr of each (tensor, dtype, name, shape), all on `device`."""
+    ptrs = []
+    for t, dtype, name, shape in checks:
+        ptrs.append(_dev_ptr(t, dtype, name, shape))
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return ptrs
+
+
+def _need_cuda(t, name, dims=2):
+    import torch
+
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+
+
+def _workspace(nbytes, device):
+    import torch
+
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def quantize_fp8(a, block_rows=1, codes=None, scales=None, stream=None):
+    """An 8-bit matrix (include/wl.h, wl_quantize_fp8): E4M3 codes and one
+    power-of-two scale per block of block_rows (1: activations, 128: weights)
+    x 128 elements.  a: R x C bf16 or fp32, C % 16 == 0.  Returns (codes R x C
+    uint8, scales ceil(R / block_rows) x fp8_scale_pitch(C) uint8)."""
+    import torch
+
+    _need_cuda(a, "a")
+    if a.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"a must be bfloat16 or float32, got {a.dtype}")
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
+    R, C = a.shape
+    shape = (-(-R // block_rows), fp8_scale_pitch(C))
+    with _launch_on(a.device, stream) as handle:
+        if codes is None:
+            codes = torch.empty(R, C, dtype=torch.uint8, device=a.device)
+        if scales is None:
+            scales = torch.empty(shape, dtype=torch.uint8, device=a.device)
+        ap, cp, sp = _dev_ptrs(a.device, (a, a.dtype, "a", None), (codes, torch.uint8, "codes", (R, C)),
+                               (scales, torch.uint8, "scales", shape))
+        _check(lib().wl_quantize_fp8(ap, int(a.dtype == torch.float32), R, C, block_rows, cp, sp, handle),
+               "wl_quantize_fp8")
+    return codes, scales
+
+
+def matmul_fp8(a, b, y=None, stream=None):
+    """y = A B^T for 8-bit matrices (codes, scales): a M x K with 1 x 128
+    blocks, b N x K with 128 x 128 blocks (include/wl.h, wl_matmul_fp8).
+    Returns y (M x N bf16)."""
+    import torch
+
+    (ac, asc), (bc, bsc) = a, b
+    _need_cuda(ac, "a codes")
+    _need_cuda(bc, "b codes")
+    (M, K), N, dev = ac.shape, bc.shape[0], ac.device
+    pitch = fp8_scale_pitch(K)
+    with _launch_on(dev, stream) as handle:
+        if y is None:
+            y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+        ptrs = _dev_ptrs(dev, (ac, torch.uint8, "a codes", (M, K)), (asc, torch.uint8, "a scales", (M, pitch)),
+                         (bc, torch.uint8, "b codes", (N, K)),
+                         (bsc, torch.uint8, "b scales", (-(-N // 128), pitch)), (y, torch.bfloat16, "y", (M, N)))
+        n = lib().wl_matmul_fp8_workspace(M, N, K)
+        ws = _workspace(n, dev)
+        _check(lib().wl_matmul_fp8(*ptrs, M, N, K, _ptr(ws), n, handle), "wl_matmul_fp8")
+    return y
+
+
+class Fp8Checkpoint:
+    """What stacked_backward_fp8 reads in place of x: x in 8 bits (codes M x K
+    and scales M x fp8_scale_pitch(K), uint8) and each projection's T = x V
+    (M x r bf16; None for r = 0)."""
+
+    __slots__ = ("codes", "scales", "T")
+
+    def __init__(self, codes, scales, T):
+        self.codes, self.scales, self.T = codes, scales, list(T)
+
+
+def _weight_fp8(dev, codes, scales, s, U, V, K):
+    """(codes, scales, s, U, V) pointers, N and r of one 8-bit projection."""
+    import torch
+
+    _need_cuda(codes, "codes")
+    N = codes.shape[0]
+    r = 0 if U is None else U.shape[1]
+    if (U is None) != (V is None):
+        raise ValueError("U and V must both be given or both be None")
+    if r == 0:
+        U = V = None
+    return _dev_ptrs(dev, (codes, torch.uint8, "codes", (N, K)),
+                     (scales, torch.uint8, "scales", (-(-N // 128), fp8_scale_pitch(K))),
+                     (s, torch.float32, "s", (N,)), (U, torch.bfloat16, "U", (N, r)),
+                     (V, torch.bfloat16, "V", (K, r))), N, r
+
+
+def _forward_fp8_args(x, projs, ys, T):
+    import torch
+
+    _need_cuda(x, "x")
+    (M, K), dev = x.shape, x.device
+    if len(ys) != len(projs):
+        raise ValueError(f"{len(projs)} projections, {len(ys)} outputs")
+    arr = (_ProjFp8 * max(len(projs), 1))()
+    for i, (p, y) in enumerate(zip(projs, ys)):
+        w, N, r = _weight_fp8(dev, *p, K)
+        yp, tp = _dev_ptrs(dev, (y, torch.bfloat16, "y", (M, N)),
+                           (None if T is None else T[i], torch.bfloat16, "T", (M, r)))
+        arr[i] = _ProjFp8(*w, yp, tp, N, r)
+    return _dev_ptrs(dev, (x, torch.bfloat16, "x", (M, K)))[0], M, K, arr
+
+
+def stacked_forward_fp8(x, projs, ys=None, checkpoint=False, stream=None):
+    """The stacked forward with 8-bit shared blocks and x quantised in 1 x 128
+    blocks (include/wl.h, wl_stacked_forward_fp8).  projs: (codes N x K,
+    scales, s, U, V) per projection, codes and scales as quantize_fp8(W0, 128)
+    returns them (U = V = None for r = 0).  Returns the list of y_p (M x N_p
+    bf16); with checkpoint=True, (ys, Fp8Checkpoint) for stacked_backward_fp8."""
+    import torch
+
+    _need_cuda(x, "x")
+    (M, K), dev = x.shape, x.device
+    with _launch_on(dev, stream) as handle:
+        if ys is None:
+            ys = [torch.empty(M, p[0].shape[0], dtype=torch.bfloat16, device=dev) for p in projs]
+        ckpt = None
+        if checkpoint:
+            ckpt = Fp8Checkpoint(torch.empty(M, K, dtype=torch.uint8, device=dev),
+                                 torch.empty(M, fp8_scale_pitch(K), dtype=torch.uint8, device=dev),
+                                 [torch.empty(M, p[3].shape[1], dtype=torch.bfloat16, device=dev)
+                                  if p[3] is not None and p[3].shape[1] else None for p in projs])
+        xp, M, K, arr = _forward_fp8_args(x, projs, ys, ckpt.T if ckpt else None)
+        n = lib().wl_stacked_forward_fp8_workspace(M, K, arr, len(projs))
+        ws = _workspace(n, dev)
+        _check(lib().wl_stacked_forward_fp8(xp, M, K, arr, len(projs), _ptr(ckpt.codes) if ckpt else None,
+                                            _ptr(ckpt.scales) if ckpt else None, _ptr(ws), n, handle),
+               "wl_stacked_forward_fp8")
+    return (ys, ckpt) if checkpoint else ys
+
+
+class PreparedForwardFp8:
+    """stacked_forward_fp8 with its tensors checked and its workspace
+    allocated once; calling it issues the forward on `stream` (default:
+    torch's current stream) and returns the list of y_p.  The tensors are kept
+    alive and their storage must not be replaced.  Calls of one handle share
+    its workspace, so they must not overlap on the GPU; handles do not share
+    anything."""
+
+    def __init__(self, x, projs, ys=None):
+        import torch
+
+        _need_cuda(x, "x")
+        with _launch_on(x.device, None):
+            if ys is None:
+                ys = [torch.empty(x.shape[0], p[0].shape[0], dtype=torch.bfloat16, device=x.device) for p in projs]
+            xp, M, K, arr = _forward_fp8_args(x, projs, ys, None)
+            n = lib().wl_stacked_forward_fp8_workspace(M, K, arr, len(projs))
+            ws = _workspace(n, x.device)
+        self.ys = ys
+        self._keep = (x, projs, ws)
+        self._device = x.device
+        self._args = (xp, M, K, arr, len(projs), None, None, _ptr(ws), n)
+        self._fn = lib().wl_stacked_forward_fp8
+
+    def __call__(self, stream=None):
+        import torch
+
+        if self._device.index != torch.cuda.current_device():
+            with torch.cuda.device(self._device):
+                return self(stream)
+        _check(self._fn(*self._args, _stream_handle(stream)), "wl_stacked_forward_fp8")
+        return self.ys
+
+
+def prepare_stacked_fp8(x, projs, ys=None) -> PreparedForwardFp8:
+    """``stacked_forward_fp8`` for a decode step that repeats it on the same
+    buffers: returns a callable that issues the forward (see
+    PreparedForwardFp8)."""
+    return PreparedForwardFp8(x, projs, ys)
+
+
+def stacked_backward_fp8(ckpt, dys, projs, need_dx=True, need_params=True, stream=None):
+    """Gradients of stacked_forward_fp8 from its checkpoint (include/wl.h,
+    wl_stacked_backward_fp8).  dys: the gradient of each y_p (M x N_p bf16);
+    projs as in the forward.  Returns (dx, per): dx M x K bf16 summed over the
+    projections (None without need_dx) and (ds N fp32, dU N x r, dV K x r
+    bf16) per projection (dU = dV = None for r = 0; (None, None, None) without
+    need_params).  The shared W0 has no gradient."""
+    import torch
+
+    _need_cuda(ckpt.codes, "checkpoint codes")
+    (M, K), dev = ckpt.codes.shape, ckpt.codes.device
+    if not len(projs) == len(dys) == len(ckpt.T):
+        raise ValueError(f"{len(projs)} projections, {len(dys)} gradients, {len(ckpt.T)} T")
+    with _launch_on(dev, stream) as handle:
+        xc, xs = _dev_ptrs(dev, (ckpt.codes, torch.uint8, "checkpoint codes", (M, K)),
+                           (ckpt.scales, torch.uint8, "checkpoint scales", (M, fp8_scale_pitch(K))))
+        arr = (_GradFp8 * max(len(projs), 1))()
+        per = []
+        for i, (p, dy, T) in enumerate(zip(projs, dys, ckpt.T)):
+            w, N, r = _weight_fp8(dev, *p, K)
+            ds = dU = dV = None
+            if need_params:
+                ds = torch.empty(N, dtype=torch.float32, device=dev)
+                if r:
+                    dU = torch.empty(N, r, dtype=torch.bfloat16, device=dev)
+                    dV = torch.empty(K, r, dtype=torch.bfloat16, device=dev)
+            per.append((ds, dU, dV))
+            io = _dev_ptrs(dev, (T if r else None, torch.bfloat16, "T", (M, r)),
+                           (dy, torch.bfloat16, "dy", (M, N)))
+            arr[i] = _GradFp8(*w, *io, _ptr(ds), _ptr(dU), _ptr(dV), N, r)
+        dx = torch.empty(M, K, dtype=torch.bfloat16, device=dev) if need_dx else None
+        n = lib().wl_stacked_backward_fp8_workspace(M, K, arr, len(projs))
+        ws = _workspace(n, dev)
+        _check(lib().wl_stacked_backward_fp8(xc, xs, M, K, arr, len(projs), _ptr(dx), _ptr(ws), n, handle),
+               "wl_stacked_backward_fp8")
+    return dx, per
 
 
 def prefetch_ranges(items):

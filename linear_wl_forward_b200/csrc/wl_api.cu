@@ -69,6 +69,20 @@ wl_status encode_map_2d_u32(CUtensorMap *m, const void *ptr, uint64_t cols, uint
     return r == CUDA_SUCCESS ? WL_OK : WL_ERR_CUDA;
 }
 
+wl_status encode_map_2d_u8(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, uint64_t ld_bytes,
+                           uint32_t box_cols, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return WL_ERR_CUDA;
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {ld_bytes};
+    const cuuint32_t box[2] = {box_cols, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? WL_OK : WL_ERR_CUDA;
+}
+
 wl_status encode_map_1d_f32(CUtensorMap *m, const void *ptr, uint64_t n, uint32_t box) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return WL_ERR_CUDA;
@@ -685,6 +699,16 @@ wl_status forward(const wl_bf16 *x, int M, int K, const wl_proj *projs, int P, w
 }
 
 }  // namespace
+
+wl_status device_info(int *num_sms, int **status) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    DevicePool *pool = nullptr;
+    wl_status st = pool_for_current_device(&pool);
+    if (st != WL_OK) return st;
+    *num_sms = pool->num_sms;
+    *status = pool->words;
+    return WL_OK;
+}
 
 unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
 

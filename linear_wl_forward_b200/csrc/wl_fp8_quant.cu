@@ -1,0 +1,208 @@
+// Quantisation to 8 bits: E4M3 codes with one power-of-two scale per block of
+// 1 x 128 (activations) or 128 x 128 (weights) elements.
+//
+// For a block with largest finite magnitude amax, the scale is 2^E with E the
+// smallest integer such that 448 * 2^E >= amax: writing amax = (1 + f) 2^e,
+// E = e - 8 when 1 + f <= 1.75 (448 = 1.75 * 2^8) and e - 7 otherwise, so E
+// comes from the bits of amax and the quotient a * 2^-E is exact.  One
+// rounding (to nearest even, by the hardware's conversion) makes the code.
+//
+// Both kernels read each element once and write one byte for it; the memory
+// traffic bounds them.
+#include "wl_common.cuh"
+#include "wl_fp8.h"
+
+namespace wl {
+
+namespace {
+
+// Exponent E of the scale of a block with largest finite magnitude amax >= 0.
+__device__ __forceinline__ int scale_exponent(float amax) {
+    if (amax == 0.f) return 0;
+    const uint32_t b = __float_as_uint(amax);
+    if ((b >> 23) == 0) return -127;  // subnormal: E <= -133, clamped
+    const int e = (int)(b >> 23) - 127;
+    const int E = e - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return E < -127 ? -127 : E;
+}
+
+// 2^-E; E in [-127, 120].
+__device__ __forceinline__ float inverse_scale(int E) { return __uint_as_float((uint32_t)(127 - E) << 23); }
+
+__device__ __forceinline__ float finite_abs(float v) {
+    const float a = fabsf(v);
+    return a <= 3.402823466e38f ? a : 0.f;  // false for infinities and NaN
+}
+
+// Two codes; an element that is not finite becomes the NaN code.
+__device__ __forceinline__ uint32_t code_pair(float lo, float hi) {
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
+    uint32_t v = c;
+    if (isinf(lo)) v = (v & 0xFF00u) | 0x7Fu;
+    if (isinf(hi)) v = (v & 0x00FFu) | 0x7F00u;
+    return v;
+}
+
+// 16 consecutive elements as floats; `n` of them exist.
+template <typename T>
+__device__ __forceinline__ void load16(const T *p, int n, bool vec, float (&v)[16]);
+
+template <>
+__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16 *p, int n, bool vec, float (&v)[16]) {
+    if (vec && n >= 16) {
+        const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[2 * i] = bf16lo(w[i]);
+            v[2 * i + 1] = bf16hi(w[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = i < n ? __bfloat162float(p[i]) : 0.f;
+    }
+}
+
+template <>
+__device__ __forceinline__ void load16<float>(const float *p, int n, bool vec, float (&v)[16]) {
+    if (vec && n >= 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 a = reinterpret_cast<const float4 *>(p)[i];
+            v[4 * i] = a.x;
+            v[4 * i + 1] = a.y;
+            v[4 * i + 2] = a.z;
+            v[4 * i + 3] = a.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = i < n ? p[i] : 0.f;
+    }
+}
+
+__device__ __forceinline__ float amax16(const float (&v)[16]) {
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a = fmaxf(a, finite_abs(v[i]));
+    return a;
+}
+
+__device__ __forceinline__ uint4 codes16(const float (&v)[16], float inv) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = code_pair(v[4 * i] * inv, v[4 * i + 1] * inv) | code_pair(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One warp: 512 columns of one row, 16 per lane, so eight lanes share a block
+// and the warp fills one word of scales.
+template <typename T, bool kColScale>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict__ a, long long lda, int rows, int cols,
+                                                            int words, const float *__restrict__ colscale,
+                                                            uint8_t *__restrict__ codes, long long ld_codes,
+                                                            uint8_t *__restrict__ scales, bool vec) {
+    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (w >= (long long)rows * words) return;
+    const int row = (int)(w / words), q = (int)(w % words);
+    const int c = q * 512 + lane * 16;
+    float v[16];
+    load16(a + (size_t)row * lda + c, cols - c, vec, v);
+    if (kColScale) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (c + i < cols) v[i] *= __ldg(colscale + c + i);
+    }
+    float m = amax16(v);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int E = scale_exponent(m);
+    if (c < ld_codes) *reinterpret_cast<uint4 *>(codes + (size_t)row * ld_codes + c) = codes16(v, inverse_scale(E));
+    uint32_t s = (uint32_t)(E + 127);
+    s = __shfl_sync(0xffffffffu, s, 0) | __shfl_sync(0xffffffffu, s, 8) << 8 | __shfl_sync(0xffffffffu, s, 16) << 16 |
+        __shfl_sync(0xffffffffu, s, 24) << 24;
+    if (lane == 0) *reinterpret_cast<uint32_t *>(scales + ((size_t)row * words + q) * 4) = s;
+}
+
+// One CTA: a 128 x 128 block, 16 elements of four rows per thread.
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_tiles_kernel(const T *__restrict__ a, int rows, int cols,
+                                                             uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
+                                                             int pitch) {
+    __shared__ float warp_max[8];
+    const int r0 = blockIdx.y * 128 + (threadIdx.x >> 3), c = blockIdx.x * 128 + (threadIdx.x & 7) * 16;
+    float v[4][16];
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 32 * i;
+        load16(a + (size_t)(r < rows ? r : 0) * cols + c, r < rows ? cols - c : 0, true, v[i]);
+        m = fmaxf(m, amax16(v[i]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, warp_max[i]);
+    const int E = scale_exponent(m);
+    const float inv = inverse_scale(E);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 32 * i;
+        if (r < rows && c < cols) *reinterpret_cast<uint4 *>(codes + (size_t)r * cols + c) = codes16(v[i], inv);
+    }
+    uint8_t *srow = scales + (size_t)blockIdx.y * pitch;
+    if (threadIdx.x == 0) srow[blockIdx.x] = (uint8_t)(E + 127);
+    if (blockIdx.x == gridDim.x - 1) {  // bytes behind the last block
+        const int b = gridDim.x + threadIdx.x;
+        if (b < pitch) srow[b] = 127;
+    }
+}
+
+template <typename T>
+cudaError_t quantize_rows(const T *a, long long lda, int rows, int cols, const float *colscale, uint8_t *codes,
+                          long long ld_codes, uint8_t *scales, cudaStream_t stream) {
+    const int words = fp8_pitch(cols) / 4;
+    const long long blocks = ((long long)rows * words + 7) / 8;
+    if (blocks == 0) return cudaSuccess;
+    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    const bool vec = (reinterpret_cast<uintptr_t>(a) & 15u) == 0 && (lda * sizeof(T)) % 16 == 0;
+    if (colscale)
+        quantize_rows_kernel<T, true><<<(unsigned)blocks, 256, 0, stream>>>(a, lda, rows, cols, words, colscale, codes,
+                                                                            ld_codes, scales, vec);
+    else
+        quantize_rows_kernel<T, false><<<(unsigned)blocks, 256, 0, stream>>>(a, lda, rows, cols, words, colscale, codes,
+                                                                             ld_codes, scales, vec);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_quantize_rows(const void *a, wl_type type, long long lda, int rows, int cols,
+                                     const float *colscale, uint8_t *codes, long long ld_codes, uint8_t *scales,
+                                     cudaStream_t stream) {
+    return type == WL_BF16 ? quantize_rows(static_cast<const __nv_bfloat16 *>(a), lda, rows, cols, colscale, codes,
+                                           ld_codes, scales, stream)
+                           : quantize_rows(static_cast<const float *>(a), lda, rows, cols, colscale, codes, ld_codes,
+                                           scales, stream);
+}
+
+cudaError_t launch_fp8_quantize_tiles(const void *a, wl_type type, int rows, int cols, uint8_t *codes, uint8_t *scales,
+                                      cudaStream_t stream) {
+    if (rows == 0 || cols == 0) return cudaSuccess;
+    // rows on the y axis: at most 65535 blocks, 8 M rows
+    dim3 grid((cols + 127) / 128, (rows + 127) / 128);
+    if (grid.y > 65535) return cudaErrorInvalidValue;
+    if (type == WL_BF16)
+        quantize_tiles_kernel<<<grid, 256, 0, stream>>>(static_cast<const __nv_bfloat16 *>(a), rows, cols, codes, scales,
+                                                        fp8_pitch(cols));
+    else
+        quantize_tiles_kernel<<<grid, 256, 0, stream>>>(static_cast<const float *>(a), rows, cols, codes, scales,
+                                                        fp8_pitch(cols));
+    return cudaGetLastError();
+}
+
+}  // namespace wl

@@ -128,6 +128,9 @@ wl_status encode_map_2d(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t
 // (a multiple of 16), no swizzle.
 wl_status encode_map_2d_u32(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, uint64_t ld_bytes,
                             uint32_t box_cols, uint32_t box_rows);
+// Bytes, 128-byte swizzling (box_cols <= 128); out-of-range reads give 0.
+wl_status encode_map_2d_u8(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, uint64_t ld_bytes,
+                           uint32_t box_cols, uint32_t box_rows);
 // n fp32 values, boxes of `box`.
 wl_status encode_map_1d_f32(CUtensorMap *m, const void *ptr, uint64_t n, uint32_t box);
 wl_status encode_map_3d(CUtensorMap *m, const void *ptr, uint64_t d0, uint64_t d1, uint64_t d2,
@@ -333,6 +336,10 @@ cudaError_t launch_materialize(const __nv_bfloat16 *W0, const float *s, const __
 // Time limit of every device-side wait the forward kernels make (2 s unless
 // wl_set_wait_limit changed it).
 unsigned long long wait_limit_ns();
+
+// The current device's SM count and status word; WL_ERR_UNSUPPORTED unless it
+// is an sm_100 device.
+wl_status device_info(int *num_sms, int **status);
 
 // --------------------------------------------------------------- probes ----
 cudaError_t launch_wait_probe(int *flag, int *status, unsigned long long limit_ns,
