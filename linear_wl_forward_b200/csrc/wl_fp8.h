@@ -38,24 +38,66 @@ cudaError_t launch_fp8_quantize_tiles(const void *a, wl_type type, int rows, int
 cudaError_t launch_fp8_lowrank(const __nv_bfloat16 *X, long long ldx, int M, int C, const __nv_bfloat16 *V,
                                int r, __nv_bfloat16 *T, cudaStream_t stream);
 
-// y = s (.) (A B^T) + T U^T; s nullptr: 1; r == 0: no second term.
-cudaError_t launch_fp8_forward(const Fp8Mat &A, const Fp8Mat &B, int M, int N, int K, const float *s,
-                               const __nv_bfloat16 *T, const __nv_bfloat16 *U, int r, __nv_bfloat16 *y,
-                               cudaStream_t stream);
-
-// acc (+)= G W + E V^T (fp32, M x K); out (bf16) written when not null.
-cudaError_t launch_fp8_dgrad(const Fp8Mat &G, const Fp8Mat &W, int M, int N, int K, const __nv_bfloat16 *E,
-                             const __nv_bfloat16 *V, int r, float *acc, bool add, __nv_bfloat16 *out,
-                             cudaStream_t stream);
-
-// ds[n] = sum_m dy[m][n] (A B^T)[m][n].
-cudaError_t launch_fp8_ds(const Fp8Mat &A, const Fp8Mat &B, int M, int N, int K, const __nv_bfloat16 *dy,
-                          float *ds, cudaStream_t stream);
-
 // out[c][j] = sum_m X[m][c] B[m][j] for X in bf16 (dU), or in 8 bits (dV).
 cudaError_t launch_fp8_tn_bf16(const __nv_bfloat16 *X, const __nv_bfloat16 *B, int M, int C, int r,
                                __nv_bfloat16 *out, cudaStream_t stream);
 cudaError_t launch_fp8_tn_codes(const Fp8Mat &X, const __nv_bfloat16 *B, int M, int C, int r, __nv_bfloat16 *out,
                                 cudaStream_t stream);
+
+// -------------------------------------------------------------------- GEMM ----
+// Tensor-core product over CTA pairs: 256 x 224 output tiles,
+//   out[m][n] = s[n] * sum over parts, k of A[m][k] B[n][k]  +  sum over parts, j of T[m][j] U[n][j]
+// with A in 8 bits (1 x 128 blocks along the contraction) and B in 8 bits
+// (128 x 128 blocks).  The forward has one output per projection, each with
+// one part; dx has one output whose parts are the projections.
+constexpr int kFp8BM = 256;      // rows per CTA pair, 128 per CTA
+constexpr int kFp8BN = 224;      // columns per CTA pair
+constexpr int kFp8GemmThreads = 384;
+constexpr int kFp8Stages = 6;
+constexpr int kFp8StageBytes = 32768;  // 16 KB of A (or T), up to 16 KB of B (or U)
+constexpr int kFp8SfSlots = 4;
+constexpr int kFp8SfBytes = 1536;      // four blocks of scales: 128 rows of A, 256 of B
+
+struct Fp8Part {
+    const uint8_t *a_scales, *b_scales;
+    int a_pitch, b_pitch;
+    int nkb;  // blocks of the contraction
+    int lr;   // 64-column blocks of T and U, 0 = none
+};
+
+struct Fp8Out {
+    const float *s;        // nullptr: 1
+    __nv_bfloat16 *y;      // rows N elements apart
+    int N;
+    int part0, nparts;
+    int tile_begin;
+    // column sums instead of y (kFp8ColSums)
+    const __nv_bfloat16 *dy;  // M x N
+    float *sums;              // [ceil(M / 32)][N]: sum over 32 rows of dy (.) (A B^T)
+};
+
+struct Fp8GemmParams {
+    CUtensorMap tm_a[kMaxSeg];  // codes, box 128 bytes x 128 rows
+    CUtensorMap tm_b[kMaxSeg];  // codes, box 128 bytes x 112 rows; transposed: x 128 rows
+    CUtensorMap tm_t[kMaxSeg];  // bf16, box 64 x 128 rows
+    CUtensorMap tm_u[kMaxSeg];  // bf16, box 64 x 112 rows
+    Fp8Part part[kMaxSeg];
+    Fp8Out out[kMaxSeg];
+    int nout;
+    int M;
+    int m_tiles, num_tiles;
+    int *status;
+    unsigned long long timeout_ns;
+};
+
+enum Fp8Mode {
+    kFp8Plain = 0,    // B rows run over the output columns (K-major)
+    kFp8Transposed,   // B rows run over the contraction (N-major): dx
+    kFp8ColSums       // K-major, the epilogue forms column sums: ds
+};
+
+cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, Fp8Mode mode, int num_sms, cudaStream_t stream);
+// ds[n] = sum over rows i < n_rows of sums[i][n].
+cudaError_t launch_fp8_sum_rows(const float *sums, int n_rows, int N, float *ds, cudaStream_t stream);
 
 }  // namespace wl

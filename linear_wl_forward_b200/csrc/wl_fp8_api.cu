@@ -94,45 +94,92 @@ wl_status forward_check(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs
     return WL_OK;
 }
 
-wl_status forward_run(const wl_bf16 *x_, int M, int K, const wl_proj_fp8 *projs, int P, uint8_t *x_codes,
-                      uint8_t *x_scales, const ForwardLayout &l, cudaStream_t stream) {
-    const __nv_bfloat16 *x = reinterpret_cast<const __nv_bfloat16 *>(x_);
-    uint8_t *codes = x_codes ? x_codes : l.codes, *scales = x_scales ? x_scales : l.scales;
-    cudaError_t e = launch_fp8_quantize_rows(x, WL_BF16, K, M, K, nullptr, codes, K, scales, stream);
-    if (e != cudaSuccess) return WL_ERR_CUDA;
-    const int pitch = fp8_pitch(K);
+// Tensor maps of one contraction part.  b_rows x b_cols: the codes of B as
+// stored; lr_rows: rows of U (output columns of the product).
+wl_status set_part(Fp8GemmParams &g, int i, const Fp8Mat &A, int M, int a_cols, const Fp8Mat &B, int b_rows, int b_cols,
+                   bool transposed, const __nv_bfloat16 *T, const __nv_bfloat16 *U, int r, int lr_rows) {
+    Fp8Part &pt = g.part[i];
+    pt.a_scales = A.scales;
+    pt.a_pitch = A.pitch;
+    pt.b_scales = B.scales;
+    pt.b_pitch = B.pitch;
+    pt.nkb = (a_cols + kFp8Block - 1) / kFp8Block;
+    pt.lr = (r + 63) / 64;
+    wl_status st = encode_map_2d_u8(&g.tm_a[i], A.codes, a_cols, M, A.ld, 128, 128);
+    if (st == WL_OK) st = encode_map_2d_u8(&g.tm_b[i], B.codes, b_cols, b_rows, B.ld, 128, transposed ? 128 : kFp8BN / 2);
+    if (st == WL_OK && r > 0) st = encode_map_2d(&g.tm_t[i], T, r, M, r, 64, 128);
+    if (st == WL_OK && r > 0) st = encode_map_2d(&g.tm_u[i], U, r, lr_rows, r, 64, kFp8BN / 2);
+    return st;
+}
+
+void init_gemm(Fp8GemmParams &g, int M, int *status) {
+    std::memset(&g, 0, sizeof g);
+    g.M = M;
+    g.m_tiles = (M + kFp8BM - 1) / kFp8BM;
+    g.status = status;
+    g.timeout_ns = wait_limit_ns();
+}
+
+Fp8Out &add_out(Fp8GemmParams &g, int N, int part0, int nparts) {
+    Fp8Out &o = g.out[g.nout++];
+    o.N = N;
+    o.part0 = part0;
+    o.nparts = nparts;
+    o.tile_begin = g.num_tiles;
+    g.num_tiles += g.m_tiles * ((N + kFp8BN - 1) / kFp8BN);
+    return o;
+}
+
+const __nv_bfloat16 *bf16(const wl_bf16 *p) { return reinterpret_cast<const __nv_bfloat16 *>(p); }
+__nv_bfloat16 *bf16(wl_bf16 *p) { return reinterpret_cast<__nv_bfloat16 *>(p); }
+
+struct Device {
+    int sms;
+    int *status;
+};
+
+wl_status forward_run(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, int P, uint8_t *x_codes,
+                      uint8_t *x_scales, const ForwardLayout &l, const Device &dev, cudaStream_t stream) {
+    const Fp8Mat X{x_codes ? x_codes : l.codes, x_scales ? x_scales : l.scales, K, fp8_pitch(K)};
+    if (launch_fp8_quantize_rows(x, WL_BF16, K, M, K, nullptr, const_cast<uint8_t *>(X.codes), K,
+                                 const_cast<uint8_t *>(X.scales), stream) != cudaSuccess)
+        return WL_ERR_CUDA;
+    Fp8GemmParams g;
+    init_gemm(g, M, dev.status);
     for (int i = 0; i < P; ++i) {
         const wl_proj_fp8 &q = projs[i];
-        __nv_bfloat16 *T = q.T ? reinterpret_cast<__nv_bfloat16 *>(q.T) : l.T[i];
-        if (q.r > 0 && (q.T || q.N > 0)) {
-            e = launch_fp8_lowrank(x, K, M, K, reinterpret_cast<const __nv_bfloat16 *>(q.V), q.r, T, stream);
-            if (e != cudaSuccess) return WL_ERR_CUDA;
-        }
+        __nv_bfloat16 *T = q.T ? bf16(q.T) : l.T[i];
+        if (q.r > 0 && (q.T || q.N > 0) &&
+            launch_fp8_lowrank(bf16(x), K, M, K, bf16(q.V), q.r, T, stream) != cudaSuccess)
+            return WL_ERR_CUDA;
         if (q.N == 0) continue;
-        e = launch_fp8_forward(Fp8Mat{codes, scales, K, pitch}, Fp8Mat{q.codes, q.scales, K, pitch}, M, q.N, K, q.s, T,
-                               reinterpret_cast<const __nv_bfloat16 *>(q.U), q.r,
-                               reinterpret_cast<__nv_bfloat16 *>(q.y), stream);
-        if (e != cudaSuccess) return WL_ERR_CUDA;
+        const int k = g.nout;
+        wl_status st = set_part(g, k, X, M, K, Fp8Mat{q.codes, q.scales, K, fp8_pitch(K)}, q.N, K, false, T, bf16(q.U), q.r, q.N);
+        if (st != WL_OK) return st;
+        Fp8Out &o = add_out(g, q.N, k, 1);
+        o.s = q.s;
+        o.y = bf16(q.y);
     }
-    return WL_OK;
+    return from_cuda(launch_fp8_gemm(g, kFp8Plain, dev.sms, stream));
 }
 
 // --------------------------------------------------------------- backward ----
 struct BackwardLayout {
     uint8_t *g_codes[kMaxSeg], *g_scales[kMaxSeg];
     __nv_bfloat16 *E[kMaxSeg];
-    float *dx;
+    float *sums[kMaxSeg];
     size_t bytes;
 };
 
 BackwardLayout backward_layout(int M, int K, const wl_grad_fp8 *projs, int P, void *ws) {
+    (void)K;
     BackwardLayout l = {};
     Arena a(ws);
-    l.dx = a.take<float>((size_t)M * K);
     for (int i = 0; i < P; ++i) {
         l.g_codes[i] = a.take<uint8_t>((size_t)M * round16(projs[i].N));
         l.g_scales[i] = a.take<uint8_t>((size_t)M * fp8_pitch(projs[i].N));
         l.E[i] = a.take<__nv_bfloat16>((size_t)M * projs[i].r);
+        l.sums[i] = a.take<float>((size_t)((M + 31) / 32) * projs[i].N);
     }
     l.bytes = a.used;
     return l;
@@ -184,40 +231,53 @@ wl_status backward_zeros(int M, int K, const wl_grad_fp8 *projs, int P, wl_bf16 
 }
 
 wl_status backward_run(const uint8_t *x_codes, const uint8_t *x_scales, int M, int K, const wl_grad_fp8 *projs, int P,
-                       wl_bf16 *dx, const BackwardLayout &l, cudaStream_t stream) {
+                       wl_bf16 *dx, const BackwardLayout &l, const Device &dev, cudaStream_t stream) {
     wl_status st = backward_zeros(M, K, projs, P, dx, stream);
     if (st != WL_OK || M == 0) return st;
     const Fp8Mat X{x_codes, x_scales, K, fp8_pitch(K)};
-    bool add = false;
-    int last = -1;
-    for (int i = 0; i < P; ++i)
-        if (projs[i].N > 0) last = i;
+    Fp8GemmParams gx, gs;
+    init_gemm(gx, M, dev.status);
+    init_gemm(gs, M, dev.status);
+    int parts = 0;
     for (int i = 0; i < P; ++i) {
         const wl_grad_fp8 &q = projs[i];
         if (q.N == 0) continue;
-        const __nv_bfloat16 *dy = reinterpret_cast<const __nv_bfloat16 *>(q.dy);
-        const __nv_bfloat16 *U = reinterpret_cast<const __nv_bfloat16 *>(q.U);
-        const __nv_bfloat16 *V = reinterpret_cast<const __nv_bfloat16 *>(q.V);
         const Fp8Mat W{q.codes, q.scales, K, fp8_pitch(K)};
+        const bool want_dv = q.dV && K > 0, want_dx = dx && K > 0;
         cudaError_t e = cudaSuccess;
-        if (q.r > 0) e = launch_fp8_lowrank(dy, q.N, M, q.N, U, q.r, l.E[i], stream);
-        if (e == cudaSuccess && q.dU && q.r > 0)
-            e = launch_fp8_tn_bf16(dy, reinterpret_cast<const __nv_bfloat16 *>(q.T), M, q.N, q.r,
-                                   reinterpret_cast<__nv_bfloat16 *>(q.dU), stream);
-        if (e == cudaSuccess && q.dV && q.r > 0 && K > 0)
-            e = launch_fp8_tn_codes(X, l.E[i], M, K, q.r, reinterpret_cast<__nv_bfloat16 *>(q.dV), stream);
-        if (e == cudaSuccess && q.ds && K > 0) e = launch_fp8_ds(X, W, M, q.N, K, dy, q.ds, stream);
-        if (e == cudaSuccess && dx && K > 0) {
-            const long long ldg = round16(q.N);
-            e = launch_fp8_quantize_rows(dy, WL_BF16, q.N, M, q.N, q.s, l.g_codes[i], ldg, l.g_scales[i], stream);
-            if (e == cudaSuccess)
-                e = launch_fp8_dgrad(Fp8Mat{l.g_codes[i], l.g_scales[i], ldg, fp8_pitch(q.N)}, W, M, q.N, K, l.E[i], V,
-                                     q.r, l.dx, add, i == last ? reinterpret_cast<__nv_bfloat16 *>(dx) : nullptr,
-                                     stream);
-            add = true;
-        }
+        if (q.r > 0 && (want_dv || want_dx)) e = launch_fp8_lowrank(bf16(q.dy), q.N, M, q.N, bf16(q.U), q.r, l.E[i], stream);
+        if (e == cudaSuccess && q.r > 0 && q.dU)
+            e = launch_fp8_tn_bf16(bf16(q.dy), bf16(q.T), M, q.N, q.r, bf16(q.dU), stream);
+        if (e == cudaSuccess && q.r > 0 && want_dv) e = launch_fp8_tn_codes(X, l.E[i], M, K, q.r, bf16(q.dV), stream);
         if (e != cudaSuccess) return WL_ERR_CUDA;
+        if (q.ds && K > 0) {
+            const int k = gs.nout;
+            if ((st = set_part(gs, k, X, M, K, W, q.N, K, false, nullptr, nullptr, 0, 0)) != WL_OK) return st;
+            Fp8Out &o = add_out(gs, q.N, k, 1);
+            o.dy = bf16(q.dy);
+            o.sums = l.sums[i];
+        }
+        if (want_dx) {
+            const long long ldg = round16(q.N);
+            if (launch_fp8_quantize_rows(q.dy, WL_BF16, q.N, M, q.N, q.s, l.g_codes[i], ldg, l.g_scales[i], stream) !=
+                cudaSuccess)
+                return WL_ERR_CUDA;
+            if ((st = set_part(gx, parts, Fp8Mat{l.g_codes[i], l.g_scales[i], ldg, fp8_pitch(q.N)}, M, q.N, W, q.N, K, true,
+                               l.E[i], bf16(q.V), q.r, K)) != WL_OK)
+                return st;
+            ++parts;
+        }
     }
+    if (parts > 0) {
+        Fp8Out &o = add_out(gx, K, 0, parts);
+        o.y = bf16(dx);
+        if (launch_fp8_gemm(gx, kFp8Transposed, dev.sms, stream) != cudaSuccess) return WL_ERR_CUDA;
+    }
+    if (launch_fp8_gemm(gs, kFp8ColSums, dev.sms, stream) != cudaSuccess) return WL_ERR_CUDA;
+    for (int i = 0; i < P; ++i)
+        if (projs[i].ds && K > 0 && projs[i].N > 0 &&
+            launch_fp8_sum_rows(l.sums[i], (M + 31) / 32, projs[i].N, projs[i].ds, stream) != cudaSuccess)
+            return WL_ERR_CUDA;
     return WL_OK;
 }
 
@@ -266,11 +326,15 @@ wl_status wl_matmul_fp8(const uint8_t *a_codes, const uint8_t *a_scales, const u
     if (K == 0) return from_cuda(cudaMemsetAsync(y, 0, (size_t)M * N * 2, stream));
     wl_status st = check_workspace(workspace, workspace_bytes, wl_matmul_fp8_workspace(M, N, K));
     if (st != WL_OK) return st;
-    int sms, *status;
-    if ((st = device_info(&sms, &status)) != WL_OK) return st;
-    return from_cuda(launch_fp8_forward(Fp8Mat{a_codes, a_scales, K, fp8_pitch(K)},
-                                        Fp8Mat{b_codes, b_scales, K, fp8_pitch(K)}, M, N, K, nullptr, nullptr, nullptr,
-                                        0, reinterpret_cast<__nv_bfloat16 *>(y), stream));
+    Device dev;
+    if ((st = device_info(&dev.sms, &dev.status)) != WL_OK) return st;
+    Fp8GemmParams g;
+    init_gemm(g, M, dev.status);
+    if ((st = set_part(g, 0, Fp8Mat{a_codes, a_scales, K, fp8_pitch(K)}, M, K, Fp8Mat{b_codes, b_scales, K, fp8_pitch(K)},
+                       N, K, false, nullptr, nullptr, 0, 0)) != WL_OK)
+        return st;
+    add_out(g, N, 0, 1).y = bf16(y);
+    return from_cuda(launch_fp8_gemm(g, kFp8Plain, dev.sms, stream));
 }
 
 size_t wl_stacked_forward_fp8_workspace(int M, int K, const wl_proj_fp8 *projs, int P) {
@@ -296,9 +360,9 @@ wl_status wl_stacked_forward_fp8(const wl_bf16 *x, int M, int K, const wl_proj_f
     }
     const ForwardLayout l = forward_layout(M, K, projs, P, workspace);
     if ((st = check_workspace(workspace, workspace_bytes, l.bytes)) != WL_OK) return st;
-    int sms, *status;
-    if ((st = device_info(&sms, &status)) != WL_OK) return st;
-    return forward_run(x, M, K, projs, P, x_codes, x_scales, l, stream);
+    Device dev;
+    if ((st = device_info(&dev.sms, &dev.status)) != WL_OK) return st;
+    return forward_run(x, M, K, projs, P, x_codes, x_scales, l, dev, stream);
 }
 
 size_t wl_stacked_backward_fp8_workspace(int M, int K, const wl_grad_fp8 *projs, int P) {
@@ -315,9 +379,9 @@ wl_status wl_stacked_backward_fp8(const uint8_t *x_codes, const uint8_t *x_scale
     if (st != WL_OK) return st;
     const BackwardLayout l = backward_layout(M, K, projs, P, workspace);
     if (M > 0 && (st = check_workspace(workspace, workspace_bytes, l.bytes)) != WL_OK) return st;
-    int sms, *status;
-    if ((st = device_info(&sms, &status)) != WL_OK) return st;
-    return backward_run(x_codes, x_scales, M, K, projs, P, dx, l, static_cast<cudaStream_t>(stream_ptr));
+    Device dev;
+    if ((st = device_info(&dev.sms, &dev.status)) != WL_OK) return st;
+    return backward_run(x_codes, x_scales, M, K, projs, P, dx, l, dev, static_cast<cudaStream_t>(stream_ptr));
 }
 
 }  // extern "C"

@@ -1,0 +1,653 @@
+// Block-scaled 8-bit GEMM on CTA pairs (tcgen05, cta_group::2):
+//
+//   out[m][n] = s[n] * sum_k 2^(ea + eb) a[m][k] b[n][k]  +  sum_j T[m][j] U[n][j]
+//
+// with E4M3 codes a, b and one E8M0 scale per 128 columns of the contraction
+// (per row of A, per 128 rows of B).  The scales are powers of two, so the
+// block-scaled MMA (kind::mxf8f6f4, which takes one scale per row and 32
+// columns) applies them at full rate and the sum over all of the contraction
+// stays in TMEM; each 128-column block issues four MMAs that select the same
+// scale byte.  The rank-r term is bf16 (kind::f16) into an accumulator of its
+// own, since s scales the first sum alone.
+//
+// A CTA pair owns a 256 x 224 tile: each CTA stages 128 rows of A and 112 of
+// B per block (30 KB against 448 tensor-core cycles; a 128 x 256 tile of one
+// CTA would stage 48 KB against 512, more than L2 delivers).  224 columns,
+// because two accumulators of that width and the scales fit the 512 columns
+// of TMEM.  The accumulators swap roles from tile to tile: tile i sums into
+// region i & 1 and its rank-r term goes to the other region, just before the
+// tile's last blocks, when the epilogue has drained tile i - 1 from there;
+// the epilogue moves the rank-r term into registers while those last blocks
+// run, which frees that region for tile i + 1.  So the tensor pipe waits for
+// no epilogue on long contractions.
+//
+// Per CTA (384 threads):
+//   warp 0      TMA producer, six stages of 32 KB; both CTAs' copies complete
+//               on the leader's barrier
+//   warp 1      TMEM allocation; in the leader CTA, one lane issues every MMA
+//   warps 2, 3  scales of A and B: four blocks at a time into the MMA's layout
+//               (32 lanes x 16 bytes per 128 rows), copied to TMEM by the
+//               MMA warp (tcgen05.cp, replicated to the four lane quarters)
+//   warps 4-11  epilogue: four lane quarters x two column halves
+#include <atomic>
+
+#include "wl_common.cuh"
+#include "wl_fp8.h"
+
+namespace wl {
+
+namespace {
+
+constexpr uint32_t kRegionCols = kFp8BN;      // region r at columns r * 224
+constexpr uint32_t kSfCol = 2 * kFp8BN;       // two slots of 12 columns: A (4), B (8)
+constexpr uint32_t kSfCols = 12;
+constexpr uint32_t kABytes = 16384;
+constexpr int kHalf = kFp8BN / 2;             // columns per CTA's half of B, and per epilogue warp
+constexpr int kChunks = kHalf / 16;
+constexpr int kLrLead = 3;                    // main blocks issued after the rank-r blocks
+
+// ------------------------------------------------------ CTA-pair primitives ----
+__device__ __forceinline__ uint32_t cluster_ctarank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// shared::cluster address of `p` in the pair's CTA `rank`
+__device__ __forceinline__ uint32_t map_rank(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_mxf8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                              uint32_t sfb, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+}
+// 32 rows x 16 bytes of shared memory into four TMEM columns of every lane quarter.
+__device__ __forceinline__ void cp_scales_pair(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs once the tcgen05
+// operations issued so far have ended.
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+
+// Instruction descriptor of kind::mxf8f6f4: E4M3 A and B (formats 0), E8M0
+// scales (bit 23), N >> 3 (17-22), M >> 7 (27-28), the byte of the scale word
+// for B (4-5) and A (29-30); bit 16: B is N-major.
+__device__ __forceinline__ uint32_t idesc_mxf8(int M, int N, bool b_n_major, uint32_t sf) {
+    return (sf << 4) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(M >> 7) << 27) | (sf << 29);
+}
+// Scales in shared memory: unswizzled, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
+
+// ---------------------------------------------------------------- schedule ----
+struct Tile {
+    int out, m0, n0;
+};
+__device__ __forceinline__ Tile tile_of(const Fp8GemmParams &p, int t) {
+    int o = 0;
+    while (o + 1 < p.nout && t >= p.out[o + 1].tile_begin) ++o;
+    const int local = t - p.out[o].tile_begin;
+    return {o, (local % p.m_tiles) * kFp8BM, (local / p.m_tiles) * kFp8BN};
+}
+
+// The blocks of a tile in issue order: main blocks part by part, the rank-r
+// blocks of every part before the last kLrLead of them.
+struct Blocks {
+    const Fp8GemmParams &p;
+    int part, kb, lr_part, lr_kb, i, pos, lr, total;
+    __device__ Blocks(const Fp8GemmParams &p_, const Fp8Out &o) : p(p_), part(o.part0), kb(-1), lr_part(o.part0), lr_kb(-1), i(-1) {
+        int main = 0;
+        lr = 0;
+        for (int q = 0; q < o.nparts; ++q) {
+            main += p.part[o.part0 + q].nkb;
+            lr += p.part[o.part0 + q].lr;
+        }
+        pos = main > kLrLead ? main - kLrLead : 0;
+        total = main + lr;
+    }
+    __device__ bool next() {
+        if (++i >= total) return false;
+        if (low_rank()) {
+            ++lr_kb;
+            while (lr_kb >= p.part[lr_part].lr) {
+                ++lr_part;
+                lr_kb = 0;
+            }
+        } else {
+            ++kb;
+            while (kb >= p.part[part].nkb) {
+                ++part;
+                kb = 0;
+            }
+        }
+        return true;
+    }
+    __device__ bool low_rank() const { return i >= pos && i < pos + lr; }
+    __device__ bool first_low_rank() const { return i == pos; }
+    __device__ bool last_low_rank() const { return i == pos + lr - 1; }
+    __device__ bool first_main() const { return pos > 0 ? i == 0 : i == lr; }
+    __device__ bool new_scales() const { return (kb & 3) == 0; }
+};
+
+// Waits whose outcome the warp agrees on; `cluster`: for barriers the other
+// CTA arrives on.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Fp8GemmParams &p, volatile int *abort_flag,
+                                          bool cluster = false) {
+    bool ok = true;
+    if (!(cluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!(cluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) {
+            if (*abort_flag) {
+                ok = false;
+                break;
+            }
+            if (globaltimer_ns() - t0 > p.timeout_ns) {
+                record_status(p.status, kStatusTimeout);
+                ok = false;
+                break;
+            }
+        }
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok && (threadIdx.x & 31) == 0) *abort_flag = 1;
+    return ok;
+}
+
+struct Ring {
+    uint32_t slot = 0, phase = 0, n;
+    __device__ explicit Ring(uint32_t n_) : n(n_) {}
+    __device__ void advance() {
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// The scale words of one chunk of B for output columns n0 .. n0 + 255.
+template <bool kT>
+__device__ __forceinline__ void b_scale_words(const Fp8Part &pt, int N, int n0, int q, int lane, uint32_t (&w)[8]) {
+    if (!kT) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int n = n0 + i * 32 + lane;
+            w[i] = n < N ? __ldg(reinterpret_cast<const uint32_t *>(pt.b_scales + (size_t)(n >> 7) * pt.b_pitch + 4 * q))
+                         : 0x7F7F7F7Fu;
+        }
+    } else {
+        // byte i of a word: contraction block 4q + i; 256 columns touch at most three blocks of columns
+        const int c0 = n0 >> 7, blk = lane >> 2, i = lane & 3;
+        uint32_t b = 0x7Fu;
+        if (blk < 3 && (c0 + blk) * 128 < N && 4 * q + i < pt.nkb)
+            b = __ldg(pt.b_scales + (size_t)(4 * q + i) * pt.b_pitch + c0 + blk);
+        b <<= 8 * i;
+        b |= __shfl_xor_sync(0xffffffffu, b, 1);
+        b |= __shfl_xor_sync(0xffffffffu, b, 2);
+        const uint32_t w0 = __shfl_sync(0xffffffffu, b, 0), w1 = __shfl_sync(0xffffffffu, b, 4),
+                       w2 = __shfl_sync(0xffffffffu, b, 8);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int c = ((n0 + k * 32 + lane) >> 7) - c0;
+            w[k] = c == 0 ? w0 : c == 1 ? w1 : w2;
+        }
+    }
+}
+
+}  // namespace
+
+template <int kMode>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
+    fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams p) {
+    constexpr bool kT = kMode == kFp8Transposed;
+    constexpr uint32_t kBBytes = kT ? 16384 : kHalf * 128;
+    pdl_launch_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t *sf = base + kFp8Stages * kFp8StageBytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sf + kFp8SfSlots * kFp8SfBytes);
+    uint64_t *empty = full + kFp8Stages;
+    uint64_t *sf_full = empty + kFp8Stages;
+    uint64_t *sf_empty = sf_full + kFp8SfSlots;
+    uint64_t *m_full = sf_empty + kFp8SfSlots;  // [2] main sum of a region complete
+    uint64_t *m_empty = m_full + 2;             // [2] ... and drained
+    uint64_t *l_full = m_empty + 2;             // rank-r term complete
+    uint64_t *l_empty = l_full + 1;             // ... and drained
+    uint64_t *drain = l_empty + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kFp8Stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < kFp8SfSlots; ++i) {
+            mbar_init(&sf_full[i], 4);  // two warps of each CTA
+            mbar_init(&sf_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&m_full[i], 1);
+            mbar_init(&m_empty[i], 16);  // eight warps of each CTA
+        }
+        mbar_init(l_full, 1);
+        mbar_init(l_empty, 16);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before either signals the other
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait_primary();
+
+    if (warp == 0) {
+        // ------------------------------------------------------ producer ----
+        Ring r(kFp8Stages);
+        uint32_t issued = 0;
+        bool ok = true;
+        for (int t = cluster; t < p.num_tiles && ok; t += nclusters) {
+            const Tile ti = tile_of(p, t);
+            Blocks b(p, p.out[ti.out]);
+            const int m = ti.m0 + (int)rank * 128, n = ti.n0 + (int)rank * kHalf;
+            while (b.next()) {
+                if (!warp_wait(&empty[r.slot], r.phase ^ 1u, p, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    const uint32_t sa = smem_addr(base + r.slot * kFp8StageBytes), sb = sa + kABytes;
+                    const uint32_t bar = map_rank(&full[r.slot], 0);
+                    if (b.low_rank()) {
+                        if (rank == 0) mbar_arrive_expect_tx(&full[r.slot], 2 * (kABytes + kHalf * 128));
+                        tma_load_2d_pair(sa, &p.tm_t[b.lr_part], b.lr_kb * 64, m, bar);
+                        tma_load_2d_pair(sb, &p.tm_u[b.lr_part], b.lr_kb * 64, n, bar);
+                    } else {
+                        if (rank == 0) mbar_arrive_expect_tx(&full[r.slot], 2 * (kABytes + kBBytes));
+                        tma_load_2d_pair(sa, &p.tm_a[b.part], b.kb * 128, m, bar);
+                        if (kT)
+                            tma_load_2d_pair(sb, &p.tm_b[b.part], n, b.kb * 128, bar);
+                        else
+                            tma_load_2d_pair(sb, &p.tm_b[b.part], b.kb * 128, n, bar);
+                    }
+                }
+                __syncwarp();
+                r.advance();
+                ++issued;
+            }
+        }
+        if (!ok && rank == 0) {
+            // Let the copies already issued land before the pair exits; their
+            // bytes are counted here, in the leader.
+            const uint32_t left = issued < kFp8Stages ? issued : kFp8Stages;
+            for (uint32_t i = issued - left; i < issued; ++i)
+                mbar_wait(&full[i % kFp8Stages], (i / kFp8Stages) & 1u, p.status, 1000000ull);
+        }
+    } else if (warp == 1) {
+        // ----------------------------------------------------- MMA issuer ---
+        if (rank == 0) {
+            const uint32_t idesc_lr = idesc_bf16_f32(kFp8BM, kFp8BN);
+            Ring r(kFp8Stages), sr(kFp8SfSlots);
+            uint32_t it = 0, lr_count = 0, m_uses[2] = {0, 0}, chunk = 0;
+            bool ok = true;
+            for (int t = cluster; t < p.num_tiles && ok; t += nclusters, ++it) {
+                const Tile ti = tile_of(p, t);
+                Blocks b(p, p.out[ti.out]);
+                const uint32_t reg = it & 1u, other = reg ^ 1u;
+                const uint32_t d_main = tmem + reg * kRegionCols, d_lr = tmem + other * kRegionCols;
+                // the region's last main sum and the last rank-r term have been read
+                if (m_uses[reg] > 0) ok = warp_wait(&m_empty[reg], (m_uses[reg] - 1) & 1u, p, abort_flag, true);
+                if (ok && lr_count > 0) ok = warp_wait(l_empty, (lr_count - 1) & 1u, p, abort_flag, true);
+                tc_fence_after();
+                while (ok && b.next()) {
+                    const bool low = b.low_rank();
+                    if (low && b.first_low_rank() && m_uses[other] > 0) {
+                        ok = warp_wait(&m_empty[other], (m_uses[other] - 1) & 1u, p, abort_flag, true);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    if (!low && b.new_scales()) {
+                        ok = warp_wait(&sf_full[sr.slot], sr.phase, p, abort_flag, true);
+                        if (!ok) break;
+                        tc_fence_after();
+                        ++chunk;
+                        if (lane == 0) {
+                            const uint32_t s = smem_addr(sf + sr.slot * kFp8SfBytes);
+                            const uint32_t c = tmem + kSfCol + (chunk & 1u) * kSfCols;
+                            cp_scales_pair(c, scale_desc(s));
+                            cp_scales_pair(c + 4, scale_desc(s + 512));
+                            cp_scales_pair(c + 8, scale_desc(s + 1024));
+                            commit_pair(&sf_empty[sr.slot]);
+                        }
+                        __syncwarp();
+                        sr.advance();
+                    }
+                    ok = warp_wait(&full[r.slot], r.phase, p, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t sa = smem_addr(base + r.slot * kFp8StageBytes);
+                        const uint64_t da = sw128_kmajor_desc(sa), db = sw128_kmajor_desc(sa + kABytes);
+                        if (low) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f16_pair(d_lr, da + 2 * k, db + 2 * k, idesc_lr, !(b.first_low_rank() && k == 0));
+                        } else {
+                            const uint32_t c = tmem + kSfCol + (chunk & 1u) * kSfCols;
+                            const uint32_t idesc = idesc_mxf8(kFp8BM, kFp8BN, kT, (uint32_t)b.kb & 3u);
+                            // 32 columns of the contraction further: 32 bytes inside the
+                            // swizzled rows, or (N-major) 32 rows of 128 bytes
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_mxf8_pair(d_main, da + 2 * k, db + (kT ? 256 : 2) * k, idesc, c, c + 4,
+                                              !(b.first_main() && k == 0));
+                        }
+                        commit_pair(&empty[r.slot]);
+                        if (low && b.last_low_rank()) commit_pair(l_full);
+                    }
+                    __syncwarp();
+                    r.advance();
+                }
+                if (!ok) break;
+                if (lane == 0) commit_pair(&m_full[reg]);
+                __syncwarp();
+                ++m_uses[reg];
+                if (b.lr > 0) ++lr_count;
+            }
+            if (lane == 0) commit_pair(drain);
+            __syncwarp();
+        }
+    } else if (warp < 4) {
+        // ------------------------------------------------------- scales -----
+        Ring r(kFp8SfSlots);
+        bool ok = true;
+        for (int t = cluster; t < p.num_tiles && ok; t += nclusters) {
+            const Tile ti = tile_of(p, t);
+            const Fp8Out &o = p.out[ti.out];
+            for (int q = 0; q < o.nparts && ok; ++q) {
+                const Fp8Part &pt = p.part[o.part0 + q];
+                for (int c = 0; 4 * c < pt.nkb; ++c) {
+                    uint32_t w[8];
+                    if (warp == 2) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int m = ti.m0 + (int)rank * 128 + i * 32 + lane;
+                            w[i] = m < p.M ? __ldg(reinterpret_cast<const uint32_t *>(pt.a_scales + (size_t)m * pt.a_pitch + 4 * c))
+                                           : 0x7F7F7F7Fu;
+                        }
+                    } else {
+                        b_scale_words<kT>(pt, o.N, ti.n0, c, lane, w);
+                    }
+                    if (!warp_wait(&sf_empty[r.slot], r.phase ^ 1u, p, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *dst = sf + r.slot * kFp8SfBytes + lane * 16;
+                    if (warp == 2) {
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                    } else {
+                        *reinterpret_cast<uint4 *>(dst + 512) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(dst + 1024) = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(map_rank(&sf_full[r.slot], 0));
+                    r.advance();
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------- epilogue ---
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
+        const uint32_t m_empty_l[2] = {map_rank(&m_empty[0], 0), map_rank(&m_empty[1], 0)};
+        const uint32_t l_empty_l = map_rank(l_empty, 0);
+        uint32_t it = 0, lr_count = 0, m_uses[2] = {0, 0};
+        for (int t = cluster; t < p.num_tiles; t += nclusters, ++it) {
+            const Tile ti = tile_of(p, t);
+            const Fp8Out &o = p.out[ti.out];
+            const uint32_t reg = it & 1u;
+            int lr = 0;
+            for (int q = 0; q < o.nparts; ++q) lr += p.part[o.part0 + q].lr;
+            const int m = ti.m0 + (int)rank * 128 + quarter * 32 + lane;
+            const int n0 = ti.n0 + half * kHalf;
+            uint32_t d[kChunks][16];
+            if (kMode != kFp8ColSums && lr > 0) {
+                if (!warp_wait(l_full, lr_count & 1u, p, abort_flag)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) tmem_ld16(lane_addr + (reg ^ 1u) * kRegionCols + c * 16, d[c]);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(l_empty_l);
+                ++lr_count;
+            } else {
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) d[c][i] = 0;
+            }
+            if (!warp_wait(&m_full[reg], m_uses[reg] & 1u, p, abort_flag)) break;
+            ++m_uses[reg];
+            tc_fence_after();
+            if (kMode == kFp8ColSums) {
+                const bool vec = (o.N & 7) == 0 && (reinterpret_cast<uintptr_t>(o.dy) & 15u) == 0;
+                const __nv_bfloat16 *dyr = o.dy + (size_t)m * o.N;
+#pragma unroll 1
+                for (int c = 0; c < kChunks; ++c) {
+                    const int n = n0 + c * 16;
+                    uint32_t v[16];
+                    tmem_ld16(lane_addr + reg * kRegionCols + c * 16, v);
+                    float g[16];
+                    if (m < p.M && vec && n + 16 <= o.N) {
+                        const uint4 a = *reinterpret_cast<const uint4 *>(dyr + n), b = *reinterpret_cast<const uint4 *>(dyr + n + 8);
+                        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            g[2 * i] = bf16lo(w[i]);
+                            g[2 * i + 1] = bf16hi(w[i]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) g[i] = m < p.M && n + i < o.N ? __bfloat162float(dyr[n + i]) : 0.f;
+                    }
+                    tmem_ld_wait();
+                    // rows that do not exist add nothing, whatever their accumulator holds
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) g[i] = m < p.M ? g[i] * __uint_as_float(v[i]) : 0.f;
+                    // transpose-and-add over the 32 rows: lane l ends with column l & 15
+#pragma unroll
+                    for (int w = 8; w > 0; w >>= 1) {
+                        const bool up = lane & w;
+#pragma unroll
+                        for (int i = 0; i < w; ++i) {
+                            const float send = up ? g[i] : g[i + w], keep = up ? g[i + w] : g[i];
+                            g[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+                        }
+                    }
+                    g[0] += __shfl_xor_sync(0xffffffffu, g[0], 16);
+                    const int row = (ti.m0 >> 5) + (int)rank * 4 + quarter;
+                    if (lane < 16 && n + lane < o.N && row * 32 < p.M) o.sums[(size_t)row * o.N + n + lane] = g[0];
+                }
+            } else {
+                const bool vec = (o.N & 7) == 0 && (reinterpret_cast<uintptr_t>(o.y) & 15u) == 0;
+                const bool svec = (reinterpret_cast<uintptr_t>(o.s) & 15u) == 0;
+                __nv_bfloat16 *yr = o.y + (size_t)m * o.N;
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const int n = n0 + c * 16;
+                    uint32_t v[16];
+                    tmem_ld16(lane_addr + reg * kRegionCols + c * 16, v);
+                    float sc[16];
+                    if (o.s && svec && n + 16 <= o.N) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 f = __ldg(reinterpret_cast<const float4 *>(o.s + n) + i);
+                            sc[4 * i] = f.x;
+                            sc[4 * i + 1] = f.y;
+                            sc[4 * i + 2] = f.z;
+                            sc[4 * i + 3] = f.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) sc[i] = o.s && n + i < o.N ? __ldg(o.s + n + i) : 1.f;
+                    }
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sc[i] = fmaf(sc[i], __uint_as_float(v[i]), __uint_as_float(d[c][i]));
+                    if (m < p.M) {
+                        if (vec && n + 16 <= o.N) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                *reinterpret_cast<uint4 *>(yr + n + 8 * i) =
+                                    make_uint4(pack_bf16x2(sc[8 * i], sc[8 * i + 1]), pack_bf16x2(sc[8 * i + 2], sc[8 * i + 3]),
+                                               pack_bf16x2(sc[8 * i + 4], sc[8 * i + 5]), pack_bf16x2(sc[8 * i + 6], sc[8 * i + 7]));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (n + i < o.N) yr[n + i] = __float2bfloat16_rn(sc[i]);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(m_empty_l[reg]);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    // Every MMA issued has ended and every signal of theirs has arrived here.
+    if (warp == 1) mbar_wait(drain, 0, p.status, p.timeout_ns);
+    cluster_sync();  // neither CTA leaves while the other may signal it or its MMAs read here
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+namespace {
+constexpr size_t kGemmSmem = 1024 + kFp8Stages * kFp8StageBytes + kFp8SfSlots * kFp8SfBytes +
+                             (2 * kFp8Stages + 2 * kFp8SfSlots + 7) * 8 + 16;
+static_assert(kGemmSmem <= 227 * 1024, "shared memory of one CTA");
+}  // namespace
+
+cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, Fp8Mode mode, int num_sms, cudaStream_t stream) {
+    if (p.num_tiles == 0) return cudaSuccess;
+    void (*const kernels[3])(Fp8GemmParams) = {fp8_gemm_kernel<kFp8Plain>, fp8_gemm_kernel<kFp8Transposed>,
+                                               fp8_gemm_kernel<kFp8ColSums>};
+    // Opt in to the large shared-memory carve-out once per device and kernel.
+    static std::atomic<bool> done[64][3] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!done[dev][mode].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kernels[mode], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
+        if (e != cudaSuccess) return e;
+        done[dev][mode].store(true, std::memory_order_release);
+    }
+    const int pairs = num_sms / 2 < p.num_tiles ? num_sms / 2 : p.num_tiles;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(kFp8GemmThreads);
+    cfg.dynamicSmemBytes = kGemmSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernels[mode], p);
+}
+
+namespace {
+__global__ void __launch_bounds__(256) sum_rows_kernel(const float *__restrict__ sums, int n_rows, int N,
+                                                       float *__restrict__ ds) {
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const int n = blockIdx.x * 256 + threadIdx.x;
+    if (n >= N) return;
+    float a = 0.f;
+    for (int i = 0; i < n_rows; ++i) a += sums[(size_t)i * N + n];
+    ds[n] = a;
+}
+}  // namespace
+
+cudaError_t launch_fp8_sum_rows(const float *sums, int n_rows, int N, float *ds, cudaStream_t stream) {
+    if (N == 0) return cudaSuccess;
+    sum_rows_kernel<<<(N + 255) / 256, 256, 0, stream>>>(sums, n_rows, N, ds);
+    return cudaGetLastError();
+}
+
+}  // namespace wl

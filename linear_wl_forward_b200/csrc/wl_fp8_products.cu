@@ -22,12 +22,6 @@ struct Rows8 {  // fp8 matrix, 1 x 128 blocks
         return ldexpf(e4m3_value(m.codes[(size_t)i * m.ld + k]), (int)m.scales[(size_t)i * m.pitch + k / 128] - 127);
     }
 };
-struct Tiles8 {  // fp8 matrix, 128 x 128 blocks
-    Fp8Mat m;
-    __device__ float at(int i, int k) const {
-        return ldexpf(e4m3_value(m.codes[(size_t)i * m.ld + k]), (int)m.scales[(size_t)(i / 128) * m.pitch + k / 128] - 127);
-    }
-};
 template <typename V>
 struct Transposed {
     V v;
@@ -83,30 +77,6 @@ __global__ void __launch_bounds__(256) product_kernel(A1 a1, B1 b1, int K1, cons
         }
 }
 
-// ds[n] = sum_m dy[m][n] z[m][n], z recomputed tile by tile down the rows
-__global__ void __launch_bounds__(256) ds_kernel(Rows8 a, Tiles8 b, int M, int N, int K, const __nv_bfloat16 *dy,
-                                                 float *ds) {
-    const int n0 = blockIdx.x * kT, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float sum[4] = {};
-    for (int m0 = 0; m0 < M; m0 += kT) {
-        float z[4][4] = {};
-        tile_product(a, b, M, N, K, m0, n0, z);
-        for (int x = 0; x < 4; ++x)
-            for (int y = 0; y < 4; ++y) {
-                const int m = m0 + 16 * x + ty, n = n0 + 16 * y + tx;
-                if (m < M && n < N) sum[y] = fmaf(__bfloat162float(dy[(size_t)m * N + n]), z[x][y], sum[y]);
-            }
-    }
-    __shared__ float part[16][kT];
-    for (int y = 0; y < 4; ++y) part[ty][16 * y + tx] = sum[y];
-    __syncthreads();
-    if (threadIdx.x < kT && n0 + threadIdx.x < N) {
-        float v = 0.f;
-        for (int i = 0; i < 16; ++i) v += part[i][threadIdx.x];
-        ds[n0 + threadIdx.x] = v;
-    }
-}
-
 template <typename A1, typename B1, typename A2, typename B2>
 cudaError_t product(A1 a1, B1 b1, int K1, const float *scale, A2 a2, B2 b2, int K2, int M, int N, float *acc, bool add,
                     __nv_bfloat16 *out, cudaStream_t stream) {
@@ -123,26 +93,6 @@ cudaError_t launch_fp8_lowrank(const __nv_bfloat16 *X, long long ldx, int M, int
                                __nv_bfloat16 *T, cudaStream_t stream) {
     const Bf16 none{nullptr, 0};
     return product(Bf16{X, ldx}, Transposed<Bf16>{{V, r}}, C, nullptr, none, none, 0, M, r, nullptr, false, T, stream);
-}
-
-cudaError_t launch_fp8_forward(const Fp8Mat &A, const Fp8Mat &B, int M, int N, int K, const float *s,
-                               const __nv_bfloat16 *T, const __nv_bfloat16 *U, int r, __nv_bfloat16 *y,
-                               cudaStream_t stream) {
-    return product(Rows8{A}, Tiles8{B}, K, s, Bf16{T, r}, Bf16{U, r}, r, M, N, nullptr, false, y, stream);
-}
-
-cudaError_t launch_fp8_dgrad(const Fp8Mat &G, const Fp8Mat &W, int M, int N, int K, const __nv_bfloat16 *E,
-                             const __nv_bfloat16 *V, int r, float *acc, bool add, __nv_bfloat16 *out,
-                             cudaStream_t stream) {
-    return product(Rows8{G}, Transposed<Tiles8>{{W}}, N, nullptr, Bf16{E, r}, Bf16{V, r}, r, M, K, acc, add, out,
-                   stream);
-}
-
-cudaError_t launch_fp8_ds(const Fp8Mat &A, const Fp8Mat &B, int M, int N, int K, const __nv_bfloat16 *dy, float *ds,
-                          cudaStream_t stream) {
-    if (N == 0) return cudaSuccess;
-    ds_kernel<<<(N + kT - 1) / kT, 256, 0, stream>>>(Rows8{A}, Tiles8{B}, M, N, K, dy, ds);
-    return cudaGetLastError();
 }
 
 cudaError_t launch_fp8_tn_bf16(const __nv_bfloat16 *X, const __nv_bfloat16 *B, int M, int C, int r,
