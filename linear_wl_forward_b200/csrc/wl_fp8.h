@@ -33,16 +33,40 @@ cudaError_t launch_fp8_quantize_rows(const void *a, wl_type type, long long lda,
 cudaError_t launch_fp8_quantize_tiles(const void *a, wl_type type, int rows, int cols, uint8_t *codes,
                                       uint8_t *scales, cudaStream_t stream);
 
-// ---------------------------------------------------------------- products ----
-// T[m][j] = sum_c X[m][c] V[c][j], bf16 out (X rows ldx elements apart).
-cudaError_t launch_fp8_lowrank(const __nv_bfloat16 *X, long long ldx, int M, int C, const __nv_bfloat16 *V,
-                               int r, __nv_bfloat16 *T, cudaStream_t stream);
-
-// out[c][j] = sum_m X[m][c] B[m][j] for X in bf16 (dU), or in 8 bits (dV).
-cudaError_t launch_fp8_tn_bf16(const __nv_bfloat16 *X, const __nv_bfloat16 *B, int M, int C, int r,
-                               __nv_bfloat16 *out, cudaStream_t stream);
-cudaError_t launch_fp8_tn_codes(const Fp8Mat &X, const __nv_bfloat16 *B, int M, int C, int r, __nv_bfloat16 *out,
+// Rows of `a` copied to rows `ld` elements apart, zeros behind column `cols`.
+cudaError_t launch_fp8_pad_rows(const __nv_bfloat16 *a, int rows, int cols, __nv_bfloat16 *out, long long ld,
                                 cudaStream_t stream);
+
+// ---------------------------------------------------- products of rank r ----
+// out[i][j] = sum_k A(i, k) B[k][j] for up to kMaxSeg products in one launch.
+enum LowrankMode {
+    kLowrankRows = 0,  // A row-major in i, bf16
+    kLowrankCols,      // A row-major in k, bf16
+    kLowrankCodes      // A row-major in k, 8 bits with 1 x 128 blocks along i; B in two bf16 terms
+};
+
+struct LowrankJob {
+    CUtensorMap tm_a;   // box 64 columns x 128 rows (Rows), 64 x 64 (Cols), 32 words x 64 rows, not swizzled (Codes)
+    CUtensorMap tm_b;   // K x r, box 64 x 64
+    CUtensorMap tm_b2;  // Codes: the low term
+    const uint8_t *a_scales;
+    int a_pitch;
+    int I, K, r;
+    int kb;             // 64-row blocks of the contraction
+    __nv_bfloat16 *out;      // I x r
+    __nv_bfloat16 *out_low;  // what rounding `out` to bf16 left over, or nullptr
+    int tile_begin;
+};
+
+struct LowrankParams {
+    LowrankJob job[kMaxSeg];
+    int njobs;
+    int BN, split, stages, stage_bytes, tmem_cols;  // filled by the launcher
+    int *status;
+    unsigned long long timeout_ns;
+};
+
+cudaError_t launch_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms, cudaStream_t stream);
 
 // -------------------------------------------------------------------- GEMM ----
 // Tensor-core product over CTA pairs: 256 x 224 output tiles,

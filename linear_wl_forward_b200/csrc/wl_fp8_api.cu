@@ -138,23 +138,68 @@ struct Device {
     int *status;
 };
 
+void init_lowrank(LowrankParams &p, const Device &dev) {
+    std::memset(&p, 0, sizeof p);
+    p.status = dev.status;
+    p.timeout_ns = wait_limit_ns();
+}
+
+// Adds out = A B (+ what its rounding left in out_low).  A: I x K (rows) or
+// K x I (cols), rows lda elements apart; B: K x r.
+wl_status add_lowrank(LowrankParams &p, LowrankMode mode, const __nv_bfloat16 *A, long long lda, int I, int K,
+                      const __nv_bfloat16 *B, int r, __nv_bfloat16 *out, __nv_bfloat16 *out_low) {
+    LowrankJob &j = p.job[p.njobs++];
+    j.I = I;
+    j.K = K;
+    j.r = r;
+    j.kb = (K + 63) / 64;
+    j.out = out;
+    j.out_low = out_low;
+    wl_status st = mode == kLowrankRows ? encode_map_2d(&j.tm_a, A, K, I, lda, 64, 128)
+                                        : encode_map_2d(&j.tm_a, A, I, K, lda, 64, 64);
+    return st == WL_OK ? encode_map_2d(&j.tm_b, B, r, K, r, 64, 64) : st;
+}
+
+// Adds out = X^T (B + B_low) for X in 8 bits (K x I).
+wl_status add_lowrank_codes(LowrankParams &p, const Fp8Mat &X, int I, int K, const __nv_bfloat16 *B,
+                            const __nv_bfloat16 *B_low, int r, __nv_bfloat16 *out) {
+    LowrankJob &j = p.job[p.njobs++];
+    j.I = I;
+    j.K = K;
+    j.r = r;
+    j.kb = (K + 63) / 64;
+    j.a_scales = X.scales;
+    j.a_pitch = X.pitch;
+    j.out = out;
+    wl_status st = encode_map_2d_u32(&j.tm_a, X.codes, I / 4, K, X.ld, 32, 64);
+    if (st == WL_OK) st = encode_map_2d(&j.tm_b, B, r, K, r, 64, 64);
+    return st == WL_OK ? encode_map_2d(&j.tm_b2, B_low, r, K, r, 64, 64) : st;
+}
+
 wl_status forward_run(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, int P, uint8_t *x_codes,
                       uint8_t *x_scales, const ForwardLayout &l, const Device &dev, cudaStream_t stream) {
     const Fp8Mat X{x_codes ? x_codes : l.codes, x_scales ? x_scales : l.scales, K, fp8_pitch(K)};
     if (launch_fp8_quantize_rows(x, WL_BF16, K, M, K, nullptr, const_cast<uint8_t *>(X.codes), K,
                                  const_cast<uint8_t *>(X.scales), stream) != cudaSuccess)
         return WL_ERR_CUDA;
+    wl_status st;
+    LowrankParams lp;
+    init_lowrank(lp, dev);
+    for (int i = 0; i < P; ++i) {
+        const wl_proj_fp8 &q = projs[i];
+        if (q.r > 0 && (q.T || q.N > 0) &&
+            (st = add_lowrank(lp, kLowrankRows, bf16(x), K, M, K, bf16(q.V), q.r, q.T ? bf16(q.T) : l.T[i], nullptr)) != WL_OK)
+            return st;
+    }
+    if (launch_fp8_lowrank(lp, kLowrankRows, dev.sms, stream) != cudaSuccess) return WL_ERR_CUDA;
     Fp8GemmParams g;
     init_gemm(g, M, dev.status);
     for (int i = 0; i < P; ++i) {
         const wl_proj_fp8 &q = projs[i];
-        __nv_bfloat16 *T = q.T ? bf16(q.T) : l.T[i];
-        if (q.r > 0 && (q.T || q.N > 0) &&
-            launch_fp8_lowrank(bf16(x), K, M, K, bf16(q.V), q.r, T, stream) != cudaSuccess)
-            return WL_ERR_CUDA;
         if (q.N == 0) continue;
+        const __nv_bfloat16 *T = q.T ? bf16(q.T) : l.T[i];
         const int k = g.nout;
-        wl_status st = set_part(g, k, X, M, K, Fp8Mat{q.codes, q.scales, K, fp8_pitch(K)}, q.N, K, false, T, bf16(q.U), q.r, q.N);
+        st = set_part(g, k, X, M, K, Fp8Mat{q.codes, q.scales, K, fp8_pitch(K)}, q.N, K, false, T, bf16(q.U), q.r, q.N);
         if (st != WL_OK) return st;
         Fp8Out &o = add_out(g, q.N, k, 1);
         o.s = q.s;
@@ -166,19 +211,22 @@ wl_status forward_run(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, 
 // --------------------------------------------------------------- backward ----
 struct BackwardLayout {
     uint8_t *g_codes[kMaxSeg], *g_scales[kMaxSeg];
-    __nv_bfloat16 *E[kMaxSeg];
+    __nv_bfloat16 *E[kMaxSeg], *E_low[kMaxSeg];
+    __nv_bfloat16 *dy[kMaxSeg];  // copies of gradients whose rows are not 16-byte aligned
     float *sums[kMaxSeg];
     size_t bytes;
 };
 
-BackwardLayout backward_layout(int M, int K, const wl_grad_fp8 *projs, int P, void *ws) {
-    (void)K;
+// Sizes alone: a copy of dy is laid out wherever one could be needed.
+BackwardLayout backward_layout(int M, const wl_grad_fp8 *projs, int P, void *ws) {
     BackwardLayout l = {};
     Arena a(ws);
     for (int i = 0; i < P; ++i) {
         l.g_codes[i] = a.take<uint8_t>((size_t)M * round16(projs[i].N));
         l.g_scales[i] = a.take<uint8_t>((size_t)M * fp8_pitch(projs[i].N));
         l.E[i] = a.take<__nv_bfloat16>((size_t)M * projs[i].r);
+        l.E_low[i] = a.take<__nv_bfloat16>((size_t)M * projs[i].r);
+        l.dy[i] = a.take<__nv_bfloat16>(projs[i].r > 0 ? (size_t)M * round16(projs[i].N) : 0);
         l.sums[i] = a.take<float>((size_t)((M + 31) / 32) * projs[i].N);
     }
     l.bytes = a.used;
@@ -238,18 +286,31 @@ wl_status backward_run(const uint8_t *x_codes, const uint8_t *x_scales, int M, i
     Fp8GemmParams gx, gs;
     init_gemm(gx, M, dev.status);
     init_gemm(gs, M, dev.status);
+    LowrankParams le, lu, lv;
+    init_lowrank(le, dev);
+    init_lowrank(lu, dev);
+    init_lowrank(lv, dev);
     int parts = 0;
     for (int i = 0; i < P; ++i) {
         const wl_grad_fp8 &q = projs[i];
         if (q.N == 0) continue;
         const Fp8Mat W{q.codes, q.scales, K, fp8_pitch(K)};
         const bool want_dv = q.dV && K > 0, want_dx = dx && K > 0;
-        cudaError_t e = cudaSuccess;
-        if (q.r > 0 && (want_dv || want_dx)) e = launch_fp8_lowrank(bf16(q.dy), q.N, M, q.N, bf16(q.U), q.r, l.E[i], stream);
-        if (e == cudaSuccess && q.r > 0 && q.dU)
-            e = launch_fp8_tn_bf16(bf16(q.dy), bf16(q.T), M, q.N, q.r, bf16(q.dU), stream);
-        if (e == cudaSuccess && q.r > 0 && want_dv) e = launch_fp8_tn_codes(X, l.E[i], M, K, q.r, bf16(q.dV), stream);
-        if (e != cudaSuccess) return WL_ERR_CUDA;
+        if (q.r > 0 && (want_dv || want_dx || q.dU)) {
+            const __nv_bfloat16 *dy = bf16(q.dy);
+            long long ld = q.N;
+            if (q.N % 8 != 0 || !aligned(q.dy, 16)) {
+                ld = round16(q.N);
+                if (launch_fp8_pad_rows(dy, M, q.N, l.dy[i], ld, stream) != cudaSuccess) return WL_ERR_CUDA;
+                dy = l.dy[i];
+            }
+            if ((want_dv || want_dx) && (st = add_lowrank(le, kLowrankRows, dy, ld, M, q.N, bf16(q.U), q.r, l.E[i],
+                                                          want_dv ? l.E_low[i] : nullptr)) != WL_OK)
+                return st;
+            if (q.dU && (st = add_lowrank(lu, kLowrankCols, dy, ld, q.N, M, bf16(q.T), q.r, bf16(q.dU), nullptr)) != WL_OK)
+                return st;
+            if (want_dv && (st = add_lowrank_codes(lv, X, K, M, l.E[i], l.E_low[i], q.r, bf16(q.dV))) != WL_OK) return st;
+        }
         if (q.ds && K > 0) {
             const int k = gs.nout;
             if ((st = set_part(gs, k, X, M, K, W, q.N, K, false, nullptr, nullptr, 0, 0)) != WL_OK) return st;
@@ -268,6 +329,10 @@ wl_status backward_run(const uint8_t *x_codes, const uint8_t *x_scales, int M, i
             ++parts;
         }
     }
+    if (launch_fp8_lowrank(le, kLowrankRows, dev.sms, stream) != cudaSuccess ||
+        launch_fp8_lowrank(lu, kLowrankCols, dev.sms, stream) != cudaSuccess ||
+        launch_fp8_lowrank(lv, kLowrankCodes, dev.sms, stream) != cudaSuccess)
+        return WL_ERR_CUDA;
     if (parts > 0) {
         Fp8Out &o = add_out(gx, K, 0, parts);
         o.y = bf16(dx);
@@ -368,7 +433,7 @@ wl_status wl_stacked_forward_fp8(const wl_bf16 *x, int M, int K, const wl_proj_f
 size_t wl_stacked_backward_fp8_workspace(int M, int K, const wl_grad_fp8 *projs, int P) {
     using namespace wl;
     if (check_sizes(M, K, projs, P) != WL_OK) return 0;
-    return backward_layout(M, K, projs, P, nullptr).bytes;
+    return backward_layout(M, projs, P, nullptr).bytes;
 }
 
 wl_status wl_stacked_backward_fp8(const uint8_t *x_codes, const uint8_t *x_scales, int M, int K,
@@ -377,7 +442,7 @@ wl_status wl_stacked_backward_fp8(const uint8_t *x_codes, const uint8_t *x_scale
     using namespace wl;
     wl_status st = backward_check(x_codes, x_scales, M, K, projs, P, dx);
     if (st != WL_OK) return st;
-    const BackwardLayout l = backward_layout(M, K, projs, P, workspace);
+    const BackwardLayout l = backward_layout(M, projs, P, workspace);
     if (M > 0 && (st = check_workspace(workspace, workspace_bytes, l.bytes)) != WL_OK) return st;
     Device dev;
     if ((st = device_info(&dev.sms, &dev.status)) != WL_OK) return st;

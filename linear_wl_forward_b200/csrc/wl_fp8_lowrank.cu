@@ -1,0 +1,378 @@
+// Products with a rank-r factor, on the tensor cores (tcgen05, bf16, fp32 sums):
+//
+//   out[i][j] = sum_k A(i, k) B[k][j],   B row-major with r <= 1024 columns
+//
+//   T = x V, E = dy U    A row-major in i (K-major operand)
+//   dU = dy^T T          A row-major in k (M-major operand): no transposed copy
+//   dV = (x^)^T E        the same, with A in 8 bits: four warps expand a tile's
+//                        codes to bf16 (code * 2^E is exact there) on its way
+//                        to the MMA; E comes as two bf16 terms (high and low
+//                        part), so that dV's error is its own rounding, at
+//                        twice the MMAs of a product that is small beside
+//                        the M x N x K ones
+//
+// B is read as it lies (N-major operand, boxes of 64 columns x 64 rows).
+// A CTA owns 128 rows x up to 256 columns of one product and a range of the
+// contraction; the CTAs of a cluster (1, 2, 4 or 8) share a tile's contraction
+// and add their sums over distributed shared memory in rank order, so there
+// are no partial results in memory and the result is reproducible.  The tile
+// width and the split are chosen by a cost estimate (plan below): a tile of N
+// columns stages (128 + N) x 128 bytes per 64 columns of the contraction
+// against 2 N tensor-core cycles, so wide tiles are fed best; short products
+// are cut instead, to put every SM to work.
+//
+//   warp 0  TMA producer;  warp 1  MMA issuer;  warps 2-5  expansion of codes,
+//   then the epilogue
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+
+#include <cuda_fp16.h>
+
+#include "wl_common.cuh"
+#include "wl_fp8.h"
+
+namespace wl {
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr uint32_t kATile = 16384;  // 128 x 64 bf16
+constexpr uint32_t kBBox = 8192;    // 64 x 64 bf16
+constexpr uint32_t kCodeTile = 8192;  // 64 rows x 128 codes
+constexpr int kMaxStages = 8;
+
+// Descriptor of an M- or N-major bf16 tile: boxes of 64 elements (128 swizzled
+// bytes) x 64 contraction rows; 8 rows are 1024 bytes, the next 64 elements one box on.
+__device__ __forceinline__ uint64_t mn_major_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(kBBox >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+__device__ __forceinline__ uint32_t ctarank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t local_addr, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local_addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+    uint32_t u[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "r"(taddr));
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+}
+
+// Two E4M3 codes (low byte first) times a power of two, as a pair of bf16.
+__device__ __forceinline__ uint32_t expand_pair(uint32_t codes, float scale) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+    const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h));
+    return pack_bf16x2(f.x * scale, f.y * scale);
+}
+
+__device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, const LowrankParams &p) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status, p.timeout_ns));
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16 *dst, const float (&v)[8]) {
+    *reinterpret_cast<uint4 *>(dst) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+__device__ __forceinline__ void write8(const LowrankJob &jb, int i, int j, const float (&v)[8]) {
+    if (i >= jb.I || j >= jb.r) return;
+    store8(jb.out + (size_t)i * jb.r + j, v);
+    if (jb.out_low) {
+        float lo[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) lo[k] = v[k] - __bfloat162float(__float2bfloat16_rn(v[k]));
+        store8(jb.out_low + (size_t)i * jb.r + j, lo);
+    }
+}
+
+}  // namespace
+
+template <int kMode>
+__global__ void __launch_bounds__(kThreads, 1) lowrank_kernel(const __grid_constant__ LowrankParams p) {
+    constexpr bool kCodes = kMode == kLowrankCodes;
+    pdl_launch_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(base + (size_t)p.stages * p.stage_bytes);
+    uint64_t *empty = full + kMaxStages;
+    uint64_t *ready = empty + kMaxStages;  // codes expanded
+    uint64_t *done = ready + kMaxStages;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = p.split;
+    const uint32_t rank = S > 1 ? ctarank() : 0;
+    const int unit = blockIdx.x / S;
+    int jx = 0;
+    while (jx + 1 < p.njobs && unit >= p.job[jx + 1].tile_begin) ++jx;
+    const LowrankJob &jb = p.job[jx];
+    const int local = unit - jb.tile_begin;
+    const int i_tiles = (jb.I + 127) / 128;
+    const int i0 = (local % i_tiles) * 128, j0 = (local / i_tiles) * p.BN;
+    const int width = min(p.BN, jb.r - j0), n_mma = (width + 15) & ~15, boxes = (width + 63) / 64;
+    const int per = (jb.kb + S - 1) / S;
+    const int kb0 = min((int)rank * per, jb.kb), kb1 = min(kb0 + per, jb.kb);
+    const int terms = kCodes ? 2 : 1;  // B high, B low
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+            mbar_init(&ready[i], 4);
+        }
+        mbar_init(done, 1);
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, p.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait_primary();
+
+    const uint32_t b_off = kATile + (kCodes ? kCodeTile : 0);
+    bool ok = true;
+    if (warp == 0) {
+        uint32_t slot = 0, ph = 0, issued = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!all_wait(&empty[slot], ph ^ 1u, p)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                uint8_t *st = base + (size_t)slot * p.stage_bytes;
+                mbar_arrive_expect_tx(&full[slot], (kCodes ? kCodeTile : kATile) + (uint32_t)(terms * boxes) * kBBox);
+                if (kMode == kLowrankRows) {
+                    tma_load_2d(st, &jb.tm_a, kb * 64, i0, &full[slot]);
+                } else if (kMode == kLowrankCols) {
+                    tma_load_2d(st, &jb.tm_a, i0, kb * 64, &full[slot]);
+                    tma_load_2d(st + kBBox, &jb.tm_a, i0 + 64, kb * 64, &full[slot]);
+                } else {
+                    tma_load_2d(st + kATile, &jb.tm_a, i0 / 4, kb * 64, &full[slot]);  // in words
+                }
+                for (int b = 0; b < boxes; ++b) {
+                    tma_load_2d(st + b_off + b * kBBox, &jb.tm_b, j0 + b * 64, kb * 64, &full[slot]);
+                    if (kCodes) tma_load_2d(st + b_off + (boxes + b) * kBBox, &jb.tm_b2, j0 + b * 64, kb * 64, &full[slot]);
+                }
+            }
+            __syncwarp();
+            ++issued;
+            if (++slot == (uint32_t)p.stages) slot = 0, ph ^= 1u;
+        }
+        if (!ok) {  // let the copies already issued land before the CTA exits
+            const uint32_t left = issued < (uint32_t)p.stages ? issued : p.stages;
+            for (uint32_t i = issued - left; i < issued; ++i)
+                mbar_wait(&full[i % p.stages], (i / p.stages) & 1u, p.status, 1000000ull);
+        }
+    } else if (warp == 1) {
+        // fp32 sums of bf16 products; A M-major (bit 15) unless its rows run along i; B N-major (bit 16)
+        const uint32_t idesc = idesc_bf16_f32(128, n_mma) | (kMode == kLowrankRows ? 0u : 1u << 15) | 1u << 16;
+        uint32_t slot = 0, ph = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!all_wait(kCodes ? &ready[slot] : &full[slot], ph, p)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t sa = smem_addr(base + (size_t)slot * p.stage_bytes);
+                const uint64_t da = kMode == kLowrankRows ? sw128_kmajor_desc(sa) : mn_major_desc(sa);
+                for (int t = 0; t < terms; ++t) {
+                    const uint64_t db = mn_major_desc(sa + b_off + (uint32_t)(t * boxes) * kBBox);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)  // 16 contraction rows on: 32 bytes, or 16 rows of 128
+                        tc_mma_f16(tmem, da + (kMode == kLowrankRows ? 2 : 128) * k, db + 128 * k, idesc,
+                                   kb > kb0 || t > 0 || k > 0);
+                }
+                tc_commit(&empty[slot]);
+            }
+            __syncwarp();
+            if (++slot == (uint32_t)p.stages) slot = 0, ph ^= 1u;
+        }
+        if (lane == 0) tc_commit(done);
+        __syncwarp();
+        // Outstanding MMAs end before TMEM is released, whatever happened.
+        if (!ok) mbar_wait(done, 0, p.status, 1000000ull);
+    } else {
+        const int tid = threadIdx.x - 64;
+        if (kCodes) {
+            uint32_t slot = 0, ph = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!all_wait(&full[slot], ph, p)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *st = base + (size_t)slot * p.stage_bytes;
+                // 16 codes of one row per step; chunk c of 16 bytes of row k sits at c ^ (k & 7)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int k = s * 16 + (tid >> 3), seg = tid & 7;
+                    const int m = kb * 64 + k;
+                    const uint32_t e = m < jb.K ? __ldg(jb.a_scales + (size_t)m * jb.a_pitch + (i0 >> 7)) : 127u;
+                    const uint4 c = *reinterpret_cast<const uint4 *>(st + kATile + k * 128 + seg * 16);
+                    // 2^(e - 127); e = 0 is the subnormal 2^-127, e = 255 the NaN scale
+                    const float sc = e == 0 ? __uint_as_float(0x00400000u) : e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(e << 23);
+                    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        o[2 * q] = expand_pair(w[q] & 0xFFFFu, sc);
+                        o[2 * q + 1] = expand_pair(w[q] >> 16, sc);
+                    }
+                    uint8_t *row = st + (seg >> 2) * kBBox + k * 128;
+                    const int ch = (seg & 3) * 2;
+                    *reinterpret_cast<uint4 *>(row + ((ch ^ (k & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(row + (((ch + 1) ^ (k & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ready[slot]);
+                if (++slot == (uint32_t)p.stages) slot = 0, ph ^= 1u;
+            }
+        }
+        // MMAs done.  A CTA with an empty range of the contraction has no sums.
+        if (ok && kb1 > kb0) ok = all_wait(done, 0, p);
+        tc_fence_after();
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16);
+        float *buf = reinterpret_cast<float *>(base);  // [column][row], over the idle stages
+        if (ok)
+            for (int c = 0; c < n_mma; c += 8) {
+                float v[8];
+                if (kb1 > kb0) {
+                    tmem_ld8(taddr + c, v);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = 0.f;
+                }
+                if (S == 1) {
+                    if (c < width) write8(jb, i0 + row, j0 + c, v);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) buf[(c + k) * 128 + row] = v[k];
+                }
+            }
+    }
+    if (S > 1) {
+        __syncwarp();
+        cluster_barrier();  // every CTA's sums are in its shared memory
+        if (warp >= 2 && ok) {
+            const int row = (warp & 3) * 32 + lane;
+            for (int c = (int)rank * 8; c < width; c += 8 * S) {
+                float v[8] = {};
+                for (int s = 0; s < S; ++s)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        v[k] += ld_cluster(smem_addr(base) + (uint32_t)((c + k) * 128 + row) * 4, s);
+                write8(jb, i0 + row, j0 + c, v);
+            }
+        }
+        __syncwarp();
+        cluster_barrier();  // no CTA leaves while its sums are read
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, p.tmem_cols);
+    }
+}
+
+// Tile width and split of the contraction.  Estimated cycles of a call: waves
+// of CTAs, each with its blocks of the contraction at the slower of the MMAs
+// (2 cycles per column, terms times) and the loads (64 bytes per cycle), plus
+// about 3000 for the start, the drain and, with a split, the exchange.
+static void plan(LowrankParams &p, int terms, int num_sms) {
+    double best = 0;
+    for (int bn = 256; bn >= 64; bn /= 2)
+        for (int s = 1; s <= 8; s *= 2) {
+            long long tiles = 0;
+            int kb = 0, widest = 0;
+            for (int i = 0; i < p.njobs; ++i) {
+                tiles += (long long)((p.job[i].I + 127) / 128) * ((p.job[i].r + bn - 1) / bn);
+                kb = std::max(kb, p.job[i].kb);
+                widest = std::max(widest, p.job[i].r);
+            }
+            if (bn > 64 && bn / 2 >= widest) continue;
+            const int cols = std::min(bn, (widest + 15) / 16 * 16);
+            const double block = std::max(2.0 * cols * terms, (16384 + 128.0 * cols * terms) / 64);
+            const double waves = (double)((tiles * s + num_sms - 1) / num_sms);
+            const double cost = waves * (((kb + s - 1) / s) * block + 3000 + (s > 1 ? 1000 + 8.0 * cols : 0));
+            if (best == 0 || cost < best) {
+                best = cost;
+                p.BN = bn;
+                p.split = s;
+            }
+        }
+}
+
+cudaError_t launch_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms, cudaStream_t stream) {
+    if (p.njobs == 0) return cudaSuccess;
+    const int terms = mode == kLowrankCodes ? 2 : 1;
+    plan(p, terms, num_sms);
+    int tiles = 0, widest = 0;
+    for (int i = 0; i < p.njobs; ++i) {
+        p.job[i].tile_begin = tiles;
+        tiles += (p.job[i].I + 127) / 128 * ((p.job[i].r + p.BN - 1) / p.BN);
+        widest = std::max(widest, p.job[i].r);
+    }
+    const int boxes = (std::min(widest, p.BN) + 63) / 64;
+    p.stage_bytes = (int)(kATile + (mode == kLowrankCodes ? kCodeTile : 0) + terms * boxes * kBBox);
+    // narrow tiles leave room for a second CTA on the SM
+    p.stages = std::max(2, std::min(kMaxStages, (p.BN > 64 ? 200 * 1024 : 100 * 1024) / p.stage_bytes));
+    p.tmem_cols = 32;
+    while (p.tmem_cols < std::min((widest + 15) / 16 * 16, p.BN)) p.tmem_cols *= 2;
+    // the exchange of a split tile reuses the stages
+    const size_t exchange = p.split > 1 ? (size_t)std::min((widest + 15) / 16 * 16, p.BN) * 512 : 0;
+    while ((size_t)p.stages * p.stage_bytes < exchange) ++p.stages;
+    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + (3 * kMaxStages + 1) * 8 + 16;
+    if (p.stages > kMaxStages || smem > 227 * 1024) return cudaErrorInvalidValue;
+    void (*const kernels[3])(LowrankParams) = {lowrank_kernel<kLowrankRows>, lowrank_kernel<kLowrankCols>,
+                                               lowrank_kernel<kLowrankCodes>};
+    static std::atomic<bool> done[64][3] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!done[dev][mode].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kernels[mode], cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e != cudaSuccess) return e;
+        done[dev][mode].store(true, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * p.split));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernels[mode], p);
+}
+
+}  // namespace wl

@@ -162,6 +162,13 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const T *__restrict
     }
 }
 
+__global__ void __launch_bounds__(256) pad_rows_kernel(const __nv_bfloat16 *__restrict__ a, int cols,
+                                                       __nv_bfloat16 *__restrict__ out, long long ld) {
+    const size_t row = blockIdx.x;
+    for (int c = threadIdx.x; c < ld; c += 256)
+        out[row * ld + c] = c < cols ? a[row * cols + c] : __float2bfloat16_rn(0.f);
+}
+
 template <typename T>
 cudaError_t quantize_rows(const T *a, long long lda, int rows, int cols, const float *colscale, uint8_t *codes,
                           long long ld_codes, uint8_t *scales, cudaStream_t stream) {
@@ -180,6 +187,13 @@ cudaError_t quantize_rows(const T *a, long long lda, int rows, int cols, const f
 }
 
 }  // namespace
+
+cudaError_t launch_fp8_pad_rows(const __nv_bfloat16 *a, int rows, int cols, __nv_bfloat16 *out, long long ld,
+                                cudaStream_t stream) {
+    if (rows == 0) return cudaSuccess;
+    pad_rows_kernel<<<rows, 256, 0, stream>>>(a, cols, out, ld);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_fp8_quantize_rows(const void *a, wl_type type, long long lda, int rows, int cols,
                                      const float *colscale, uint8_t *codes, long long ld_codes, uint8_t *scales,
