@@ -77,8 +77,9 @@ cudaError_t launch_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms, 
 constexpr int kFp8BM = 256;      // rows per CTA pair, 128 per CTA
 constexpr int kFp8BN = 224;      // columns per CTA pair
 constexpr int kFp8GemmThreads = 384;
-constexpr int kFp8Stages = 6;
-constexpr int kFp8StageBytes = 32768;  // 16 KB of A (or T), up to 16 KB of B (or U)
+constexpr int kFp8Stages = 3;
+constexpr int kFp8BlockBytes = 32768;  // 16 KB of A (or T), up to 16 KB of B (or U)
+constexpr int kFp8StageBytes = 2 * kFp8BlockBytes;
 constexpr int kFp8SfSlots = 4;
 constexpr int kFp8SfBytes = 1536;      // four blocks of scales: 128 rows of A, 256 of B
 

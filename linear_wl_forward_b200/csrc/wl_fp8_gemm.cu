@@ -22,8 +22,8 @@
 // no epilogue on long contractions.
 //
 // Per CTA (384 threads):
-//   warp 0      TMA producer, six stages of 32 KB; both CTAs' copies complete
-//               on the leader's barrier
+//   warp 0      TMA producer, three stages of two blocks (64 KB); both CTAs'
+//               copies complete on the leader's barrier
 //   warp 1      TMEM allocation; in the leader CTA, one lane issues every MMA
 //   warps 2, 3  scales of A and B: four blocks at a time into the MMA's layout
 //               (32 lanes x 16 bytes per 128 rows), copied to TMEM by the
@@ -39,12 +39,11 @@ namespace wl {
 namespace {
 
 constexpr uint32_t kRegionCols = kFp8BN;      // region r at columns r * 224
-constexpr uint32_t kSfCol = 2 * kFp8BN;       // two slots of 12 columns: A (4), B (8)
-constexpr uint32_t kSfCols = 12;
+constexpr uint32_t kSfCol = 2 * kFp8BN;       // two slots of scales, 16 columns apart: A (4 columns), B (8)
 constexpr uint32_t kABytes = 16384;
 constexpr int kHalf = kFp8BN / 2;             // columns per CTA's half of B, and per epilogue warp
 constexpr int kChunks = kHalf / 16;
-constexpr int kLrLead = 3;                    // main blocks issued after the rank-r blocks
+constexpr int kLrLead = 2;                    // main stages issued after the rank-r blocks
 
 // ------------------------------------------------------ CTA-pair primitives ----
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -152,67 +151,60 @@ __device__ __forceinline__ Tile tile_of(const Fp8GemmParams &p, int t) {
     return {o, (local % p.m_tiles) * kFp8BM, (local / p.m_tiles) * kFp8BN};
 }
 
-// The blocks of a tile in issue order: main blocks part by part, the rank-r
-// blocks of every part before the last kLrLead of them.
-struct Blocks {
-    const Fp8GemmParams &p;
-    int part, kb, lr_part, lr_kb, i, pos, lr, total;
-    __device__ Blocks(const Fp8GemmParams &p_, const Fp8Out &o) : p(p_), part(o.part0), kb(-1), lr_part(o.part0), lr_kb(-1), i(-1) {
-        int main = 0;
-        lr = 0;
-        for (int q = 0; q < o.nparts; ++q) {
-            main += p.part[o.part0 + q].nkb;
-            lr += p.part[o.part0 + q].lr;
-        }
-        pos = main > kLrLead ? main - kLrLead : 0;
-        total = main + lr;
-    }
-    __device__ bool next() {
-        if (++i >= total) return false;
-        if (low_rank()) {
-            ++lr_kb;
-            while (lr_kb >= p.part[lr_part].lr) {
-                ++lr_part;
-                lr_kb = 0;
+// A tile's work in issue order, up to two blocks (one stage) at a time:
+// main(part, block, two) part by part, and before the last kLrLead stages of
+// them low(part, block, two) for the rank-r blocks of every part.  Stops when
+// either returns false.  Run by one thread, whose instructions bound how fast
+// the tensor pipe is fed: an MMA takes it about 64 cycles, a barrier wait 130
+// and a commit 65, against 448 cycles of MMAs per block, so one block per
+// stage would leave the pipe waiting (measured: 950 cycles per block with
+// per-block waits and bookkeeping).
+template <typename Main, typename Low>
+__device__ __forceinline__ bool for_stages(const Fp8GemmParams &p, const Fp8Out &o, Main main, Low low) {
+    int left = 0;
+    for (int q = 0; q < o.nparts; ++q) left += (p.part[o.part0 + q].nkb + 1) >> 1;
+    for (int q = o.part0; q < o.part0 + o.nparts; ++q) {
+        const int nkb = p.part[q].nkb;
+        for (int kb = 0; kb < nkb; kb += 2, --left) {
+            if (left == kLrLead || (left < kLrLead && kb == 0 && q == o.part0)) {
+                for (int l = o.part0; l < o.part0 + o.nparts; ++l) {
+                    const int lr = p.part[l].lr;
+                    for (int j = 0; j < lr; j += 2)
+                        if (!low(l, j, j + 1 < lr)) return false;
+                }
             }
-        } else {
-            ++kb;
-            while (kb >= p.part[part].nkb) {
-                ++part;
-                kb = 0;
-            }
+            if (!main(q, kb, kb + 1 < nkb)) return false;
         }
-        return true;
     }
-    __device__ bool low_rank() const { return i >= pos && i < pos + lr; }
-    __device__ bool first_low_rank() const { return i == pos; }
-    __device__ bool last_low_rank() const { return i == pos + lr - 1; }
-    __device__ bool first_main() const { return pos > 0 ? i == 0 : i == lr; }
-    __device__ bool new_scales() const { return (kb & 3) == 0; }
-};
+    return true;
+}
 
-// Waits whose outcome the warp agrees on; `cluster`: for barriers the other
-// CTA arrives on.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Fp8GemmParams &p, volatile int *abort_flag,
-                                          bool cluster = false) {
-    bool ok = true;
-    if (!(cluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) {
-        const uint64_t t0 = globaltimer_ns();
-        while (!(cluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) {
-            if (*abort_flag) {
-                ok = false;
-                break;
-            }
-            if (globaltimer_ns() - t0 > p.timeout_ns) {
-                record_status(p.status, kStatusTimeout);
-                ok = false;
-                break;
-            }
+__device__ __forceinline__ int lr_blocks(const Fp8GemmParams &p, const Fp8Out &o) {
+    int lr = 0;
+    for (int q = 0; q < o.nparts; ++q) lr += p.part[o.part0 + q].lr;
+    return lr;
+}
+
+// Bounded wait of one thread; `cluster`: for barriers the other CTA arrives on.
+__device__ __forceinline__ bool thread_wait(uint64_t *bar, uint32_t parity, const Fp8GemmParams &p, volatile int *abort_flag,
+                                            bool cluster = false) {
+    if (cluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!(cluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) {
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > p.timeout_ns) {
+            record_status(p.status, kStatusTimeout);
+            *abort_flag = 1;
+            return false;
         }
     }
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok && (threadIdx.x & 31) == 0) *abort_flag = 1;
-    return ok;
+    return true;
+}
+
+// The same for a warp that goes on together.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Fp8GemmParams &p, volatile int *abort_flag) {
+    const bool ok = thread_wait(bar, parity, p, abort_flag);
+    return __all_sync(0xffffffffu, ok);
 }
 
 struct Ring {
@@ -265,8 +257,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
     pdl_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    uint8_t *sf = base + kFp8Stages * kFp8StageBytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(sf + kFp8SfSlots * kFp8SfBytes);
+    uint8_t *sf_base = base + kFp8Stages * kFp8StageBytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sf_base + kFp8SfSlots * kFp8SfBytes);
     uint64_t *empty = full + kFp8Stages;
     uint64_t *sf_full = empty + kFp8Stages;
     uint64_t *sf_empty = sf_full + kFp8SfSlots;
@@ -311,120 +303,144 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------ producer ----
-        Ring r(kFp8Stages);
-        uint32_t issued = 0;
-        bool ok = true;
-        for (int t = cluster; t < p.num_tiles && ok; t += nclusters) {
-            const Tile ti = tile_of(p, t);
-            Blocks b(p, p.out[ti.out]);
-            const int m = ti.m0 + (int)rank * 128, n = ti.n0 + (int)rank * kHalf;
-            while (b.next()) {
-                if (!warp_wait(&empty[r.slot], r.phase ^ 1u, p, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    const uint32_t sa = smem_addr(base + r.slot * kFp8StageBytes), sb = sa + kABytes;
-                    const uint32_t bar = map_rank(&full[r.slot], 0);
-                    if (b.low_rank()) {
-                        if (rank == 0) mbar_arrive_expect_tx(&full[r.slot], 2 * (kABytes + kHalf * 128));
-                        tma_load_2d_pair(sa, &p.tm_t[b.lr_part], b.lr_kb * 64, m, bar);
-                        tma_load_2d_pair(sb, &p.tm_u[b.lr_part], b.lr_kb * 64, n, bar);
-                    } else {
-                        if (rank == 0) mbar_arrive_expect_tx(&full[r.slot], 2 * (kABytes + kBBytes));
-                        tma_load_2d_pair(sa, &p.tm_a[b.part], b.kb * 128, m, bar);
-                        if (kT)
-                            tma_load_2d_pair(sb, &p.tm_b[b.part], n, b.kb * 128, bar);
-                        else
-                            tma_load_2d_pair(sb, &p.tm_b[b.part], b.kb * 128, n, bar);
-                    }
-                }
-                __syncwarp();
-                r.advance();
-                ++issued;
+        if (lane == 0) {
+            Ring r(kFp8Stages);
+            uint32_t issued = 0;
+            const uint32_t stage0 = smem_addr(base), full0 = map_rank(full, 0);
+            bool ok = true;
+            for (int t = cluster; t < p.num_tiles && ok; t += nclusters) {
+                const Tile ti = tile_of(p, t);
+                const int m = ti.m0 + (int)rank * 128, n = ti.n0 + (int)rank * kHalf;
+                // both CTAs' bytes of a stage are expected by the leader
+                auto stage = [&](uint32_t bytes) -> bool {
+                    if (!thread_wait(&empty[r.slot], r.phase ^ 1u, p, abort_flag)) return false;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[r.slot], 2 * bytes);
+                    return true;
+                };
+                ok = for_stages(
+                    p, p.out[ti.out],
+                    [&](int q, int kb, bool two) {
+                        if (!stage((kABytes + kBBytes) << two)) return false;
+                        const uint32_t bar = full0 + r.slot * 8;
+                        uint32_t sa = stage0 + r.slot * kFp8StageBytes;
+                        for (int c = kb * 128; c <= (kb + two) * 128; c += 128, sa += kFp8BlockBytes) {
+                            tma_load_2d_pair(sa, &p.tm_a[q], c, m, bar);
+                            tma_load_2d_pair(sa + kABytes, &p.tm_b[q], kT ? n : c, kT ? c : n, bar);
+                        }
+                        r.advance();
+                        ++issued;
+                        return true;
+                    },
+                    [&](int q, int j, bool two) {
+                        if (!stage((kABytes + kHalf * 128) << two)) return false;
+                        const uint32_t bar = full0 + r.slot * 8;
+                        uint32_t sa = stage0 + r.slot * kFp8StageBytes;
+                        for (int c = j * 64; c <= (j + two) * 64; c += 64, sa += kFp8BlockBytes) {
+                            tma_load_2d_pair(sa, &p.tm_t[q], c, m, bar);
+                            tma_load_2d_pair(sa + kABytes, &p.tm_u[q], c, n, bar);
+                        }
+                        r.advance();
+                        ++issued;
+                        return true;
+                    });
+            }
+            if (!ok && rank == 0) {
+                // Let the copies already issued land before the pair exits; their
+                // bytes are counted here, in the leader.
+                const uint32_t left = issued < kFp8Stages ? issued : kFp8Stages;
+                for (uint32_t i = issued - left; i < issued; ++i)
+                    mbar_wait(&full[i % kFp8Stages], (i / kFp8Stages) & 1u, p.status, 1000000ull);
             }
         }
-        if (!ok && rank == 0) {
-            // Let the copies already issued land before the pair exits; their
-            // bytes are counted here, in the leader.
-            const uint32_t left = issued < kFp8Stages ? issued : kFp8Stages;
-            for (uint32_t i = issued - left; i < issued; ++i)
-                mbar_wait(&full[i % kFp8Stages], (i / kFp8Stages) & 1u, p.status, 1000000ull);
-        }
+        __syncwarp();
     } else if (warp == 1) {
         // ----------------------------------------------------- MMA issuer ---
-        if (rank == 0) {
+        if (rank == 0 && lane == 0) {
             const uint32_t idesc_lr = idesc_bf16_f32(kFp8BM, kFp8BN);
+            const uint32_t idesc0 = idesc_mxf8(kFp8BM, kFp8BN, kT, 0), idesc_step = (1u << 4) | (1u << 29);
+            const uint64_t da0 = sw128_kmajor_desc(smem_addr(base)), db0 = sw128_kmajor_desc(smem_addr(base) + kABytes);
             Ring r(kFp8Stages), sr(kFp8SfSlots);
-            uint32_t it = 0, lr_count = 0, m_uses[2] = {0, 0}, chunk = 0;
+            uint32_t it = 0, lr_count = 0, sf_slot = 0, sf_col = 0;
             bool ok = true;
             for (int t = cluster; t < p.num_tiles && ok; t += nclusters, ++it) {
                 const Tile ti = tile_of(p, t);
-                Blocks b(p, p.out[ti.out]);
+                const Fp8Out &o = p.out[ti.out];
                 const uint32_t reg = it & 1u, other = reg ^ 1u;
                 const uint32_t d_main = tmem + reg * kRegionCols, d_lr = tmem + other * kRegionCols;
+                const uint32_t uses = it >> 1, other_uses = (it + 1) >> 1;  // of the regions, by earlier tiles
                 // the region's last main sum and the last rank-r term have been read
-                if (m_uses[reg] > 0) ok = warp_wait(&m_empty[reg], (m_uses[reg] - 1) & 1u, p, abort_flag, true);
-                if (ok && lr_count > 0) ok = warp_wait(l_empty, (lr_count - 1) & 1u, p, abort_flag, true);
+                if (uses > 0) ok = thread_wait(&m_empty[reg], (uses - 1) & 1u, p, abort_flag, true);
+                if (ok && lr_count > 0) ok = thread_wait(l_empty, (lr_count - 1) & 1u, p, abort_flag, true);
+                if (!ok) break;
                 tc_fence_after();
-                while (ok && b.next()) {
-                    const bool low = b.low_rank();
-                    if (low && b.first_low_rank() && m_uses[other] > 0) {
-                        ok = warp_wait(&m_empty[other], (m_uses[other] - 1) & 1u, p, abort_flag, true);
-                        if (!ok) break;
-                        tc_fence_after();
-                    }
-                    if (!low && b.new_scales()) {
-                        ok = warp_wait(&sf_full[sr.slot], sr.phase, p, abort_flag, true);
-                        if (!ok) break;
-                        tc_fence_after();
-                        ++chunk;
-                        if (lane == 0) {
-                            const uint32_t s = smem_addr(sf + sr.slot * kFp8SfBytes);
-                            const uint32_t c = tmem + kSfCol + (chunk & 1u) * kSfCols;
-                            cp_scales_pair(c, scale_desc(s));
-                            cp_scales_pair(c + 4, scale_desc(s + 512));
-                            cp_scales_pair(c + 8, scale_desc(s + 1024));
+                const int lr = lr_blocks(p, o);
+                int lr_left = lr;
+                uint32_t acc = 0;
+                ok = for_stages(
+                    p, o,
+                    [&](int, int kb, bool two) {
+                        const uint32_t sf = (uint32_t)kb & 3u;
+                        if (sf == 0) {
+                            if (!thread_wait(&sf_full[sr.slot], sr.phase, p, abort_flag, true)) return false;
+                            tc_fence_after();
+                            sf_col = tmem + kSfCol + ((sf_slot ^= 16u));  // the other slot of scales
+                            const uint64_t ds = scale_desc(smem_addr(sf_base) + sr.slot * kFp8SfBytes);
+                            cp_scales_pair(sf_col, ds);
+                            cp_scales_pair(sf_col + 4, ds + (512 >> 4));
+                            cp_scales_pair(sf_col + 8, ds + (1024 >> 4));
                             commit_pair(&sf_empty[sr.slot]);
+                            sr.advance();
                         }
-                        __syncwarp();
-                        sr.advance();
-                    }
-                    ok = warp_wait(&full[r.slot], r.phase, p, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t sa = smem_addr(base + r.slot * kFp8StageBytes);
-                        const uint64_t da = sw128_kmajor_desc(sa), db = sw128_kmajor_desc(sa + kABytes);
-                        if (low) {
+                        if (!thread_wait(&full[r.slot], r.phase, p, abort_flag)) return false;
+                        tc_fence_after();
+                        const uint32_t idesc = idesc0 + sf * idesc_step;
+                        const uint64_t da = da0 + r.slot * (kFp8StageBytes >> 4), db = db0 + r.slot * (kFp8StageBytes >> 4);
+                        // 32 columns of the contraction further: 32 bytes inside the
+                        // swizzled rows, or (N-major) 32 rows of 128 bytes
+                        mma_mxf8_pair(d_main, da, db, idesc, sf_col, sf_col + 4, acc);
+                        acc = 1;
+#pragma unroll
+                        for (int k = 1; k < 4; ++k)
+                            mma_mxf8_pair(d_main, da + 2 * k, db + (kT ? 256 : 2) * k, idesc, sf_col, sf_col + 4, 1);
+                        if (two) {
+                            constexpr int next = kFp8BlockBytes >> 4;
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma_f16_pair(d_lr, da + 2 * k, db + 2 * k, idesc_lr, !(b.first_low_rank() && k == 0));
-                        } else {
-                            const uint32_t c = tmem + kSfCol + (chunk & 1u) * kSfCols;
-                            const uint32_t idesc = idesc_mxf8(kFp8BM, kFp8BN, kT, (uint32_t)b.kb & 3u);
-                            // 32 columns of the contraction further: 32 bytes inside the
-                            // swizzled rows, or (N-major) 32 rows of 128 bytes
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_mxf8_pair(d_main, da + 2 * k, db + (kT ? 256 : 2) * k, idesc, c, c + 4,
-                                              !(b.first_main() && k == 0));
+                                mma_mxf8_pair(d_main, da + next + 2 * k, db + next + (kT ? 256 : 2) * k, idesc + idesc_step,
+                                              sf_col, sf_col + 4, 1);
                         }
                         commit_pair(&empty[r.slot]);
-                        if (low && b.last_low_rank()) commit_pair(l_full);
-                    }
-                    __syncwarp();
-                    r.advance();
-                }
+                        r.advance();
+                        return true;
+                    },
+                    [&](int, int, bool two) {
+                        const bool first = lr_left == lr;
+                        if (first && other_uses > 0) {
+                            if (!thread_wait(&m_empty[other], (other_uses - 1) & 1u, p, abort_flag, true)) return false;
+                        }
+                        if (!thread_wait(&full[r.slot], r.phase, p, abort_flag)) return false;
+                        tc_fence_after();
+                        const uint64_t da = da0 + r.slot * (kFp8StageBytes >> 4), db = db0 + r.slot * (kFp8StageBytes >> 4);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16_pair(d_lr, da + 2 * k, db + 2 * k, idesc_lr, !(first && k == 0));
+                        if (two) {
+                            constexpr int next = kFp8BlockBytes >> 4;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) mma_f16_pair(d_lr, da + next + 2 * k, db + next + 2 * k, idesc_lr, 1);
+                        }
+                        commit_pair(&empty[r.slot]);
+                        r.advance();
+                        if ((lr_left -= 1 + two) == 0) commit_pair(l_full);
+                        return true;
+                    });
                 if (!ok) break;
-                if (lane == 0) commit_pair(&m_full[reg]);
-                __syncwarp();
-                ++m_uses[reg];
-                if (b.lr > 0) ++lr_count;
+                commit_pair(&m_full[reg]);
+                lr_count += lr > 0;
             }
-            if (lane == 0) commit_pair(drain);
-            __syncwarp();
+            commit_pair(drain);
         }
+        __syncwarp();
     } else if (warp < 4) {
         // ------------------------------------------------------- scales -----
         Ring r(kFp8SfSlots);
@@ -450,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
                         ok = false;
                         break;
                     }
-                    uint8_t *dst = sf + r.slot * kFp8SfBytes + lane * 16;
+                    uint8_t *dst = sf_base + r.slot * kFp8SfBytes + lane * 16;
                     if (warp == 2) {
                         *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
                     } else {
@@ -468,15 +484,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
         // ------------------------------------------------------- epilogue ---
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
-        const uint32_t m_empty_l[2] = {map_rank(&m_empty[0], 0), map_rank(&m_empty[1], 0)};
+        const uint32_t m_empty_l = map_rank(m_empty, 0);
         const uint32_t l_empty_l = map_rank(l_empty, 0);
-        uint32_t it = 0, lr_count = 0, m_uses[2] = {0, 0};
+        uint32_t it = 0, lr_count = 0;
         for (int t = cluster; t < p.num_tiles; t += nclusters, ++it) {
             const Tile ti = tile_of(p, t);
             const Fp8Out &o = p.out[ti.out];
             const uint32_t reg = it & 1u;
-            int lr = 0;
-            for (int q = 0; q < o.nparts; ++q) lr += p.part[o.part0 + q].lr;
+            const int lr = lr_blocks(p, o);
             const int m = ti.m0 + (int)rank * 128 + quarter * 32 + lane;
             const int n0 = ti.n0 + half * kHalf;
             uint32_t d[kChunks][16];
@@ -496,8 +511,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) d[c][i] = 0;
             }
-            if (!warp_wait(&m_full[reg], m_uses[reg] & 1u, p, abort_flag)) break;
-            ++m_uses[reg];
+            if (!warp_wait(&m_full[reg], (it >> 1) & 1u, p, abort_flag)) break;
             tc_fence_after();
             if (kMode == kFp8ColSums) {
                 const bool vec = (o.N & 7) == 0 && (reinterpret_cast<uintptr_t>(o.dy) & 15u) == 0;
@@ -581,7 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_cluster(m_empty_l[reg]);
+            if (lane == 0) arrive_cluster(m_empty_l + reg * 8);
         }
     }
 
