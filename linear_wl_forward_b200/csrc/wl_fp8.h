@@ -26,9 +26,10 @@ struct Fp8Mat {
 // 1 x 128 blocks of rows of `a` (bf16 or fp32, `lda` elements apart), each
 // element times colscale[column] first (nullptr: 1, bf16 only).  Rows of codes are ld_codes
 // bytes apart, a multiple of 16; columns from `cols` up to ld_codes get code 0.
+// `zero`: n_zero words that the launch also clears.
 cudaError_t launch_fp8_quantize_rows(const void *a, wl_type type, long long lda, int rows, int cols,
                                      const float *colscale, uint8_t *codes, long long ld_codes,
-                                     uint8_t *scales, cudaStream_t stream);
+                                     uint8_t *scales, unsigned int *zero, int n_zero, cudaStream_t stream);
 // 128 x 128 blocks; cols % 16 == 0, rows of codes cols bytes apart.
 cudaError_t launch_fp8_quantize_tiles(const void *a, wl_type type, int rows, int cols, uint8_t *codes,
                                       uint8_t *scales, cudaStream_t stream);
@@ -124,5 +125,44 @@ enum Fp8Mode {
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, Fp8Mode mode, int num_sms, cudaStream_t stream);
 // ds[n] = sum over rows i < n_rows of sums[i][n].
 cudaError_t launch_fp8_sum_rows(const float *sums, int n_rows, int N, float *ds, cudaStream_t stream);
+
+// ------------------------------------------------------- few-token stream ----
+constexpr int kFp8StreamMaxM = 128;
+constexpr int kFp8StreamMaxGrid = 148;  // CTAs, whatever the device: the cut is made before one is known, and no CTA waits for another
+
+struct Fp8StreamSeg {
+    const uint8_t *w_scales;
+    const float *s;      // nullptr: 1
+    __nv_bfloat16 *y;    // M x N
+    int N;
+    int nkb;             // 128-column blocks of the contraction
+    int units;           // nkb + 64-column blocks of U
+    long long unit_begin;
+    int tile_begin;
+};
+
+struct Fp8StreamParams {
+    CUtensorMap tm_w[kMaxSeg];  // codes, box 128 bytes x 128 rows
+    CUtensorMap tm_u[kMaxSeg];  // bf16, box 64 x 128 rows
+    CUtensorMap tm_t[kMaxSeg];  // bf16, box 64 x Mp rows
+    CUtensorMap tm_x;           // codes, box 128 bytes x Mp rows
+    Fp8StreamSeg seg[kMaxSeg];
+    const uint8_t *x_scales;
+    int pitch;
+    int nseg, M;
+    int early;  // the weights may be read before the wait for the previous kernel
+    // plan
+    int Mp, stages, grid, by_tile, tiles;
+    long long units;
+    float *parts;            // [grid][2][Mp][128]
+    unsigned int *counters;  // [tiles], zero
+    int *status;
+    unsigned long long timeout_ns;
+};
+
+// Needs nseg, M and each segment's N, nkb and units.
+void plan_fp8_stream(Fp8StreamParams &p);
+size_t fp8_stream_part_floats(const Fp8StreamParams &p);
+cudaError_t launch_fp8_stream(const Fp8StreamParams &p, cudaStream_t stream);
 
 }  // namespace wl

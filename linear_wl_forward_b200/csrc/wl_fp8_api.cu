@@ -54,18 +54,44 @@ wl_status check_sizes(int M, int K, const Proj *projs, int P) {
     return WL_OK;
 }
 
+// The few-token kernel's cut of a product; s, y, maps and pointers are not set.
+void plan_stream(Fp8StreamParams &sp, int M, int K, const int *N, const int *r, int P) {
+    std::memset(&sp, 0, sizeof sp);
+    sp.M = M;
+    sp.pitch = fp8_pitch(K);
+    for (int i = 0; i < P; ++i) {
+        if (N[i] == 0) continue;
+        Fp8StreamSeg &sg = sp.seg[sp.nseg++];
+        sg.N = N[i];
+        sg.nkb = (K + kFp8Block - 1) / kFp8Block;
+        sg.units = sg.nkb + (r[i] + 63) / 64;
+    }
+    plan_fp8_stream(sp);
+}
+
 struct ForwardLayout {
     uint8_t *codes, *scales;
     __nv_bfloat16 *T[kMaxSeg];
+    float *parts;
+    unsigned int *counters;
     size_t bytes;
 };
 
+// With projs->T set or not, and x_codes given or not, the layout is the same.
 ForwardLayout forward_layout(int M, int K, const wl_proj_fp8 *projs, int P, void *ws) {
     ForwardLayout l = {};
     Arena a(ws);
     l.codes = a.take<uint8_t>((size_t)M * K);
     l.scales = a.take<uint8_t>((size_t)M * fp8_pitch(K));
     for (int i = 0; i < P; ++i) l.T[i] = a.take<__nv_bfloat16>((size_t)M * projs[i].r);
+    if (M > 0 && M <= kFp8StreamMaxM && K > 0) {
+        int N[kMaxSeg], r[kMaxSeg];
+        for (int i = 0; i < P; ++i) N[i] = projs[i].N, r[i] = projs[i].r;
+        Fp8StreamParams sp;
+        plan_stream(sp, M, K, N, r, P);
+        l.parts = a.take<float>(fp8_stream_part_floats(sp));
+        l.counters = a.take<unsigned int>(sp.tiles);
+    }
     l.bytes = a.used;
     return l;
 }
@@ -176,30 +202,65 @@ wl_status add_lowrank_codes(LowrankParams &p, const Fp8Mat &X, int I, int K, con
     return st == WL_OK ? encode_map_2d(&j.tm_b2, B_low, r, K, r, 64, 64) : st;
 }
 
+// y_p = s_p (.) (X W_p^T) + T_p U_p^T on the few-token kernel.  parts and
+// counters as plan_stream's cut needs them, counters zero.
+wl_status run_stream(const Fp8Mat &X, int M, int K, const wl_proj_fp8 *projs, __nv_bfloat16 *const *T, int P,
+                     float *parts, unsigned int *counters, bool early, const Device &dev, cudaStream_t stream) {
+    int N[kMaxSeg], r[kMaxSeg];
+    for (int i = 0; i < P; ++i) N[i] = projs[i].N, r[i] = projs[i].r;
+    Fp8StreamParams sp;
+    plan_stream(sp, M, K, N, r, P);
+    sp.x_scales = X.scales;
+    sp.early = early;
+    sp.parts = parts;
+    sp.counters = counters;
+    sp.status = dev.status;
+    sp.timeout_ns = wait_limit_ns();
+    wl_status st = encode_map_2d_u8(&sp.tm_x, X.codes, K, M, X.ld, 128, sp.Mp);
+    int k = 0;
+    for (int i = 0; i < P && st == WL_OK; ++i) {
+        const wl_proj_fp8 &q = projs[i];
+        if (q.N == 0) continue;
+        sp.seg[k].w_scales = q.scales;
+        sp.seg[k].s = q.s;
+        sp.seg[k].y = bf16(q.y);
+        st = encode_map_2d_u8(&sp.tm_w[k], q.codes, K, q.N, K, 128, 128);
+        if (st == WL_OK && q.r > 0) st = encode_map_2d(&sp.tm_u[k], bf16(q.U), q.r, q.N, q.r, 64, 128);
+        if (st == WL_OK && q.r > 0) st = encode_map_2d(&sp.tm_t[k], T[i], q.r, M, q.r, 64, sp.Mp);
+        ++k;
+    }
+    return st != WL_OK ? st : from_cuda(launch_fp8_stream(sp, stream));
+}
+
 wl_status forward_run(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, int P, uint8_t *x_codes,
                       uint8_t *x_scales, const ForwardLayout &l, const Device &dev, cudaStream_t stream) {
     const Fp8Mat X{x_codes ? x_codes : l.codes, x_scales ? x_scales : l.scales, K, fp8_pitch(K)};
+    const bool few = M <= kFp8StreamMaxM;
+    int tiles = 0;
+    for (int i = 0; i < P; ++i) tiles += (projs[i].N + 127) / 128;
     if (launch_fp8_quantize_rows(x, WL_BF16, K, M, K, nullptr, const_cast<uint8_t *>(X.codes), K,
-                                 const_cast<uint8_t *>(X.scales), stream) != cudaSuccess)
+                                 const_cast<uint8_t *>(X.scales), l.counters, few ? tiles : 0, stream) != cudaSuccess)
         return WL_ERR_CUDA;
     wl_status st;
     LowrankParams lp;
     init_lowrank(lp, dev);
+    __nv_bfloat16 *T[kMaxSeg];
     for (int i = 0; i < P; ++i) {
         const wl_proj_fp8 &q = projs[i];
+        T[i] = q.T ? bf16(q.T) : l.T[i];
         if (q.r > 0 && (q.T || q.N > 0) &&
-            (st = add_lowrank(lp, kLowrankRows, bf16(x), K, M, K, bf16(q.V), q.r, q.T ? bf16(q.T) : l.T[i], nullptr)) != WL_OK)
+            (st = add_lowrank(lp, kLowrankRows, bf16(x), K, M, K, bf16(q.V), q.r, T[i], nullptr)) != WL_OK)
             return st;
     }
     if (launch_fp8_lowrank(lp, kLowrankRows, dev.sms, stream) != cudaSuccess) return WL_ERR_CUDA;
+    if (few) return run_stream(X, M, K, projs, T, P, l.parts, l.counters, true, dev, stream);
     Fp8GemmParams g;
     init_gemm(g, M, dev.status);
     for (int i = 0; i < P; ++i) {
         const wl_proj_fp8 &q = projs[i];
         if (q.N == 0) continue;
-        const __nv_bfloat16 *T = q.T ? bf16(q.T) : l.T[i];
         const int k = g.nout;
-        st = set_part(g, k, X, M, K, Fp8Mat{q.codes, q.scales, K, fp8_pitch(K)}, q.N, K, false, T, bf16(q.U), q.r, q.N);
+        st = set_part(g, k, X, M, K, Fp8Mat{q.codes, q.scales, K, fp8_pitch(K)}, q.N, K, false, T[i], bf16(q.U), q.r, q.N);
         if (st != WL_OK) return st;
         Fp8Out &o = add_out(g, q.N, k, 1);
         o.s = q.s;
@@ -320,7 +381,8 @@ wl_status backward_run(const uint8_t *x_codes, const uint8_t *x_scales, int M, i
         }
         if (want_dx) {
             const long long ldg = round16(q.N);
-            if (launch_fp8_quantize_rows(q.dy, WL_BF16, q.N, M, q.N, q.s, l.g_codes[i], ldg, l.g_scales[i], stream) !=
+            if (launch_fp8_quantize_rows(q.dy, WL_BF16, q.N, M, q.N, q.s, l.g_codes[i], ldg, l.g_scales[i], nullptr, 0,
+                                         stream) !=
                 cudaSuccess)
                 return WL_ERR_CUDA;
             if ((st = set_part(gx, parts, Fp8Mat{l.g_codes[i], l.g_scales[i], ldg, fp8_pitch(q.N)}, M, q.N, W, q.N, K, true,
@@ -365,14 +427,43 @@ wl_status wl_quantize_fp8(const void *a, wl_type type, int rows, int cols, int b
     if (st != WL_OK) return st;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     return from_cuda(block_rows == 1
-                         ? launch_fp8_quantize_rows(a, type, cols, rows, cols, nullptr, codes, cols, scales, stream)
+                         ? launch_fp8_quantize_rows(a, type, cols, rows, cols, nullptr, codes, cols, scales, nullptr, 0, stream)
                          : launch_fp8_quantize_tiles(a, type, rows, cols, codes, scales, stream));
 }
 
-size_t wl_matmul_fp8_workspace(int M, int N, int K) {
-    (void)M, (void)N, (void)K;
-    return 0;
+}  // extern "C"
+
+namespace wl {
+namespace {
+
+struct MatmulLayout {
+    float *parts;
+    unsigned int *counters;
+    int tiles;  // counters to clear: 0 when no tile is cut
+    size_t bytes;
+};
+
+MatmulLayout matmul_layout(int M, int N, int K, void *ws) {
+    MatmulLayout l = {};
+    Arena a(ws);
+    if (M > 0 && M <= kFp8StreamMaxM && N > 0 && K > 0) {
+        const int r = 0;
+        Fp8StreamParams sp;
+        plan_stream(sp, M, K, &N, &r, 1);
+        l.tiles = sp.by_tile ? 0 : sp.tiles;
+        l.parts = a.take<float>(fp8_stream_part_floats(sp));
+        l.counters = a.take<unsigned int>(l.tiles);
+    }
+    l.bytes = a.used;
+    return l;
 }
+
+}  // namespace
+}  // namespace wl
+
+extern "C" {
+
+size_t wl_matmul_fp8_workspace(int M, int N, int K) { return wl::matmul_layout(M, N, K, nullptr).bytes; }
 
 wl_status wl_matmul_fp8(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *b_codes,
                         const uint8_t *b_scales, wl_bf16 *y, int M, int N, int K, void *workspace,
@@ -389,10 +480,22 @@ wl_status wl_matmul_fp8(const uint8_t *a_codes, const uint8_t *a_scales, const u
     if (M == 0 || N == 0) return WL_OK;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     if (K == 0) return from_cuda(cudaMemsetAsync(y, 0, (size_t)M * N * 2, stream));
-    wl_status st = check_workspace(workspace, workspace_bytes, wl_matmul_fp8_workspace(M, N, K));
+    const MatmulLayout l = matmul_layout(M, N, K, workspace);
+    wl_status st = check_workspace(workspace, workspace_bytes, l.bytes);
     if (st != WL_OK) return st;
     Device dev;
     if ((st = device_info(&dev.sms, &dev.status)) != WL_OK) return st;
+    if (M <= kFp8StreamMaxM) {
+        if (l.tiles > 0 && cudaMemsetAsync(l.counters, 0, (size_t)l.tiles * sizeof(unsigned), stream) != cudaSuccess)
+            return WL_ERR_CUDA;
+        wl_proj_fp8 q = {};
+        q.codes = b_codes;
+        q.scales = b_scales;
+        q.y = y;
+        q.N = N;
+        __nv_bfloat16 *T = nullptr;
+        return run_stream(Fp8Mat{a_codes, a_scales, K, fp8_pitch(K)}, M, K, &q, &T, 1, l.parts, l.counters, false, dev, stream);
+    }
     Fp8GemmParams g;
     init_gemm(g, M, dev.status);
     if ((st = set_part(g, 0, Fp8Mat{a_codes, a_scales, K, fp8_pitch(K)}, M, K, Fp8Mat{b_codes, b_scales, K, fp8_pitch(K)},

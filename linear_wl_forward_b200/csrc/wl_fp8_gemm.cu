@@ -646,21 +646,29 @@ cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, Fp8Mode mode, int num_sms, c
 }
 
 namespace {
-__global__ void __launch_bounds__(256) sum_rows_kernel(const float *__restrict__ sums, int n_rows, int N,
-                                                       float *__restrict__ ds) {
+// 32 columns x 32 partial sums per step and CTA, so a warp reads 128 bytes of
+// a row; each thread adds every 32nd row, then the 32 sums of a column meet in
+// a fixed order.
+__global__ void __launch_bounds__(1024) sum_rows_kernel(const float *__restrict__ sums, int n_rows, int N,
+                                                        float *__restrict__ ds) {
+    __shared__ float part[32][33];
     pdl_launch_dependents();
     pdl_wait_primary();
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= N) return;
+    const int n = blockIdx.x * 32 + threadIdx.x;
     float a = 0.f;
-    for (int i = 0; i < n_rows; ++i) a += sums[(size_t)i * N + n];
-    ds[n] = a;
+    if (n < N)
+        for (int i = threadIdx.y; i < n_rows; i += 32) a += sums[(size_t)i * N + n];
+    part[threadIdx.y][threadIdx.x] = a;
+    __syncthreads();
+    const float v = warp_sum(part[threadIdx.x][threadIdx.y]);
+    const int m = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && m < N) ds[m] = v;
 }
 }  // namespace
 
 cudaError_t launch_fp8_sum_rows(const float *sums, int n_rows, int N, float *ds, cudaStream_t stream) {
     if (N == 0) return cudaSuccess;
-    sum_rows_kernel<<<(N + 255) / 256, 256, 0, stream>>>(sums, n_rows, N, ds);
+    sum_rows_kernel<<<(N + 31) / 32, dim3(32, 32), 0, stream>>>(sums, n_rows, N, ds);
     return cudaGetLastError();
 }
 

@@ -107,7 +107,6 @@ __device__ __forceinline__ void write8(const LowrankJob &jb, int i, int j, const
 template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1) lowrank_kernel(const __grid_constant__ LowrankParams p) {
     constexpr bool kCodes = kMode == kLowrankCodes;
-    pdl_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(base + (size_t)p.stages * p.stage_bytes);
@@ -148,7 +147,9 @@ __global__ void __launch_bounds__(kThreads, 1) lowrank_kernel(const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // Dependents start once everything before this kernel is complete.
     pdl_wait_primary();
+    pdl_launch_dependents();
 
     const uint32_t b_off = kATile + (kCodes ? kCodeTile : 0);
     bool ok = true;
@@ -338,8 +339,11 @@ cudaError_t launch_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms, 
     }
     const int boxes = (std::min(widest, p.BN) + 63) / 64;
     p.stage_bytes = (int)(kATile + (mode == kLowrankCodes ? kCodeTile : 0) + terms * boxes * kBBox);
-    // narrow tiles leave room for a second CTA on the SM
-    p.stages = std::max(2, std::min(kMaxStages, (p.BN > 64 ? 200 * 1024 : 100 * 1024) / p.stage_bytes));
+    // narrow tiles leave room for a second CTA on the SM, short ranges for the kernel that follows
+    int longest = 0;
+    for (int i = 0; i < p.njobs; ++i) longest = std::max(longest, (p.job[i].kb + p.split - 1) / p.split);
+    p.stages = std::min(kMaxStages, (p.BN > 64 ? 200 * 1024 : 100 * 1024) / p.stage_bytes);
+    p.stages = std::max(2, std::min(p.stages, longest));
     p.tmem_cols = 32;
     while (p.tmem_cols < std::min((widest + 15) / 16 * 16, p.BN)) p.tmem_cols *= 2;
     // the exchange of a split tile reuses the stages

@@ -1,0 +1,448 @@
+// Few-token product with 8-bit weights: the weights are the MMA's A operand,
+//
+//   y[m][n] = s[n] * sum_k 2^(ew + ex) w[n][k] x[m][k]  +  sum_j U[n][j] T[m][j],
+//
+// so a tile is 128 output rows, its accumulator column a token (Mp = M rounded
+// up to 16, at most 128), and a 16 KB block of weights (128 rows x 128
+// columns) costs four MMAs of N = Mp.  Reading the weights bounds it: at the
+// measured copy rate a block takes each of 148 SMs about 700 cycles, the MMA
+// thread about 530.
+//
+// The call's blocks (per tile: the contraction's, then U's in 64-column
+// blocks) form one list that is cut evenly over the CTAs, one per SM, so the
+// stream has no tail; a tile cut between CTAs is summed by the CTA that
+// completes it, from fp32 parts s * z + d in CTA order (reproducible).  Short
+// calls are cut at tiles instead, which needs no exchange (plan below).
+//
+//   warp 0  TMA producer (up to 12 stages; weights are fetched before the wait
+//           for the kernel that makes x and T)
+//   warp 1  MMA issuer;  warp 2  scales;  warps 4-7  epilogue
+#include <algorithm>
+#include <atomic>
+
+#include "wl_common.cuh"
+#include "wl_fp8.h"
+
+namespace wl {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr uint32_t kWBytes = 16384;
+constexpr uint32_t kSfBytes = 1024;  // four blocks of scales: 128 rows, 128 tokens
+
+__device__ __forceinline__ void mma_mxf8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ bool thread_wait(uint64_t *bar, uint32_t parity, const Fp8StreamParams &p, volatile int *abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > p.timeout_ns) {
+            record_status(p.status, kStatusTimeout);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// A run of blocks of one tile: [u0, u1) of the tile's own blocks.
+struct Segment {
+    int seg, tile, u0, u1, nu;  // nu: the tile's blocks
+    long long t0;               // first block of the tile in the call's list
+};
+
+__device__ __forceinline__ Segment segment_at(const Fp8StreamParams &p, long long u, long long end) {
+    int sp = 0;
+    while (sp + 1 < p.nseg && u >= p.seg[sp + 1].unit_begin) ++sp;
+    const Fp8StreamSeg &sg = p.seg[sp];
+    Segment s;
+    s.seg = sp;
+    s.nu = sg.units;
+    const long long local = u - sg.unit_begin;
+    s.tile = (int)(local / sg.units);
+    s.u0 = (int)(local - (long long)s.tile * sg.units);
+    s.u1 = (int)min((long long)sg.units, s.u0 + (end - u));
+    s.t0 = sg.unit_begin + (long long)s.tile * sg.units;
+    return s;
+}
+
+// First block of CTA c.
+__device__ __forceinline__ long long range_begin(const Fp8StreamParams &p, int c) {
+    if (!p.by_tile) return p.units * c / (int)gridDim.x;
+    // whole tiles: tile t of the call starts CTA c's share
+    const int t = (int)((long long)p.tiles * c / (int)gridDim.x);
+    if (t >= p.tiles) return p.units;
+    int sp = 0;
+    while (sp + 1 < p.nseg && t >= p.seg[sp + 1].tile_begin) ++sp;
+    return p.seg[sp].unit_begin + (long long)(t - p.seg[sp].tile_begin) * p.seg[sp].units;
+}
+
+__device__ __forceinline__ int cta_of(const Fp8StreamParams &p, long long u) {
+    int c = (int)(u * (int)gridDim.x / p.units);
+    while (c + 1 < (int)gridDim.x && range_begin(p, c + 1) <= u) ++c;
+    while (c > 0 && range_begin(p, c) > u) --c;
+    return c;
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_constant__ Fp8StreamParams p) {
+    pdl_launch_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t stages = (uint32_t)p.stages, xbytes = (uint32_t)p.Mp * 128, stage_bytes = kWBytes + xbytes;
+    uint8_t *sf_base = base + stages * stage_bytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sf_base + 2 * kSfBytes);
+    uint64_t *empty = full + stages;
+    uint64_t *sf_full = empty + stages;  // [2]
+    uint64_t *sf_empty = sf_full + 2;    // [2]
+    uint64_t *acc_full = sf_empty + 2;   // [2]
+    uint64_t *acc_empty = acc_full + 2;  // [2]
+    uint64_t *drain = acc_empty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *last_flag = abort_flag + 1;
+
+    // TMEM columns: two sums of W0 x, one of U T, two slots of 8 for scales
+    const uint32_t set_cols = (uint32_t)max(p.Mp, 32), d_col = 2 * set_cols, sf_col = 3 * set_cols;
+    const uint32_t tmem_cols = sf_col + 16 <= 128 ? 128 : sf_col + 16 <= 256 ? 256 : 512;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long begin = range_begin(p, blockIdx.x), end = range_begin(p, blockIdx.x + 1);
+
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sf_full[i], 1);
+            mbar_init(&sf_empty[i], 1);
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 4);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (warp != 0) pdl_wait_primary();
+
+    if (warp == 0) {
+        // ------------------------------------------------------ producer ----
+        if (lane == 0) {
+            // weights of the first `stages` blocks, then (x and T made) their
+            // operands, then the rest in order
+            const uint32_t total = (uint32_t)(end - begin);
+            uint32_t issued = 0;
+            bool ok = true;
+            if (!p.early) pdl_wait_primary();
+            for (int pass = 0; pass < 2 && ok; ++pass) {
+                // pass 0: weights of blocks [0, head); pass 1: everything else
+                const uint32_t head = p.early ? min(total, stages) : 0;
+                if (pass == 1 && p.early) pdl_wait_primary();
+                uint32_t i = 0, slot = 0, ph = 0;
+                for (long long u = begin; u < end && ok;) {
+                    const Segment s = segment_at(p, u, end);
+                    const Fp8StreamSeg &sg = p.seg[s.seg];
+                    const int n0 = s.tile * 128;
+                    for (int b = s.u0; b < s.u1; ++b, ++i) {
+                        if (pass == 0 && i >= head) break;
+                        const bool first_pass = i < head;
+                        uint8_t *w = base + slot * stage_bytes, *x = w + kWBytes;
+                        const bool low = b >= sg.nkb;
+                        const int c = low ? (b - sg.nkb) * 64 : b * 128;
+                        if (pass == 0 || !first_pass) {
+                            if (!first_pass && !thread_wait(&empty[slot], ph ^ 1u, p, abort_flag)) {
+                                ok = false;
+                                break;
+                            }
+                            mbar_arrive_expect_tx(&full[slot], stage_bytes);
+                            tma_load_2d(w, low ? &p.tm_u[s.seg] : &p.tm_w[s.seg], c, n0, &full[slot]);
+                            ++issued;
+                        }
+                        if (pass == 1) tma_load_2d(x, low ? &p.tm_t[s.seg] : &p.tm_x, c, 0, &full[slot]);
+                        if (++slot == stages) slot = 0, ph ^= 1u;
+                    }
+                    if (pass == 0 && i >= head) break;
+                    u += s.u1 - s.u0;
+                }
+            }
+            if (!ok) {  // let the copies already issued land before the CTA exits
+                const uint32_t left = issued < stages ? issued : stages;
+                for (uint32_t i = issued - left; i < issued; ++i)
+                    mbar_wait(&full[i % stages], (i / stages) & 1u, p.status, 1000000ull);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ----------------------------------------------------- MMA issuer ---
+        if (lane == 0) {
+            // E4M3 operands (formats 0), E8M0 scales (bit 23), N >> 3, M >> 7 (27-28);
+            // the scale byte of a block: bits 4-5 (B), 29-30 (A)
+            const uint32_t idesc0 = ((uint32_t)(p.Mp >> 3) << 17) | (1u << 23) | (1u << 27);
+            const uint32_t idesc_lr = idesc_bf16_f32(128, p.Mp);
+            const uint64_t da0 = sw128_kmajor_desc(smem_addr(base)), db0 = sw128_kmajor_desc(smem_addr(base) + kWBytes);
+            const uint64_t sfd0 = (uint64_t)((smem_addr(sf_base) & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+            uint32_t slot = 0, ph = 0, count = 0, chunk = 0;
+            bool ok = true;
+            for (long long u = begin; u < end && ok; ++count) {
+                const Segment s = segment_at(p, u, end);
+                const Fp8StreamSeg &sg = p.seg[s.seg];
+                const uint32_t set = count & 1u, d_main = tmem + set * set_cols;
+                if (count >= 2) ok = thread_wait(&acc_empty[set], ((count >> 1) - 1) & 1u, p, abort_flag);
+                tc_fence_after();
+                uint32_t acc = 0, acc_lr = 0;
+                for (int b = s.u0; b < s.u1 && ok; ++b) {
+                    const bool low = b >= sg.nkb;
+                    if (low && acc_lr == 0 && count >= 1) {  // the only U T accumulator: read by the segment before
+                        ok = thread_wait(&acc_empty[set ^ 1u], ((count - 1) >> 1) & 1u, p, abort_flag);
+                        if (!ok) break;
+                    }
+                    if (!low && (b == s.u0 || (b & 3) == 0)) {
+                        ++chunk;
+                        ok = thread_wait(&sf_full[chunk & 1u], ((chunk - 1) >> 1) & 1u, p, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t sd = sfd0 + (chunk & 1u) * (kSfBytes >> 4);
+                        cp_scales(tmem + sf_col + (chunk & 1u) * 8, sd);
+                        cp_scales(tmem + sf_col + (chunk & 1u) * 8 + 4, sd + (512 >> 4));
+                        tc_commit(&sf_empty[chunk & 1u]);
+                    }
+                    ok = thread_wait(&full[slot], ph, p, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t da = da0 + slot * (stage_bytes >> 4), db = db0 + slot * (stage_bytes >> 4);
+                    if (low) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            tc_mma_f16(tmem + d_col, da + 2 * k, db + 2 * k, idesc_lr, acc_lr);
+                            acc_lr = 1;
+                        }
+                    } else {
+                        const uint32_t sf = (uint32_t)b & 3u, c = tmem + sf_col + (chunk & 1u) * 8;
+                        const uint32_t idesc = idesc0 + sf * ((1u << 4) | (1u << 29));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            mma_mxf8(d_main, da + 2 * k, db + 2 * k, idesc, c, c + 4, acc);
+                            acc = 1;
+                        }
+                    }
+                    tc_commit(&empty[slot]);
+                    if (++slot == stages) slot = 0, ph ^= 1u;
+                }
+                if (ok) tc_commit(&acc_full[set]);
+                u += s.u1 - s.u0;
+            }
+            tc_commit(drain);
+            mbar_wait(drain, 0, p.status, p.timeout_ns);  // before TMEM is released
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // --------------------------------------------------------- scales ---
+        uint32_t chunk = 0;
+        bool ok = true;
+        for (long long u = begin; u < end && ok;) {
+            const Segment s = segment_at(p, u, end);
+            const Fp8StreamSeg &sg = p.seg[s.seg];
+            const uint8_t *wrow = sg.w_scales + (size_t)s.tile * p.pitch;
+            for (int b = s.u0; b < min(s.u1, sg.nkb); b = (b & ~3) + 4) {
+                ++chunk;
+                const int q = b >> 2;
+                const uint32_t ww = __ldg(reinterpret_cast<const uint32_t *>(wrow + 4 * q));
+                uint32_t xw[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int m = i * 32 + lane;
+                    xw[i] = m < p.M ? __ldg(reinterpret_cast<const uint32_t *>(p.x_scales + (size_t)m * p.pitch + 4 * q)) : 0x7F7F7F7Fu;
+                }
+                if (chunk > 2) {
+                    ok = thread_wait(&sf_empty[chunk & 1u], ((chunk - 3) >> 1) & 1u, p, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                }
+                uint8_t *dst = sf_base + (chunk & 1u) * kSfBytes + lane * 16;
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(ww, ww, ww, ww);
+                *reinterpret_cast<uint4 *>(dst + 512) = make_uint4(xw[0], xw[1], xw[2], xw[3]);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sf_full[chunk & 1u]);
+            }
+            u += s.u1 - s.u0;
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------- epilogue ---
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
+        const size_t part_stride = (size_t)p.Mp * 128;
+        uint32_t count = 0;
+        for (long long u = begin; u < end; ++count) {
+            const Segment s = segment_at(p, u, end);
+            const Fp8StreamSeg &sg = p.seg[s.seg];
+            const uint32_t set = count & 1u;
+            const bool whole = s.u0 == 0 && s.u1 == s.nu;
+            const bool has_z = s.u0 < sg.nkb, has_d = s.u1 > sg.nkb;
+            bool ok = thread_wait(&acc_full[set], (count >> 1) & 1u, p, abort_flag);
+            {
+                // the four warps meet below: they go on, or stop, together
+                uint32_t fail;
+                asm volatile(
+                    "{\n\t.reg .pred p, q;\n\t"
+                    "setp.ne.u32 p, %1, 0;\n\t"
+                    "bar.red.or.pred q, 1, 128, p;\n\t"
+                    "selp.u32 %0, 1, 0, q;\n\t}"
+                    : "=r"(fail)
+                    : "r"((uint32_t)!ok)
+                    : "memory");
+                if (fail) break;
+            }
+            tc_fence_after();
+            const int n = s.tile * 128 + row;
+            const bool in = n < sg.N;
+            const float sc = sg.s && in ? __ldg(sg.s + n) : 1.f;
+            // which of the CTA's two partial tiles this is: its first, or its last
+            float *part = p.parts + ((size_t)blockIdx.x * 2 + (u == begin ? 0 : 1)) * part_stride;
+            for (int c = 0; c < p.M; c += 8) {
+                uint32_t z[8], d[8];
+                if (has_z) tmem_ld8(lane_addr + set * set_cols + c, z);
+                if (has_d) tmem_ld8(lane_addr + d_col + c, d);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float zf = has_z ? __uint_as_float(z[i]) : 0.f, df = has_d ? __uint_as_float(d[i]) : 0.f;
+                    const float v = has_z ? fmaf(sc, zf, df) : df;
+                    if (whole) {
+                        if (in && c + i < p.M) sg.y[(size_t)(c + i) * sg.N + n] = __float2bfloat16_rn(v);
+                    } else if (c + i < p.M) {
+                        part[(c + i) * 128 + row] = v;
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[set]);
+            if (!whole) {
+                const int c0 = cta_of(p, s.t0), c1 = cta_of(p, s.t0 + s.nu - 1);
+                __threadfence();
+                asm volatile("bar.sync 2, 128;" ::: "memory");
+                if (threadIdx.x == 128)
+                    *last_flag = atomicAdd(&p.counters[sg.tile_begin + s.tile], 1u) == (unsigned)(c1 - c0);
+                asm volatile("bar.sync 2, 128;" ::: "memory");
+                if (*last_flag) {
+                    __threadfence();
+                    // the tile is the last piece of its first CTA (or all of
+                    // that CTA's range so far), the first piece of the others
+                    const float *first = p.parts + ((size_t)c0 * 2 + (range_begin(p, c0) < s.t0 ? 1 : 0)) * part_stride + row;
+                    for (int m = 0; m < p.M; m += 4) {
+                        float v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = m + i < p.M ? __ldcg(first + (m + i) * 128) : 0.f;
+                        for (int k = c0 + 1; k <= c1; ++k) {
+                            const float *q = p.parts + (size_t)k * 2 * part_stride + row;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (m + i < p.M) v[i] += __ldcg(q + (m + i) * 128);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (in && m + i < p.M) sg.y[(size_t)(m + i) * sg.N + n] = __float2bfloat16_rn(v[i]);
+                    }
+                }
+                asm volatile("bar.sync 2, 128;" ::: "memory");  // last_flag is used again
+            }
+            u += s.u1 - s.u0;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, tmem_cols);
+    }
+}
+
+// CTAs and the cut of the list.  Cutting at tiles leaves SMs idle when the
+// tiles are few; cutting evenly costs an exchange, about as long as ten blocks
+// take one SM whose loads have the memory to themselves (about 250 cycles per
+// block; 700 when all 148 SMs stream).
+void plan_fp8_stream(Fp8StreamParams &p) {
+    constexpr int num_sms = kFp8StreamMaxGrid;
+    long long units = 0;
+    int tiles = 0, longest = 0;
+    for (int i = 0; i < p.nseg; ++i) {
+        Fp8StreamSeg &sg = p.seg[i];
+        sg.unit_begin = units;
+        sg.tile_begin = tiles;
+        const int t = (sg.N + 127) / 128;
+        tiles += t;
+        units += (long long)t * sg.units;
+        longest = std::max(longest, sg.units);
+    }
+    p.units = units;
+    p.tiles = tiles;
+    const int by_tile = std::min(tiles, num_sms), even = (int)std::min<long long>(units, num_sms);
+    auto block = [&](int ctas) { return std::max(250.0, 700.0 * ctas / num_sms); };
+    const double cost_tile = (double)((tiles + by_tile - 1) / by_tile) * longest * block(by_tile);
+    const double cost_even = (double)((units + even - 1) / even) * block(even) + 2500;
+    p.by_tile = cost_tile <= cost_even;
+    p.grid = p.by_tile ? by_tile : even;
+    p.Mp = (p.M + 15) / 16 * 16;
+    const int stage = (int)kWBytes + p.Mp * 128;
+    p.stages = std::min(12, (200 * 1024) / stage);
+}
+
+size_t fp8_stream_part_floats(const Fp8StreamParams &p) { return p.by_tile ? 0 : (size_t)p.grid * 2 * p.Mp * 128; }
+
+cudaError_t launch_fp8_stream(const Fp8StreamParams &p, cudaStream_t stream) {
+    if (p.units == 0) return cudaSuccess;
+    const size_t smem = 1024 + (size_t)p.stages * (kWBytes + p.Mp * 128) + 2 * kSfBytes + (2 * p.stages + 9) * 8 + 16;
+    if (p.M < 1 || p.M > kFp8StreamMaxM || smem > 227 * 1024) return cudaErrorInvalidValue;
+    static std::atomic<bool> done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!done[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(fp8_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e != cudaSuccess) return e;
+        done[dev].store(true, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fp8_stream_kernel, p);
+}
+
+}  // namespace wl
