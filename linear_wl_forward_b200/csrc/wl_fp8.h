@@ -46,8 +46,11 @@ enum LowrankMode {
     kLowrankCodes      // A row-major in k, 8 bits with 1 x 128 blocks along i; B in two bf16 terms
 };
 
+// Rows of A per tile that are loaded (Rows mode).
+inline int lowrank_a_rows(int I) { return I >= 128 ? 128 : (I + 15) / 16 * 16; }
+
 struct LowrankJob {
-    CUtensorMap tm_a;   // box 64 columns x 128 rows (Rows), 64 x 64 (Cols), 32 words x 64 rows, not swizzled (Codes)
+    CUtensorMap tm_a;   // box 64 columns x lowrank_a_rows rows (Rows), 64 x 64 (Cols), 32 words x 64 rows, not swizzled (Codes)
     CUtensorMap tm_b;   // K x r, box 64 x 64
     CUtensorMap tm_b2;  // Codes: the low term
     const uint8_t *a_scales;
@@ -62,7 +65,7 @@ struct LowrankJob {
 struct LowrankParams {
     LowrankJob job[kMaxSeg];
     int njobs;
-    int BN, split, stages, stage_bytes, tmem_cols;  // filled by the launcher
+    int BN, split, stages, a_bytes, stage_bytes, tmem_cols;  // filled by the launcher
     int *status;
     unsigned long long timeout_ns;
 };
@@ -135,8 +138,9 @@ struct Fp8StreamSeg {
     const float *s;      // nullptr: 1
     __nv_bfloat16 *y;    // M x N
     int N;
-    int nkb;             // 128-column blocks of the contraction
-    int units;           // nkb + 64-column blocks of U
+    int nkb, lr;         // 128-column blocks of the contraction, 64-column blocks of U
+    // plan
+    int kpairs, units;   // pairs of the contraction's blocks; with those of U
     long long unit_begin;
     int tile_begin;
 };
@@ -160,7 +164,7 @@ struct Fp8StreamParams {
     unsigned long long timeout_ns;
 };
 
-// Needs nseg, M and each segment's N, nkb and units.
+// Needs nseg, M and each segment's N, nkb and lr.
 void plan_fp8_stream(Fp8StreamParams &p);
 size_t fp8_stream_part_floats(const Fp8StreamParams &p);
 cudaError_t launch_fp8_stream(const Fp8StreamParams &p, cudaStream_t stream);

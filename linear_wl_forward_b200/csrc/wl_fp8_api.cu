@@ -64,7 +64,7 @@ void plan_stream(Fp8StreamParams &sp, int M, int K, const int *N, const int *r, 
         Fp8StreamSeg &sg = sp.seg[sp.nseg++];
         sg.N = N[i];
         sg.nkb = (K + kFp8Block - 1) / kFp8Block;
-        sg.units = sg.nkb + (r[i] + 63) / 64;
+        sg.lr = (r[i] + 63) / 64;
     }
     plan_fp8_stream(sp);
 }
@@ -181,7 +181,8 @@ wl_status add_lowrank(LowrankParams &p, LowrankMode mode, const __nv_bfloat16 *A
     j.kb = (K + 63) / 64;
     j.out = out;
     j.out_low = out_low;
-    wl_status st = mode == kLowrankRows ? encode_map_2d(&j.tm_a, A, K, I, lda, 64, 128)
+    // rows that do not exist need not be loaded: each fills its own row of the sums
+    wl_status st = mode == kLowrankRows ? encode_map_2d(&j.tm_a, A, K, I, lda, 64, lowrank_a_rows(I))
                                         : encode_map_2d(&j.tm_a, A, I, K, lda, 64, 64);
     return st == WL_OK ? encode_map_2d(&j.tm_b, B, r, K, r, 64, 64) : st;
 }

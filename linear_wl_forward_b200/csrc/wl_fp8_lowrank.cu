@@ -13,7 +13,7 @@
 //
 // B is read as it lies (N-major operand, boxes of 64 columns x 64 rows).
 // A CTA owns 128 rows x up to 256 columns of one product and a range of the
-// contraction; the CTAs of a cluster (1, 2, 4 or 8) share a tile's contraction
+// contraction; the CTAs of a cluster (1 to 16) share a tile's contraction
 // and add their sums over distributed shared memory in rank order, so there
 // are no partial results in memory and the result is reproducible.  The tile
 // width and the split are chosen by a cost estimate (plan below): a tile of N
@@ -21,8 +21,8 @@
 // against 2 N tensor-core cycles, so wide tiles are fed best; short products
 // are cut instead, to put every SM to work.
 //
-//   warp 0  TMA producer;  warp 1  MMA issuer;  warps 2-5  expansion of codes,
-//   then the epilogue
+//   warp 0  TMA producer;  warp 1  MMA issuer;  warps 2-5  epilogue;
+//   warps 2-9  expansion of codes, where there are any
 #include <algorithm>
 #include <atomic>
 #include <cstring>
@@ -36,11 +36,14 @@ namespace wl {
 
 namespace {
 
-constexpr int kThreads = 192;
+// warps 2.. : four of them run the epilogue; in Codes mode eight expand the codes
+constexpr int threads_of(int mode) { return mode == kLowrankCodes ? 320 : 192; }
+constexpr int kExpanders = 8;
 constexpr uint32_t kATile = 16384;  // 128 x 64 bf16
 constexpr uint32_t kBBox = 8192;    // 64 x 64 bf16
 constexpr uint32_t kCodeTile = 8192;  // 64 rows x 128 codes
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 12;
+constexpr int kMaxSplit = 16;
 
 // Descriptor of an M- or N-major bf16 tile: boxes of 64 elements (128 swizzled
 // bytes) x 64 contraction rows; 8 rows are 1024 bytes, the next 64 elements one box on.
@@ -105,7 +108,7 @@ __device__ __forceinline__ void write8(const LowrankJob &jb, int i, int j, const
 }  // namespace
 
 template <int kMode>
-__global__ void __launch_bounds__(kThreads, 1) lowrank_kernel(const __grid_constant__ LowrankParams p) {
+__global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __grid_constant__ LowrankParams p) {
     constexpr bool kCodes = kMode == kLowrankCodes;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -134,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) lowrank_kernel(const __grid_const
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
-            mbar_init(&ready[i], 4);
+            mbar_init(&ready[i], kExpanders);
         }
         mbar_init(done, 1);
         fence_barrier_init();
@@ -151,18 +154,19 @@ __global__ void __launch_bounds__(kThreads, 1) lowrank_kernel(const __grid_const
     pdl_wait_primary();
     pdl_launch_dependents();
 
-    const uint32_t b_off = kATile + (kCodes ? kCodeTile : 0);
+    const uint32_t a_bytes = kMode == kLowrankRows ? (uint32_t)p.a_bytes : kATile;
+    const uint32_t b_off = a_bytes + (kCodes ? kCodeTile : 0);
     bool ok = true;
     if (warp == 0) {
-        uint32_t slot = 0, ph = 0, issued = 0;
-        for (int kb = kb0; kb < kb1; ++kb) {
-            if (!all_wait(&empty[slot], ph ^ 1u, p)) {
-                ok = false;
-                break;
-            }
-            if (lane == 0) {
+        if (lane == 0) {
+            uint32_t slot = 0, ph = 0, issued = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(&empty[slot], ph ^ 1u, p.status, p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
                 uint8_t *st = base + (size_t)slot * p.stage_bytes;
-                mbar_arrive_expect_tx(&full[slot], (kCodes ? kCodeTile : kATile) + (uint32_t)(terms * boxes) * kBBox);
+                mbar_arrive_expect_tx(&full[slot], (kCodes ? kCodeTile : a_bytes) + (uint32_t)(terms * boxes) * kBBox);
                 if (kMode == kLowrankRows) {
                     tma_load_2d(st, &jb.tm_a, kb * 64, i0, &full[slot]);
                 } else if (kMode == kLowrankCols) {
@@ -175,64 +179,77 @@ __global__ void __launch_bounds__(kThreads, 1) lowrank_kernel(const __grid_const
                     tma_load_2d(st + b_off + b * kBBox, &jb.tm_b, j0 + b * 64, kb * 64, &full[slot]);
                     if (kCodes) tma_load_2d(st + b_off + (boxes + b) * kBBox, &jb.tm_b2, j0 + b * 64, kb * 64, &full[slot]);
                 }
+                ++issued;
+                if (++slot == (uint32_t)p.stages) slot = 0, ph ^= 1u;
             }
-            __syncwarp();
-            ++issued;
-            if (++slot == (uint32_t)p.stages) slot = 0, ph ^= 1u;
+            if (!ok) {  // let the copies already issued land before the CTA exits
+                const uint32_t left = issued < (uint32_t)p.stages ? issued : p.stages;
+                for (uint32_t i = issued - left; i < issued; ++i)
+                    mbar_wait(&full[i % p.stages], (i / p.stages) & 1u, p.status, 1000000ull);
+            }
         }
-        if (!ok) {  // let the copies already issued land before the CTA exits
-            const uint32_t left = issued < (uint32_t)p.stages ? issued : p.stages;
-            for (uint32_t i = issued - left; i < issued; ++i)
-                mbar_wait(&full[i % p.stages], (i / p.stages) & 1u, p.status, 1000000ull);
-        }
+        __syncwarp();
     } else if (warp == 1) {
-        // fp32 sums of bf16 products; A M-major (bit 15) unless its rows run along i; B N-major (bit 16)
-        const uint32_t idesc = idesc_bf16_f32(128, n_mma) | (kMode == kLowrankRows ? 0u : 1u << 15) | 1u << 16;
-        uint32_t slot = 0, ph = 0;
-        for (int kb = kb0; kb < kb1; ++kb) {
-            if (!all_wait(kCodes ? &ready[slot] : &full[slot], ph, p)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            if (lane == 0) {
-                const uint32_t sa = smem_addr(base + (size_t)slot * p.stage_bytes);
-                const uint64_t da = kMode == kLowrankRows ? sw128_kmajor_desc(sa) : mn_major_desc(sa);
-                for (int t = 0; t < terms; ++t) {
-                    const uint64_t db = mn_major_desc(sa + b_off + (uint32_t)(t * boxes) * kBBox);
+        if (lane == 0) {
+            // fp32 sums of bf16 products; A M-major (bit 15) unless its rows run along i; B N-major (bit 16)
+            const uint32_t idesc = idesc_bf16_f32(128, n_mma) | (kMode == kLowrankRows ? 0u : 1u << 15) | 1u << 16;
+            const uint32_t s0 = smem_addr(base);
+            const uint64_t da0 = kMode == kLowrankRows ? sw128_kmajor_desc(s0) : mn_major_desc(s0);
+            const uint64_t db0 = mn_major_desc(s0 + b_off), db1 = mn_major_desc(s0 + b_off + (uint32_t)boxes * kBBox);
+            const uint64_t step = (uint32_t)p.stage_bytes >> 4;
+            uint32_t slot = 0, ph = 0, acc = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(kCodes ? &ready[slot] : &full[slot], ph, p.status, p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t da = da0 + slot * step, db = db0 + slot * step;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)  // 16 contraction rows on: 32 bytes, or 16 rows of 128
-                        tc_mma_f16(tmem, da + (kMode == kLowrankRows ? 2 : 128) * k, db + 128 * k, idesc,
-                                   kb > kb0 || t > 0 || k > 0);
+                for (int k = 0; k < 4; ++k) {  // 16 contraction rows on: 32 bytes, or 16 rows of 128
+                    tc_mma_f16(tmem, da + (kMode == kLowrankRows ? 2 : 128) * k, db + 128 * k, idesc, acc);
+                    acc = 1;
+                }
+                if (kCodes) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tc_mma_f16(tmem, da + 128 * k, db1 + slot * step + 128 * k, idesc, 1);
                 }
                 tc_commit(&empty[slot]);
+                if (++slot == (uint32_t)p.stages) slot = 0, ph ^= 1u;
             }
-            __syncwarp();
-            if (++slot == (uint32_t)p.stages) slot = 0, ph ^= 1u;
+            tc_commit(done);
+            // Outstanding MMAs end before TMEM is released, whatever happened.
+            if (!ok) mbar_wait(done, 0, p.status, 1000000ull);
         }
-        if (lane == 0) tc_commit(done);
         __syncwarp();
-        // Outstanding MMAs end before TMEM is released, whatever happened.
-        if (!ok) mbar_wait(done, 0, p.status, 1000000ull);
     } else {
         const int tid = threadIdx.x - 64;
         if (kCodes) {
+            // 16 codes of one contraction row per step, two steps of 32 rows per
+            // block; the next block's scales are on their way meanwhile
+            const int k0 = tid >> 3, seg = tid & 7;
+            auto scale_of = [&](int kb, int s) -> uint32_t {
+                const int m = kb * 64 + s * 32 + k0;
+                return m < jb.K ? __ldg(jb.a_scales + (size_t)m * jb.a_pitch + (i0 >> 7)) : 127u;
+            };
+            uint32_t e[2] = {127u, 127u};
+            if (kb0 < kb1) e[0] = scale_of(kb0, 0), e[1] = scale_of(kb0, 1);
             uint32_t slot = 0, ph = 0;
             for (int kb = kb0; kb < kb1; ++kb) {
+                uint32_t next[2] = {127u, 127u};
+                if (kb + 1 < kb1) next[0] = scale_of(kb + 1, 0), next[1] = scale_of(kb + 1, 1);
                 if (!all_wait(&full[slot], ph, p)) {
                     ok = false;
                     break;
                 }
                 uint8_t *st = base + (size_t)slot * p.stage_bytes;
-                // 16 codes of one row per step; chunk c of 16 bytes of row k sits at c ^ (k & 7)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int k = s * 16 + (tid >> 3), seg = tid & 7;
-                    const int m = kb * 64 + k;
-                    const uint32_t e = m < jb.K ? __ldg(jb.a_scales + (size_t)m * jb.a_pitch + (i0 >> 7)) : 127u;
+                for (int s = 0; s < 2; ++s) {
+                    const int k = s * 32 + k0;
                     const uint4 c = *reinterpret_cast<const uint4 *>(st + kATile + k * 128 + seg * 16);
                     // 2^(e - 127); e = 0 is the subnormal 2^-127, e = 255 the NaN scale
-                    const float sc = e == 0 ? __uint_as_float(0x00400000u) : e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(e << 23);
+                    const float sc = e[s] == 0 ? __uint_as_float(0x00400000u)
+                                               : e[s] == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(e[s] << 23);
                     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
                     uint32_t o[8];
 #pragma unroll
@@ -240,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) lowrank_kernel(const __grid_const
                         o[2 * q] = expand_pair(w[q] & 0xFFFFu, sc);
                         o[2 * q + 1] = expand_pair(w[q] >> 16, sc);
                     }
+                    // chunk c of 16 bytes of row k sits at c ^ (k & 7)
                     uint8_t *row = st + (seg >> 2) * kBBox + k * 128;
                     const int ch = (seg & 3) * 2;
                     *reinterpret_cast<uint4 *>(row + ((ch ^ (k & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -248,16 +266,18 @@ __global__ void __launch_bounds__(kThreads, 1) lowrank_kernel(const __grid_const
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ready[slot]);
+                e[0] = next[0];
+                e[1] = next[1];
                 if (++slot == (uint32_t)p.stages) slot = 0, ph ^= 1u;
             }
         }
         // MMAs done.  A CTA with an empty range of the contraction has no sums.
-        if (ok && kb1 > kb0) ok = all_wait(done, 0, p);
+        if (ok && warp < 6 && kb1 > kb0) ok = all_wait(done, 0, p);
         tc_fence_after();
         const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16);
         float *buf = reinterpret_cast<float *>(base);  // [column][row], over the idle stages
-        if (ok)
+        if (ok && warp < 6)
             for (int c = 0; c < n_mma; c += 8) {
                 float v[8];
                 if (kb1 > kb0) {
@@ -277,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) lowrank_kernel(const __grid_const
     if (S > 1) {
         __syncwarp();
         cluster_barrier();  // every CTA's sums are in its shared memory
-        if (warp >= 2 && ok) {
+        if (warp >= 2 && warp < 6 && ok) {
             const int row = (warp & 3) * 32 + lane;
             for (int c = (int)rank * 8; c < width; c += 8 * S) {
                 float v[8] = {};
@@ -299,14 +319,16 @@ __global__ void __launch_bounds__(kThreads, 1) lowrank_kernel(const __grid_const
     }
 }
 
-// Tile width and split of the contraction.  Estimated cycles of a call: waves
-// of CTAs, each with its blocks of the contraction at the slower of the MMAs
-// (2 cycles per column, terms times) and the loads (64 bytes per cycle), plus
-// about 3000 for the start, the drain and, with a split, the exchange.
+// Tile width and split of the contraction, by an estimate of a call's cycles:
+// waves of CTAs, each with its blocks of the contraction at the slowest of the
+// MMAs (2 cycles per column), the loads (48 bytes per cycle and SM) and the
+// issuing thread (450 cycles), plus 5000 for the start and the drain and, with
+// a split, the exchange of 128 x BN sums (60 cycles per column; measured:
+// 128 x 256 tiles cut in four took 63 us where whole ones take 28).
 static void plan(LowrankParams &p, int terms, int num_sms) {
     double best = 0;
     for (int bn = 256; bn >= 64; bn /= 2)
-        for (int s = 1; s <= 8; s *= 2) {
+        for (int s = 1; s <= kMaxSplit; s *= 2) {
             long long tiles = 0;
             int kb = 0, widest = 0;
             for (int i = 0; i < p.njobs; ++i) {
@@ -316,9 +338,9 @@ static void plan(LowrankParams &p, int terms, int num_sms) {
             }
             if (bn > 64 && bn / 2 >= widest) continue;
             const int cols = std::min(bn, (widest + 15) / 16 * 16);
-            const double block = std::max(2.0 * cols * terms, (16384 + 128.0 * cols * terms) / 64);
+            const double block = std::max({2.0 * cols * terms, (p.a_bytes + 128.0 * cols * terms) / 48, 200.0 + 256.0 * terms});
             const double waves = (double)((tiles * s + num_sms - 1) / num_sms);
-            const double cost = waves * (((kb + s - 1) / s) * block + 3000 + (s > 1 ? 1000 + 8.0 * cols : 0));
+            const double cost = waves * (((kb + s - 1) / s) * block + 5000 + (s > 1 ? 1000 + 60.0 * cols : 0));
             if (best == 0 || cost < best) {
                 best = cost;
                 p.BN = bn;
@@ -330,6 +352,9 @@ static void plan(LowrankParams &p, int terms, int num_sms) {
 cudaError_t launch_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms, cudaStream_t stream) {
     if (p.njobs == 0) return cudaSuccess;
     const int terms = mode == kLowrankCodes ? 2 : 1;
+    int rows = 0;
+    for (int i = 0; i < p.njobs; ++i) rows = std::max(rows, lowrank_a_rows(p.job[i].I));
+    p.a_bytes = mode == kLowrankRows ? rows * 128 : (int)kATile;
     plan(p, terms, num_sms);
     int tiles = 0, widest = 0;
     for (int i = 0; i < p.njobs; ++i) {
@@ -338,18 +363,19 @@ cudaError_t launch_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms, 
         widest = std::max(widest, p.job[i].r);
     }
     const int boxes = (std::min(widest, p.BN) + 63) / 64;
-    p.stage_bytes = (int)(kATile + (mode == kLowrankCodes ? kCodeTile : 0) + terms * boxes * kBBox);
-    // narrow tiles leave room for a second CTA on the SM, short ranges for the kernel that follows
+    p.stage_bytes = (int)(p.a_bytes + (mode == kLowrankCodes ? kCodeTile : 0) + terms * boxes * kBBox);
+    // narrow tiles leave room for a second CTA on the SM, or for the kernel that follows
     int longest = 0;
     for (int i = 0; i < p.njobs; ++i) longest = std::max(longest, (p.job[i].kb + p.split - 1) / p.split);
-    p.stages = std::min(kMaxStages, (p.BN > 64 ? 200 * 1024 : 100 * 1024) / p.stage_bytes);
+    p.stages = std::min(kMaxStages, (p.BN > 64 ? 200 * 1024 : p.a_bytes < (int)kATile ? 60 * 1024 : 100 * 1024) / p.stage_bytes);
     p.stages = std::max(2, std::min(p.stages, longest));
     p.tmem_cols = 32;
     while (p.tmem_cols < std::min((widest + 15) / 16 * 16, p.BN)) p.tmem_cols *= 2;
     // the exchange of a split tile reuses the stages
     const size_t exchange = p.split > 1 ? (size_t)std::min((widest + 15) / 16 * 16, p.BN) * 512 : 0;
     while ((size_t)p.stages * p.stage_bytes < exchange) ++p.stages;
-    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + (3 * kMaxStages + 1) * 8 + 16;
+    // an MMA reads 128 rows of A, so the last stage's tile may end behind the stages
+    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + std::max<size_t>((3 * kMaxStages + 1) * 8 + 16, kATile);
     if (p.stages > kMaxStages || smem > 227 * 1024) return cudaErrorInvalidValue;
     void (*const kernels[3])(LowrankParams) = {lowrank_kernel<kLowrankRows>, lowrank_kernel<kLowrankCols>,
                                                lowrank_kernel<kLowrankCodes>};
@@ -360,12 +386,13 @@ cudaError_t launch_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms, 
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!done[dev][mode].load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(kernels[mode], cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernels[mode], cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         done[dev][mode].store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * p.split));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads_of(mode));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];

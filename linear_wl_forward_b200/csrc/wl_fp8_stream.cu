@@ -5,16 +5,18 @@
 // so a tile is 128 output rows, its accumulator column a token (Mp = M rounded
 // up to 16, at most 128), and a 16 KB block of weights (128 rows x 128
 // columns) costs four MMAs of N = Mp.  Reading the weights bounds it: at the
-// measured copy rate a block takes each of 148 SMs about 700 cycles, the MMA
-// thread about 530.
+// measured copy rate a block takes each of 148 SMs about 700 cycles.  The MMA
+// thread needs about 64 cycles per MMA, 130 per barrier wait and 65 per commit,
+// so a stage holds two blocks (one block per stage: 60 us against 47 for
+// Gemma-4's gate/up at one token).
 //
-// The call's blocks (per tile: the contraction's, then U's in 64-column
-// blocks) form one list that is cut evenly over the CTAs, one per SM, so the
-// stream has no tail; a tile cut between CTAs is summed by the CTA that
+// The call's work (per tile: the contraction in pairs of blocks, then U's
+// 64-column blocks in pairs) forms one list of units that is cut evenly over
+// the CTAs, one per SM, so the stream has no tail; a tile cut between CTAs is summed by the CTA that
 // completes it, from fp32 parts s * z + d in CTA order (reproducible).  Short
 // calls are cut at tiles instead, which needs no exchange (plan below).
 //
-//   warp 0  TMA producer (up to 12 stages; weights are fetched before the wait
+//   warp 0  TMA producer (up to 6 stages of two blocks; weights are fetched before the wait
 //           for the kernel that makes x and T)
 //   warp 1  MMA issuer;  warp 2  scales;  warps 4-7  epilogue
 #include <algorithm>
@@ -63,10 +65,10 @@ __device__ __forceinline__ bool thread_wait(uint64_t *bar, uint32_t parity, cons
     return true;
 }
 
-// A run of blocks of one tile: [u0, u1) of the tile's own blocks.
+// A run of units of one tile: [u0, u1) of the tile's own.
 struct Segment {
-    int seg, tile, u0, u1, nu;  // nu: the tile's blocks
-    long long t0;               // first block of the tile in the call's list
+    int seg, tile, u0, u1, nu;  // nu: the tile's units
+    long long t0;               // first unit of the tile in the call's list
 };
 
 __device__ __forceinline__ Segment segment_at(const Fp8StreamParams &p, long long u, long long end) {
@@ -84,7 +86,7 @@ __device__ __forceinline__ Segment segment_at(const Fp8StreamParams &p, long lon
     return s;
 }
 
-// First block of CTA c.
+// First unit of CTA c.
 __device__ __forceinline__ long long range_begin(const Fp8StreamParams &p, int c) {
     if (!p.by_tile) return p.units * c / (int)gridDim.x;
     // whole tiles: tile t of the call starts CTA c's share
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
     pdl_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    const uint32_t stages = (uint32_t)p.stages, xbytes = (uint32_t)p.Mp * 128, stage_bytes = kWBytes + xbytes;
+    const uint32_t stages = (uint32_t)p.stages, block_bytes = kWBytes + (uint32_t)p.Mp * 128, stage_bytes = 2 * block_bytes;
     uint8_t *sf_base = base + stages * stage_bytes;
     uint64_t *full = reinterpret_cast<uint64_t *>(sf_base + 2 * kSfBytes);
     uint64_t *empty = full + stages;
@@ -155,14 +157,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
     if (warp == 0) {
         // ------------------------------------------------------ producer ----
         if (lane == 0) {
-            // weights of the first `stages` blocks, then (x and T made) their
+            // weights of the first `stages` units, then (x and T made) their
             // operands, then the rest in order
             const uint32_t total = (uint32_t)(end - begin);
             uint32_t issued = 0;
             bool ok = true;
             if (!p.early) pdl_wait_primary();
             for (int pass = 0; pass < 2 && ok; ++pass) {
-                // pass 0: weights of blocks [0, head); pass 1: everything else
+                // pass 0: weights of units [0, head); pass 1: everything else
                 const uint32_t head = p.early ? min(total, stages) : 0;
                 if (pass == 1 && p.early) pdl_wait_primary();
                 uint32_t i = 0, slot = 0, ph = 0;
@@ -172,20 +174,24 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
                     const int n0 = s.tile * 128;
                     for (int b = s.u0; b < s.u1; ++b, ++i) {
                         if (pass == 0 && i >= head) break;
-                        const bool first_pass = i < head;
-                        uint8_t *w = base + slot * stage_bytes, *x = w + kWBytes;
-                        const bool low = b >= sg.nkb;
-                        const int c = low ? (b - sg.nkb) * 64 : b * 128;
+                        const bool first_pass = i < head, low = b >= sg.kpairs;
+                        // the unit's one or two blocks, `step` columns each
+                        const int blk = 2 * (low ? b - sg.kpairs : b), step = low ? 64 : 128;
+                        const int two = blk + 1 < (low ? sg.lr : sg.nkb);
+                        uint8_t *st = base + slot * stage_bytes;
                         if (pass == 0 || !first_pass) {
                             if (!first_pass && !thread_wait(&empty[slot], ph ^ 1u, p, abort_flag)) {
                                 ok = false;
                                 break;
                             }
-                            mbar_arrive_expect_tx(&full[slot], stage_bytes);
-                            tma_load_2d(w, low ? &p.tm_u[s.seg] : &p.tm_w[s.seg], c, n0, &full[slot]);
+                            mbar_arrive_expect_tx(&full[slot], block_bytes << two);
+                            for (int k = 0; k <= two; ++k)
+                                tma_load_2d(st + k * block_bytes, low ? &p.tm_u[s.seg] : &p.tm_w[s.seg], (blk + k) * step, n0, &full[slot]);
                             ++issued;
                         }
-                        if (pass == 1) tma_load_2d(x, low ? &p.tm_t[s.seg] : &p.tm_x, c, 0, &full[slot]);
+                        if (pass == 1)
+                            for (int k = 0; k <= two; ++k)
+                                tma_load_2d(st + k * block_bytes + kWBytes, low ? &p.tm_t[s.seg] : &p.tm_x, (blk + k) * step, 0, &full[slot]);
                         if (++slot == stages) slot = 0, ph ^= 1u;
                     }
                     if (pass == 0 && i >= head) break;
@@ -218,12 +224,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
                 tc_fence_after();
                 uint32_t acc = 0, acc_lr = 0;
                 for (int b = s.u0; b < s.u1 && ok; ++b) {
-                    const bool low = b >= sg.nkb;
+                    const bool low = b >= sg.kpairs;
                     if (low && acc_lr == 0 && count >= 1) {  // the only U T accumulator: read by the segment before
                         ok = thread_wait(&acc_empty[set ^ 1u], ((count - 1) >> 1) & 1u, p, abort_flag);
                         if (!ok) break;
                     }
-                    if (!low && (b == s.u0 || (b & 3) == 0)) {
+                    if (!low && (b == s.u0 || (b & 1) == 0)) {
                         ++chunk;
                         ok = thread_wait(&sf_full[chunk & 1u], ((chunk - 1) >> 1) & 1u, p, abort_flag);
                         if (!ok) break;
@@ -237,20 +243,28 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t da = da0 + slot * (stage_bytes >> 4), db = db0 + slot * (stage_bytes >> 4);
+                    const uint64_t next = block_bytes >> 4;
                     if (low) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             tc_mma_f16(tmem + d_col, da + 2 * k, db + 2 * k, idesc_lr, acc_lr);
                             acc_lr = 1;
                         }
+                        if (2 * (b - sg.kpairs) + 1 < sg.lr)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) tc_mma_f16(tmem + d_col, da + next + 2 * k, db + next + 2 * k, idesc_lr, 1);
                     } else {
-                        const uint32_t sf = (uint32_t)b & 3u, c = tmem + sf_col + (chunk & 1u) * 8;
-                        const uint32_t idesc = idesc0 + sf * ((1u << 4) | (1u << 29));
+                        const uint32_t c = tmem + sf_col + (chunk & 1u) * 8, step = (1u << 4) | (1u << 29);
+                        const uint32_t idesc = idesc0 + (b & 1) * 2 * step;  // blocks 2b, 2b + 1 of the chunk's four
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             mma_mxf8(d_main, da + 2 * k, db + 2 * k, idesc, c, c + 4, acc);
                             acc = 1;
                         }
+                        if (2 * b + 1 < sg.nkb)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_mxf8(d_main, da + next + 2 * k, db + next + 2 * k, idesc + step, c, c + 4, 1);
                     }
                     tc_commit(&empty[slot]);
                     if (++slot == stages) slot = 0, ph ^= 1u;
@@ -270,9 +284,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
             const Segment s = segment_at(p, u, end);
             const Fp8StreamSeg &sg = p.seg[s.seg];
             const uint8_t *wrow = sg.w_scales + (size_t)s.tile * p.pitch;
-            for (int b = s.u0; b < min(s.u1, sg.nkb); b = (b & ~3) + 4) {
+            for (int b = s.u0; b < min(s.u1, sg.kpairs); b = (b & ~1) + 2) {
                 ++chunk;
-                const int q = b >> 2;
+                const int q = b >> 1;
                 const uint32_t ww = __ldg(reinterpret_cast<const uint32_t *>(wrow + 4 * q));
                 uint32_t xw[4];
 #pragma unroll
@@ -305,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
             const Fp8StreamSeg &sg = p.seg[s.seg];
             const uint32_t set = count & 1u;
             const bool whole = s.u0 == 0 && s.u1 == s.nu;
-            const bool has_z = s.u0 < sg.nkb, has_d = s.u1 > sg.nkb;
+            const bool has_z = s.u0 < sg.kpairs, has_d = s.u1 > sg.kpairs;
             bool ok = thread_wait(&acc_full[set], (count >> 1) & 1u, p, abort_flag);
             {
                 // the four warps meet below: they go on, or stop, together
@@ -386,10 +400,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
     }
 }
 
+static int fp8_stream_stage(const Fp8StreamParams &p) { return 2 * ((int)kWBytes + p.Mp * 128); }
+
 // CTAs and the cut of the list.  Cutting at tiles leaves SMs idle when the
-// tiles are few; cutting evenly costs an exchange, about as long as ten blocks
-// take one SM whose loads have the memory to themselves (about 250 cycles per
-// block; 700 when all 148 SMs stream).
+// tiles are few; cutting evenly costs an exchange, about as long as five units
+// take one SM whose loads have the memory to themselves (about 500 cycles per
+// unit; 1400 when all 148 SMs stream).
 void plan_fp8_stream(Fp8StreamParams &p) {
     constexpr int num_sms = kFp8StreamMaxGrid;
     long long units = 0;
@@ -398,6 +414,8 @@ void plan_fp8_stream(Fp8StreamParams &p) {
         Fp8StreamSeg &sg = p.seg[i];
         sg.unit_begin = units;
         sg.tile_begin = tiles;
+        sg.kpairs = (sg.nkb + 1) / 2;
+        sg.units = sg.kpairs + (sg.lr + 1) / 2;
         const int t = (sg.N + 127) / 128;
         tiles += t;
         units += (long long)t * sg.units;
@@ -406,21 +424,21 @@ void plan_fp8_stream(Fp8StreamParams &p) {
     p.units = units;
     p.tiles = tiles;
     const int by_tile = std::min(tiles, num_sms), even = (int)std::min<long long>(units, num_sms);
-    auto block = [&](int ctas) { return std::max(250.0, 700.0 * ctas / num_sms); };
+    auto block = [&](int ctas) { return std::max(500.0, 1400.0 * ctas / num_sms); };
     const double cost_tile = (double)((tiles + by_tile - 1) / by_tile) * longest * block(by_tile);
     const double cost_even = (double)((units + even - 1) / even) * block(even) + 2500;
     p.by_tile = cost_tile <= cost_even;
     p.grid = p.by_tile ? by_tile : even;
     p.Mp = (p.M + 15) / 16 * 16;
-    const int stage = (int)kWBytes + p.Mp * 128;
-    p.stages = std::min(12, (200 * 1024) / stage);
+    // up to 32 tokens 150 KB hold enough in flight and leave room for the rank-r kernel beside
+    p.stages = std::min(6, ((p.Mp <= 32 ? 150 : 200) * 1024) / fp8_stream_stage(p));
 }
 
 size_t fp8_stream_part_floats(const Fp8StreamParams &p) { return p.by_tile ? 0 : (size_t)p.grid * 2 * p.Mp * 128; }
 
 cudaError_t launch_fp8_stream(const Fp8StreamParams &p, cudaStream_t stream) {
     if (p.units == 0) return cudaSuccess;
-    const size_t smem = 1024 + (size_t)p.stages * (kWBytes + p.Mp * 128) + 2 * kSfBytes + (2 * p.stages + 9) * 8 + 16;
+    const size_t smem = 1024 + (size_t)p.stages * fp8_stream_stage(p) + 2 * kSfBytes + (2 * p.stages + 9) * 8 + 16;
     if (p.M < 1 || p.M > kFp8StreamMaxM || smem > 227 * 1024) return cudaErrorInvalidValue;
     static std::atomic<bool> done[64] = {};
     int dev = 0;
