@@ -232,42 +232,57 @@ def fp8_scale_pitch(cols: int) -> int:
     return 4 * ((cols + 511) // 512)
 
 
-@contextlib.contextmanager
-def _launch_on(device, stream):
+class _On:
     """Makes `device` current and, when a stream (torch stream or raw handle)
     is given, that stream too, so that what the call allocates belongs to the
-    stream it runs on.  Yields the stream's handle."""
-    import torch
+    stream it runs on.  Gives the stream's handle."""
 
-    with contextlib.ExitStack() as stack:
-        if device.index != torch.cuda.current_device():
-            stack.enter_context(torch.cuda.device(device))
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            elif stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-            stack.enter_context(torch.cuda.stream(stream))
-        yield torch.cuda.current_stream().cuda_stream
+    __slots__ = ("device", "stream", "stack")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.stack = device, stream, None
+
+    def __enter__(self):
+        import torch
+
+        device, stream = self.device, self.stream
+        if stream is not None or device.index != torch.cuda.current_device():
+            with contextlib.ExitStack() as stack:
+                stack.enter_context(torch.cuda.device(device))
+                if stream is not None:
+                    if isinstance(stream, int):
+                        stream = torch.cuda.ExternalStream(stream, device=device)
+                    elif stream.device != device:
+                        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+                    stack.enter_context(torch.cuda.stream(stream))
+                self.stack = stack.pop_all()
+        return torch.cuda.current_stream(device).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.stack is not None:
+            self.stack.close()
 
 
-def _dev_ptrs(device, *checks):
-    """_dev_ptr of each (tensor, dtype, name, shape), all on `device`."""
-    ptrs = []
-    for t, dtype, name, shape in checks:
-        ptrs.append(_dev_ptr(t, dtype, name, shape))
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return ptrs
+def _ptr_on(device, t, dtype, name, shape):
+    """The address of `t`, a contiguous `dtype` tensor of `shape` on `device`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev_ptr(t, dtype, name, shape)  # says what is wrong
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _need_cuda(t, name, dims=2):
+def _need_cuda(t, name):
+    """The device of a CUDA matrix."""
     import torch
 
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
+    return t.device
 
 
 def _workspace(nbytes, device):
@@ -287,22 +302,24 @@ def quantize_fp8(a, block_rows=1, codes=None, scales=None, stream=None):
     uint8, scales ceil(R / block_rows) x fp8_scale_pitch(C) uint8)."""
     import torch
 
-    _need_cuda(a, "a")
-    if a.dtype not in (torch.bfloat16, torch.float32):
+    dev = _need_cuda(a, "a")
+    f32 = a.dtype is torch.float32
+    if not f32 and a.dtype is not torch.bfloat16:
         raise TypeError(f"a must be bfloat16 or float32, got {a.dtype}")
     if block_rows not in (1, 128):
         raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
     R, C = a.shape
     shape = (-(-R // block_rows), fp8_scale_pitch(C))
-    with _launch_on(a.device, stream) as handle:
+    u8 = torch.uint8
+    with _On(dev, stream) as handle:
         if codes is None:
-            codes = torch.empty(R, C, dtype=torch.uint8, device=a.device)
+            codes = torch.empty((R, C), dtype=u8, device=dev)
         if scales is None:
-            scales = torch.empty(shape, dtype=torch.uint8, device=a.device)
-        ap, cp, sp = _dev_ptrs(a.device, (a, a.dtype, "a", None), (codes, torch.uint8, "codes", (R, C)),
-                               (scales, torch.uint8, "scales", shape))
-        _check(lib().wl_quantize_fp8(ap, int(a.dtype == torch.float32), R, C, block_rows, cp, sp, handle),
-               "wl_quantize_fp8")
+            scales = torch.empty(shape, dtype=u8, device=dev)
+        code = lib().wl_quantize_fp8(_ptr_on(dev, a, a.dtype, "a", a.shape), f32, R, C, block_rows,
+                                     _ptr_on(dev, codes, u8, "codes", (R, C)),
+                                     _ptr_on(dev, scales, u8, "scales", shape), handle)
+    _check(code, "wl_quantize_fp8")
     return codes, scales
 
 
@@ -313,19 +330,20 @@ def matmul_fp8(a, b, y=None, stream=None):
     import torch
 
     (ac, asc), (bc, bsc) = a, b
-    _need_cuda(ac, "a codes")
+    dev = _need_cuda(ac, "a codes")
     _need_cuda(bc, "b codes")
-    (M, K), N, dev = ac.shape, bc.shape[0], ac.device
-    pitch = fp8_scale_pitch(K)
-    with _launch_on(dev, stream) as handle:
+    (M, K), N = ac.shape, bc.shape[0]
+    pitch, u8, bf16 = fp8_scale_pitch(K), torch.uint8, torch.bfloat16
+    with _On(dev, stream) as handle:
         if y is None:
-            y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
-        ptrs = _dev_ptrs(dev, (ac, torch.uint8, "a codes", (M, K)), (asc, torch.uint8, "a scales", (M, pitch)),
-                         (bc, torch.uint8, "b codes", (N, K)),
-                         (bsc, torch.uint8, "b scales", (-(-N // 128), pitch)), (y, torch.bfloat16, "y", (M, N)))
+            y = torch.empty((M, N), dtype=bf16, device=dev)
         n = lib().wl_matmul_fp8_workspace(M, N, K)
         ws = _workspace(n, dev)
-        _check(lib().wl_matmul_fp8(*ptrs, M, N, K, _ptr(ws), n, handle), "wl_matmul_fp8")
+        code = lib().wl_matmul_fp8(_ptr_on(dev, ac, u8, "a codes", (M, K)), _ptr_on(dev, asc, u8, "a scales", (M, pitch)),
+                                   _ptr_on(dev, bc, u8, "b codes", (N, K)),
+                                   _ptr_on(dev, bsc, u8, "b scales", (-(-N // 128), pitch)),
+                                   _ptr_on(dev, y, bf16, "y", (M, N)), M, N, K, _ptr(ws), n, handle)
+    _check(code, "wl_matmul_fp8")
     return y
 
 
@@ -341,36 +359,37 @@ class Fp8Checkpoint:
 
 
 def _weight_fp8(dev, codes, scales, s, U, V, K):
-    """(codes, scales, s, U, V) pointers, N and r of one 8-bit projection."""
+    """Pointers (codes, scales, s, U, V), N and r of one 8-bit projection."""
     import torch
 
-    _need_cuda(codes, "codes")
-    N = codes.shape[0]
-    r = 0 if U is None else U.shape[1]
     if (U is None) != (V is None):
         raise ValueError("U and V must both be given or both be None")
-    if r == 0:
-        U = V = None
-    return _dev_ptrs(dev, (codes, torch.uint8, "codes", (N, K)),
-                     (scales, torch.uint8, "scales", (-(-N // 128), fp8_scale_pitch(K))),
-                     (s, torch.float32, "s", (N,)), (U, torch.bfloat16, "U", (N, r)),
-                     (V, torch.bfloat16, "V", (K, r))), N, r
+    _need_cuda(codes, "codes")
+    N, u8, bf16 = codes.shape[0], torch.uint8, torch.bfloat16
+    r = 0
+    up = vp = None
+    if U is not None:
+        _need_cuda(U, "U")
+        r = U.shape[1]
+        up, vp = _ptr_on(dev, U, bf16, "U", (N, r)), _ptr_on(dev, V, bf16, "V", (K, r))
+    return (_ptr_on(dev, codes, u8, "codes", (N, K)),
+            _ptr_on(dev, scales, u8, "scales", (-(-N // 128), fp8_scale_pitch(K))),
+            _ptr_on(dev, s, torch.float32, "s", (N,)), up if r else None, vp if r else None), N, r
 
 
 def _forward_fp8_args(x, projs, ys, T):
     import torch
 
-    _need_cuda(x, "x")
-    (M, K), dev = x.shape, x.device
+    dev, bf16 = _need_cuda(x, "x"), torch.bfloat16
+    M, K = x.shape
     if len(ys) != len(projs):
         raise ValueError(f"{len(projs)} projections, {len(ys)} outputs")
     arr = (_ProjFp8 * max(len(projs), 1))()
     for i, (p, y) in enumerate(zip(projs, ys)):
         w, N, r = _weight_fp8(dev, *p, K)
-        yp, tp = _dev_ptrs(dev, (y, torch.bfloat16, "y", (M, N)),
-                           (None if T is None else T[i], torch.bfloat16, "T", (M, r)))
-        arr[i] = _ProjFp8(*w, yp, tp, N, r)
-    return _dev_ptrs(dev, (x, torch.bfloat16, "x", (M, K)))[0], M, K, arr
+        tp = None if T is None or not r else _ptr_on(dev, T[i], bf16, "T", (M, r))
+        arr[i] = _ProjFp8(*w, _ptr_on(dev, y, bf16, "y", (M, N)), tp, N, r)
+    return _ptr_on(dev, x, bf16, "x", (M, K)), M, K, arr
 
 
 def stacked_forward_fp8(x, projs, ys=None, checkpoint=False, stream=None):
@@ -381,23 +400,23 @@ def stacked_forward_fp8(x, projs, ys=None, checkpoint=False, stream=None):
     bf16); with checkpoint=True, (ys, Fp8Checkpoint) for stacked_backward_fp8."""
     import torch
 
-    _need_cuda(x, "x")
-    (M, K), dev = x.shape, x.device
-    with _launch_on(dev, stream) as handle:
+    dev = _need_cuda(x, "x")
+    M, K = x.shape
+    with _On(dev, stream) as handle:
         if ys is None:
-            ys = [torch.empty(M, p[0].shape[0], dtype=torch.bfloat16, device=dev) for p in projs]
+            ys = [torch.empty((M, p[0].shape[0]), dtype=torch.bfloat16, device=dev) for p in projs]
         ckpt = None
         if checkpoint:
-            ckpt = Fp8Checkpoint(torch.empty(M, K, dtype=torch.uint8, device=dev),
-                                 torch.empty(M, fp8_scale_pitch(K), dtype=torch.uint8, device=dev),
-                                 [torch.empty(M, p[3].shape[1], dtype=torch.bfloat16, device=dev)
+            ckpt = Fp8Checkpoint(torch.empty((M, K), dtype=torch.uint8, device=dev),
+                                 torch.empty((M, fp8_scale_pitch(K)), dtype=torch.uint8, device=dev),
+                                 [torch.empty((M, p[3].shape[1]), dtype=torch.bfloat16, device=dev)
                                   if p[3] is not None and p[3].shape[1] else None for p in projs])
         xp, M, K, arr = _forward_fp8_args(x, projs, ys, ckpt.T if ckpt else None)
         n = lib().wl_stacked_forward_fp8_workspace(M, K, arr, len(projs))
         ws = _workspace(n, dev)
-        _check(lib().wl_stacked_forward_fp8(xp, M, K, arr, len(projs), _ptr(ckpt.codes) if ckpt else None,
-                                            _ptr(ckpt.scales) if ckpt else None, _ptr(ws), n, handle),
-               "wl_stacked_forward_fp8")
+        code = lib().wl_stacked_forward_fp8(xp, M, K, arr, len(projs), _ptr(ckpt.codes) if ckpt else None,
+                                            _ptr(ckpt.scales) if ckpt else None, _ptr(ws), n, handle)
+    _check(code, "wl_stacked_forward_fp8")
     return (ys, ckpt) if checkpoint else ys
 
 
@@ -412,16 +431,16 @@ class PreparedForwardFp8:
     def __init__(self, x, projs, ys=None):
         import torch
 
-        _need_cuda(x, "x")
-        with _launch_on(x.device, None):
+        dev = _need_cuda(x, "x")
+        with _On(dev, None):
             if ys is None:
-                ys = [torch.empty(x.shape[0], p[0].shape[0], dtype=torch.bfloat16, device=x.device) for p in projs]
+                ys = [torch.empty((x.shape[0], p[0].shape[0]), dtype=torch.bfloat16, device=dev) for p in projs]
             xp, M, K, arr = _forward_fp8_args(x, projs, ys, None)
             n = lib().wl_stacked_forward_fp8_workspace(M, K, arr, len(projs))
-            ws = _workspace(n, x.device)
+            ws = _workspace(n, dev)
         self.ys = ys
         self._keep = (x, projs, ws)
-        self._device = x.device
+        self._device = dev
         self._args = (xp, M, K, arr, len(projs), None, None, _ptr(ws), n)
         self._fn = lib().wl_stacked_forward_fp8
 
@@ -451,32 +470,32 @@ def stacked_backward_fp8(ckpt, dys, projs, need_dx=True, need_params=True, strea
     need_params).  The shared W0 has no gradient."""
     import torch
 
-    _need_cuda(ckpt.codes, "checkpoint codes")
-    (M, K), dev = ckpt.codes.shape, ckpt.codes.device
+    dev = _need_cuda(ckpt.codes, "checkpoint codes")
+    M, K = ckpt.codes.shape
     if not len(projs) == len(dys) == len(ckpt.T):
         raise ValueError(f"{len(projs)} projections, {len(dys)} gradients, {len(ckpt.T)} T")
-    with _launch_on(dev, stream) as handle:
-        xc, xs = _dev_ptrs(dev, (ckpt.codes, torch.uint8, "checkpoint codes", (M, K)),
-                           (ckpt.scales, torch.uint8, "checkpoint scales", (M, fp8_scale_pitch(K))))
+    u8, bf16 = torch.uint8, torch.bfloat16
+    with _On(dev, stream) as handle:
+        xc = _ptr_on(dev, ckpt.codes, u8, "checkpoint codes", (M, K))
+        xs = _ptr_on(dev, ckpt.scales, u8, "checkpoint scales", (M, fp8_scale_pitch(K)))
         arr = (_GradFp8 * max(len(projs), 1))()
         per = []
         for i, (p, dy, T) in enumerate(zip(projs, dys, ckpt.T)):
             w, N, r = _weight_fp8(dev, *p, K)
             ds = dU = dV = None
             if need_params:
-                ds = torch.empty(N, dtype=torch.float32, device=dev)
+                ds = torch.empty((N,), dtype=torch.float32, device=dev)
                 if r:
-                    dU = torch.empty(N, r, dtype=torch.bfloat16, device=dev)
-                    dV = torch.empty(K, r, dtype=torch.bfloat16, device=dev)
+                    dU = torch.empty((N, r), dtype=bf16, device=dev)
+                    dV = torch.empty((K, r), dtype=bf16, device=dev)
             per.append((ds, dU, dV))
-            io = _dev_ptrs(dev, (T if r else None, torch.bfloat16, "T", (M, r)),
-                           (dy, torch.bfloat16, "dy", (M, N)))
-            arr[i] = _GradFp8(*w, *io, _ptr(ds), _ptr(dU), _ptr(dV), N, r)
-        dx = torch.empty(M, K, dtype=torch.bfloat16, device=dev) if need_dx else None
+            arr[i] = _GradFp8(*w, _ptr_on(dev, T, bf16, "T", (M, r)) if r else None, _ptr_on(dev, dy, bf16, "dy", (M, N)),
+                              _ptr(ds), _ptr(dU), _ptr(dV), N, r)
+        dx = torch.empty((M, K), dtype=bf16, device=dev) if need_dx else None
         n = lib().wl_stacked_backward_fp8_workspace(M, K, arr, len(projs))
         ws = _workspace(n, dev)
-        _check(lib().wl_stacked_backward_fp8(xc, xs, M, K, arr, len(projs), _ptr(dx), _ptr(ws), n, handle),
-               "wl_stacked_backward_fp8")
+        code = lib().wl_stacked_backward_fp8(xc, xs, M, K, arr, len(projs), _ptr(dx), _ptr(ws), n, handle)
+    _check(code, "wl_stacked_backward_fp8")
     return dx, per
 
 

@@ -62,9 +62,20 @@ struct LowrankJob {
     int tile_begin;
 };
 
+// Rows mode, I <= 128: the launch also quantises its A (rows x cols, bf16,
+// dense) in 1 x 128 blocks and clears n_zero words; a == nullptr: nothing.
+struct LowrankQuant {
+    const __nv_bfloat16 *a;
+    uint8_t *codes, *scales;
+    int rows, cols;
+    unsigned int *zero;
+    int n_zero;
+};
+
 struct LowrankParams {
     LowrankJob job[kMaxSeg];
     int njobs;
+    LowrankQuant quant;
     int BN, split, stages, a_bytes, stage_bytes, tmem_cols;  // filled by the launcher
     int *status;
     unsigned long long timeout_ns;

@@ -121,9 +121,10 @@ wl_status forward_check(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs
 }
 
 // Tensor maps of one contraction part.  b_rows x b_cols: the codes of B as
-// stored; lr_rows: rows of U (output columns of the product).
+// stored; lr_rows: rows of U (output columns of the product); same_a: A is the
+// previous part's.
 wl_status set_part(Fp8GemmParams &g, int i, const Fp8Mat &A, int M, int a_cols, const Fp8Mat &B, int b_rows, int b_cols,
-                   bool transposed, const __nv_bfloat16 *T, const __nv_bfloat16 *U, int r, int lr_rows) {
+                   bool transposed, const __nv_bfloat16 *T, const __nv_bfloat16 *U, int r, int lr_rows, bool same_a = false) {
     Fp8Part &pt = g.part[i];
     pt.a_scales = A.scales;
     pt.a_pitch = A.pitch;
@@ -131,7 +132,11 @@ wl_status set_part(Fp8GemmParams &g, int i, const Fp8Mat &A, int M, int a_cols, 
     pt.b_pitch = B.pitch;
     pt.nkb = (a_cols + kFp8Block - 1) / kFp8Block;
     pt.lr = (r + 63) / 64;
-    wl_status st = encode_map_2d_u8(&g.tm_a[i], A.codes, a_cols, M, A.ld, 128, 128);
+    wl_status st = WL_OK;
+    if (same_a)
+        g.tm_a[i] = g.tm_a[i - 1];
+    else
+        st = encode_map_2d_u8(&g.tm_a[i], A.codes, a_cols, M, A.ld, 128, 128);
     if (st == WL_OK) st = encode_map_2d_u8(&g.tm_b[i], B.codes, b_cols, b_rows, B.ld, 128, transposed ? 128 : kFp8BN / 2);
     if (st == WL_OK && r > 0) st = encode_map_2d(&g.tm_t[i], T, r, M, r, 64, 128);
     if (st == WL_OK && r > 0) st = encode_map_2d(&g.tm_u[i], U, r, lr_rows, r, 64, kFp8BN / 2);
@@ -173,7 +178,7 @@ void init_lowrank(LowrankParams &p, const Device &dev) {
 // Adds out = A B (+ what its rounding left in out_low).  A: I x K (rows) or
 // K x I (cols), rows lda elements apart; B: K x r.
 wl_status add_lowrank(LowrankParams &p, LowrankMode mode, const __nv_bfloat16 *A, long long lda, int I, int K,
-                      const __nv_bfloat16 *B, int r, __nv_bfloat16 *out, __nv_bfloat16 *out_low) {
+                      const __nv_bfloat16 *B, int r, __nv_bfloat16 *out, __nv_bfloat16 *out_low, bool same_a = false) {
     LowrankJob &j = p.job[p.njobs++];
     j.I = I;
     j.K = K;
@@ -182,8 +187,12 @@ wl_status add_lowrank(LowrankParams &p, LowrankMode mode, const __nv_bfloat16 *A
     j.out = out;
     j.out_low = out_low;
     // rows that do not exist need not be loaded: each fills its own row of the sums
-    wl_status st = mode == kLowrankRows ? encode_map_2d(&j.tm_a, A, K, I, lda, 64, lowrank_a_rows(I))
-                                        : encode_map_2d(&j.tm_a, A, I, K, lda, 64, 64);
+    wl_status st = WL_OK;
+    if (same_a)
+        j.tm_a = p.job[p.njobs - 2].tm_a;
+    else
+        st = mode == kLowrankRows ? encode_map_2d(&j.tm_a, A, K, I, lda, 64, lowrank_a_rows(I))
+                                  : encode_map_2d(&j.tm_a, A, I, K, lda, 64, 64);
     return st == WL_OK ? encode_map_2d(&j.tm_b, B, r, K, r, 64, 64) : st;
 }
 
@@ -237,11 +246,8 @@ wl_status forward_run(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, 
                       uint8_t *x_scales, const ForwardLayout &l, const Device &dev, cudaStream_t stream) {
     const Fp8Mat X{x_codes ? x_codes : l.codes, x_scales ? x_scales : l.scales, K, fp8_pitch(K)};
     const bool few = M <= kFp8StreamMaxM;
-    int tiles = 0;
+    int tiles = 0;  // counters of the few-token kernel
     for (int i = 0; i < P; ++i) tiles += (projs[i].N + 127) / 128;
-    if (launch_fp8_quantize_rows(x, WL_BF16, K, M, K, nullptr, const_cast<uint8_t *>(X.codes), K,
-                                 const_cast<uint8_t *>(X.scales), l.counters, few ? tiles : 0, stream) != cudaSuccess)
-        return WL_ERR_CUDA;
     wl_status st;
     LowrankParams lp;
     init_lowrank(lp, dev);
@@ -250,9 +256,15 @@ wl_status forward_run(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, 
         const wl_proj_fp8 &q = projs[i];
         T[i] = q.T ? bf16(q.T) : l.T[i];
         if (q.r > 0 && (q.T || q.N > 0) &&
-            (st = add_lowrank(lp, kLowrankRows, bf16(x), K, M, K, bf16(q.V), q.r, T[i], nullptr)) != WL_OK)
+            (st = add_lowrank(lp, kLowrankRows, bf16(x), K, M, K, bf16(q.V), q.r, T[i], nullptr, lp.njobs > 0)) != WL_OK)
             return st;
     }
+    uint8_t *codes = const_cast<uint8_t *>(X.codes), *scales = const_cast<uint8_t *>(X.scales);
+    if (few && lp.njobs > 0)  // one launch less in a decode step
+        lp.quant = LowrankQuant{bf16(x), codes, scales, M, K, l.counters, tiles};
+    else if (launch_fp8_quantize_rows(x, WL_BF16, K, M, K, nullptr, codes, K, scales, l.counters, few ? tiles : 0,
+                                      stream) != cudaSuccess)
+        return WL_ERR_CUDA;
     if (launch_fp8_lowrank(lp, kLowrankRows, dev.sms, stream) != cudaSuccess) return WL_ERR_CUDA;
     if (few) return run_stream(X, M, K, projs, T, P, l.parts, l.counters, true, dev, stream);
     Fp8GemmParams g;
@@ -261,7 +273,7 @@ wl_status forward_run(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, 
         const wl_proj_fp8 &q = projs[i];
         if (q.N == 0) continue;
         const int k = g.nout;
-        st = set_part(g, k, X, M, K, Fp8Mat{q.codes, q.scales, K, fp8_pitch(K)}, q.N, K, false, T[i], bf16(q.U), q.r, q.N);
+        st = set_part(g, k, X, M, K, Fp8Mat{q.codes, q.scales, K, fp8_pitch(K)}, q.N, K, false, T[i], bf16(q.U), q.r, q.N, k > 0);
         if (st != WL_OK) return st;
         Fp8Out &o = add_out(g, q.N, k, 1);
         o.s = q.s;
@@ -375,7 +387,7 @@ wl_status backward_run(const uint8_t *x_codes, const uint8_t *x_scales, int M, i
         }
         if (q.ds && K > 0) {
             const int k = gs.nout;
-            if ((st = set_part(gs, k, X, M, K, W, q.N, K, false, nullptr, nullptr, 0, 0)) != WL_OK) return st;
+            if ((st = set_part(gs, k, X, M, K, W, q.N, K, false, nullptr, nullptr, 0, 0, k > 0)) != WL_OK) return st;
             Fp8Out &o = add_out(gs, q.N, k, 1);
             o.dy = bf16(q.dy);
             o.sums = l.sums[i];

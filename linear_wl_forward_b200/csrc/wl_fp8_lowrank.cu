@@ -31,6 +31,7 @@
 
 #include "wl_common.cuh"
 #include "wl_fp8.h"
+#include "wl_fp8_encode.cuh"
 
 namespace wl {
 
@@ -105,6 +106,40 @@ __device__ __forceinline__ void write8(const LowrankJob &jb, int i, int j, const
     }
 }
 
+// Columns [c0, c1) of the rows whose index is `part` modulo `parts`, by 128
+// threads: eight lanes share a block.  c0 is a multiple of 128.
+__device__ __forceinline__ void quantize_range(const LowrankQuant &q, int c0, int c1, int part, int parts, int tid) {
+    const int pitch = WL_FP8_SCALE_PITCH(q.cols), blocks = (c1 - c0 + 127) / 128;
+    const int rows = part < q.rows ? (q.rows - part + parts - 1) / parts : 0;
+    const int total = rows * blocks, group = tid >> 3;
+    for (int t0 = 0; t0 < total; t0 += 32) {  // 16 groups, two blocks each in flight
+        float v[2][16];
+        int row[2], c[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int t = t0 + k * 16 + group;
+            row[k] = t < total ? part + t / blocks * parts : -1;
+            c[k] = c0 + t % blocks * 128 + (tid & 7) * 16;
+            load16(q.a + (size_t)max(row[k], 0) * q.cols + c[k], row[k] >= 0 ? q.cols - c[k] : 0, true, v[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float m = amax16(v[k]);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (row[k] < 0) continue;
+            const int E = scale_exponent(m);
+            if (c[k] < q.cols)
+                *reinterpret_cast<uint4 *>(q.codes + (size_t)row[k] * q.cols + c[k]) = codes16(v[k], inverse_scale(E));
+            uint8_t *s = q.scales + (size_t)row[k] * pitch + (c[k] >> 7);
+            if ((tid & 7) == 0) *s = (uint8_t)(E + 127);
+            // bytes behind the last block
+            if ((c[k] >> 7) == (q.cols - 1) >> 7)
+                for (int b = (tid & 7) + 1; (c[k] >> 7) + b < pitch; b += 8) s[b] = 127;
+        }
+    }
+}
+
 }  // namespace
 
 template <int kMode>
@@ -129,7 +164,9 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
     const int i_tiles = (jb.I + 127) / 128;
     const int i0 = (local % i_tiles) * 128, j0 = (local / i_tiles) * p.BN;
     const int width = min(p.BN, jb.r - j0), n_mma = (width + 15) & ~15, boxes = (width + 63) / 64;
-    const int per = (jb.kb + S - 1) / S;
+    const bool quant = kMode == kLowrankRows && p.quant.a != nullptr;
+    int per = (jb.kb + S - 1) / S;
+    if (quant) per = (per + 1) & ~1;  // whole 128-column blocks
     const int kb0 = min((int)rank * per, jb.kb), kb1 = min(kb0 + per, jb.kb);
     const int terms = kCodes ? 2 : 1;  // B high, B low
 
@@ -153,6 +190,8 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
     // Dependents start once everything before this kernel is complete.
     pdl_wait_primary();
     pdl_launch_dependents();
+    if (kMode == kLowrankRows && p.quant.a)
+        for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < p.quant.n_zero; i += gridDim.x * blockDim.x) p.quant.zero[i] = 0;
 
     const uint32_t a_bytes = kMode == kLowrankRows ? (uint32_t)p.a_bytes : kATile;
     const uint32_t b_off = a_bytes + (kCodes ? kCodeTile : 0);
@@ -271,6 +310,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
                 if (++slot == (uint32_t)p.stages) slot = 0, ph ^= 1u;
             }
         }
+        if (quant) quantize_range(p.quant, kb0 * 64, min(kb1 * 64, p.quant.cols), unit, gridDim.x / S, tid);
         // MMAs done.  A CTA with an empty range of the contraction has no sums.
         if (ok && warp < 6 && kb1 > kb0) ok = all_wait(done, 0, p);
         tc_fence_after();
@@ -288,7 +328,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
                 }
                 if (S == 1) {
                     if (c < width) write8(jb, i0 + row, j0 + c, v);
-                } else {
+                } else if (i0 + row < jb.I) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) buf[(c + k) * 128 + row] = v[k];
                 }
@@ -298,14 +338,39 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
         __syncwarp();
         cluster_barrier();  // every CTA's sums are in its shared memory
         if (warp >= 2 && warp < 6 && ok) {
-            const int row = (warp & 3) * 32 + lane;
-            for (int c = (int)rank * 8; c < width; c += 8 * S) {
-                float v[8] = {};
-                for (int s = 0; s < S; ++s)
+            const int tid_epilogue = threadIdx.x - 64;
+            // groups of eight columns go round the ranks; with few rows several
+            // threads take the columns of one row
+            const int rows = min(128, jb.I - i0);
+            if (rows > 32) {
+                const int row = tid_epilogue;
+                for (int c = (int)rank * 8; c < width; c += 8 * S) {
+                    float v[8] = {};
+                    if (row < rows)
+                        for (int s = 0; s < S; ++s)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        v[k] += ld_cluster(smem_addr(base) + (uint32_t)((c + k) * 128 + row) * 4, s);
-                write8(jb, i0 + row, j0 + c, v);
+                            for (int k = 0; k < 8; ++k)
+                                v[k] += ld_cluster(smem_addr(base) + (uint32_t)((c + k) * 128 + row) * 4, s);
+                    write8(jb, i0 + row, j0 + c, v);
+                }
+            } else {
+                const int groups = (width / 8 - (int)rank + S - 1) / S;
+                for (int t = tid_epilogue; t < rows * groups * 8; t += 128) {
+                    const int row = t % rows, c = ((int)rank + t / rows / 8 * S) * 8 + t / rows % 8;
+                    const uint32_t at = smem_addr(base) + (uint32_t)(c * 128 + row) * 4;
+                    float v = 0.f;
+                    for (int s0 = 0; s0 < S; s0 += 4) {
+                        float part[4];
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) part[s] = s0 + s < S ? ld_cluster(at, s0 + s) : 0.f;
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) v += part[s];
+                    }
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+                    const size_t o = (size_t)(i0 + row) * jb.r + j0 + c;
+                    jb.out[o] = hi;
+                    if (jb.out_low) jb.out_low[o] = __float2bfloat16_rn(v - __bfloat162float(hi));
+                }
             }
         }
         __syncwarp();
@@ -355,6 +420,7 @@ cudaError_t launch_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms, 
     int rows = 0;
     for (int i = 0; i < p.njobs; ++i) rows = std::max(rows, lowrank_a_rows(p.job[i].I));
     p.a_bytes = mode == kLowrankRows ? rows * 128 : (int)kATile;
+    if (p.quant.a && rows > 128) return cudaErrorInvalidValue;
     plan(p, terms, num_sms);
     int tiles = 0, widest = 0;
     for (int i = 0; i < p.njobs; ++i) {
