@@ -256,7 +256,8 @@ class _On:
                         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
                     stack.enter_context(torch.cuda.stream(stream))
                 self.stack = stack.pop_all()
-        return torch.cuda.current_stream(device).cuda_stream
+        # the handle alone: making a Stream object costs as much as the launch
+        return torch._C._cuda_getCurrentRawStream(device.index)
 
     def __exit__(self, *exc):
         if self.stack is not None:
@@ -450,7 +451,8 @@ class PreparedForwardFp8:
         if self._device.index != torch.cuda.current_device():
             with torch.cuda.device(self._device):
                 return self(stream)
-        _check(self._fn(*self._args, _stream_handle(stream)), "wl_stacked_forward_fp8")
+        handle = torch._C._cuda_getCurrentRawStream(self._device.index) if stream is None else _stream_handle(stream)
+        _check(self._fn(*self._args, handle), "wl_stacked_forward_fp8")
         return self.ys
 
 

@@ -24,66 +24,106 @@ __device__ __forceinline__ float finite_abs(float v) {
     return a <= 3.402823466e38f ? a : 0.f;  // false for infinities and NaN
 }
 
-// Two codes; an element that is not finite becomes the NaN code.
+// Two codes.  NaN gives the NaN code; infinities saturate here (codes16 sees to them).
 __device__ __forceinline__ uint32_t code_pair(float lo, float hi) {
     uint16_t c;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
-    uint32_t v = c;
-    if (isinf(lo)) v = (v & 0xFF00u) | 0x7Fu;
-    if (isinf(hi)) v = (v & 0x00FFu) | 0x7F00u;
-    return v;
+    return c;
 }
 
-// 16 consecutive elements as floats; `n` of them exist.
+// 16 consecutive elements as they are stored; `n` of them exist, the rest are 0.
+// `vec`: p is 16-byte aligned.
 template <typename T>
-__device__ __forceinline__ void load16(const T *p, int n, bool vec, float (&v)[16]);
+struct Raw16;
 
 template <>
-__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16 *p, int n, bool vec, float (&v)[16]) {
-    if (vec && n >= 16) {
-        const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+struct Raw16<__nv_bfloat16> {
+    uint32_t w[8];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, int n, bool vec) {
+        if (vec && n >= 16) {
+            const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        } else {
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[i] = (2 * i < n ? h[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)h[2 * i + 1] << 16 : 0u);
+        }
+    }
+    __device__ __forceinline__ void unpack(float (&v)[16]) const {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             v[2 * i] = bf16lo(w[i]);
             v[2 * i + 1] = bf16hi(w[i]);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = i < n ? __bfloat162float(p[i]) : 0.f;
     }
-}
+};
 
 template <>
-__device__ __forceinline__ void load16<float>(const float *p, int n, bool vec, float (&v)[16]) {
-    if (vec && n >= 16) {
+struct Raw16<float> {
+    float f[16];
+    __device__ __forceinline__ void load(const float *p, int n, bool vec) {
+        if (vec && n >= 16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 a = reinterpret_cast<const float4 *>(p)[i];
-            v[4 * i] = a.x;
-            v[4 * i + 1] = a.y;
-            v[4 * i + 2] = a.z;
-            v[4 * i + 3] = a.w;
+            for (int i = 0; i < 4; ++i) {
+                const float4 a = reinterpret_cast<const float4 *>(p)[i];
+                f[4 * i] = a.x, f[4 * i + 1] = a.y, f[4 * i + 2] = a.z, f[4 * i + 3] = a.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[i] = i < n ? p[i] : 0.f;
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = i < n ? p[i] : 0.f;
     }
+    __device__ __forceinline__ void unpack(float (&v)[16]) const {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = f[i];
+    }
+};
+
+// Largest magnitude, NaN left out, infinities not: one instruction per element.
+__device__ __forceinline__ float amax16(const float (&v)[16]) {
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(v[i]));
+    return a;
 }
 
-__device__ __forceinline__ float amax16(const float (&v)[16]) {
+// Largest finite magnitude: for blocks that amax16 found an infinity in.
+__device__ __forceinline__ float finite_amax16(const float (&v)[16]) {
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) a = fmaxf(a, finite_abs(v[i]));
     return a;
 }
 
-__device__ __forceinline__ uint4 codes16(const float (&v)[16], float inv) {
+// `infinities`: some element of the block is infinite; those get the NaN code.
+__device__ __forceinline__ uint4 codes16(const float (&v)[16], float inv, bool infinities) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         w[i] = code_pair(v[4 * i] * inv, v[4 * i + 1] * inv) | code_pair(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16;
+    if (infinities) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (isinf(v[i])) w[i >> 2] = (w[i >> 2] & ~(0xFFu << (i & 3) * 8)) | 0x7Fu << (i & 3) * 8;
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Maximum over the eight lanes that share a 1 x 128 block.
+__device__ __forceinline__ float max_of_8_lanes(float m) {
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+
+// The scale exponent of a 1 x 128 block held by eight lanes, and whether it
+// has infinities.  Called by whole warps.
+__device__ __forceinline__ int block_exponent(const float (&v)[16], bool &infinities) {
+    float m = max_of_8_lanes(amax16(v));
+    infinities = isinf(m);
+    if (__any_sync(0xffffffffu, infinities)) m = max_of_8_lanes(finite_amax16(v));
+    return scale_exponent(m);
 }
 
 }  // namespace wl

@@ -120,17 +120,17 @@ __device__ __forceinline__ void quantize_range(const LowrankQuant &q, int c0, in
             const int t = t0 + k * 16 + group;
             row[k] = t < total ? part + t / blocks * parts : -1;
             c[k] = c0 + t % blocks * 128 + (tid & 7) * 16;
-            load16(q.a + (size_t)max(row[k], 0) * q.cols + c[k], row[k] >= 0 ? q.cols - c[k] : 0, true, v[k]);
+            Raw16<__nv_bfloat16> raw;
+            raw.load(q.a + (size_t)max(row[k], 0) * q.cols + c[k], row[k] >= 0 ? q.cols - c[k] : 0, true);
+            raw.unpack(v[k]);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            float m = amax16(v[k]);
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            bool infinities;
+            const int E = block_exponent(v[k], infinities);
             if (row[k] < 0) continue;
-            const int E = scale_exponent(m);
             if (c[k] < q.cols)
-                *reinterpret_cast<uint4 *>(q.codes + (size_t)row[k] * q.cols + c[k]) = codes16(v[k], inverse_scale(E));
+                *reinterpret_cast<uint4 *>(q.codes + (size_t)row[k] * q.cols + c[k]) = codes16(v[k], inverse_scale(E), infinities);
             uint8_t *s = q.scales + (size_t)row[k] * pitch + (c[k] >> 7);
             if ((tid & 7) == 0) *s = (uint8_t)(E + 127);
             // bytes behind the last block

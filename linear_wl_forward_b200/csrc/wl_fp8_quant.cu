@@ -17,13 +17,13 @@ namespace wl {
 
 namespace {
 
-// One warp: 512 columns of kRows rows, 16 columns per lane, so eight lanes
-// share a block and the warp fills one word of scales per row.  With kRows = 4
-// a lane has eight 16-byte loads in flight and reads its column scales once
-// for four rows; single rows are for inputs too small to fill the GPU that way
-// (4096 x 16384 with column scales: 148 us with single rows, where the scales
-// are twice the data's loads).
-template <typename T, bool kColScale, int kRows>
+// One warp: 512 columns of one row, 16 per lane, so eight lanes share a block
+// and the warp fills one word of scales.  One row per warp: 4096 x 21504 bf16
+// take 46 us (5.8 TB/s), 86 with four rows, whose registers cost more warps
+// than their loads in flight give.  With column scales neighbouring warps take
+// neighbouring rows of the same columns, so the scales (twice the data's bytes
+// per element) come from L1.
+template <typename T, bool kColScale>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict__ a, long long lda, int rows, int cols,
                                                             int words, const float *__restrict__ colscale,
                                                             uint8_t *__restrict__ codes, long long ld_codes,
@@ -36,66 +36,77 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict_
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n_zero; i += (long long)gridDim.x * 256) zero[i] = 0;
     const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    if (w / words * kRows >= rows) return;
-    const int row0 = (int)(w / words) * kRows, q = (int)(w % words);
+    if (w >= (long long)rows * words) return;
+    const int row = kColScale ? (int)(w % rows) : (int)(w / words), q = kColScale ? (int)(w / rows) : (int)(w % words);
     const int c = q * 512 + lane * 16;
-    float v[kRows][16];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        const bool in = row0 + r < rows;
-        load16(a + (size_t)(in ? row0 + r : row0) * lda + c, in ? cols - c : 0, vec, v[r]);
-    }
+    Raw16<T> raw;
+    raw.load(a + (size_t)row * lda + c, cols - c, vec);
+    float v[16];
+    raw.unpack(v);
     if (kColScale) {
-        float s[16];
-        load16(colscale + c, cols - c, svec, s);
+        Raw16<float> s;
+        s.load(colscale + c, cols - c, svec);
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[r][i] *= s[i];
+        for (int i = 0; i < 16; ++i) v[i] *= s.f[i];
     }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        const size_t row = row0 + r;
-        float m = amax16(v[r]);
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int E = scale_exponent(m);
-        const uint32_t e = (uint32_t)(E + 127);
-        const uint32_t word = __shfl_sync(0xffffffffu, e, 0) | __shfl_sync(0xffffffffu, e, 8) << 8 |
-                              __shfl_sync(0xffffffffu, e, 16) << 16 | __shfl_sync(0xffffffffu, e, 24) << 24;
-        if ((int)row >= rows) continue;
-        if (c < ld_codes) *reinterpret_cast<uint4 *>(codes + row * ld_codes + c) = codes16(v[r], inverse_scale(E));
-        if (lane == 0) *reinterpret_cast<uint32_t *>(scales + (row * words + q) * 4) = word;
-    }
+    bool infinities;
+    const int E = block_exponent(v, infinities);
+    const uint32_t e = (uint32_t)(E + 127);
+    const uint32_t word = __shfl_sync(0xffffffffu, e, 0) | __shfl_sync(0xffffffffu, e, 8) << 8 |
+                          __shfl_sync(0xffffffffu, e, 16) << 16 | __shfl_sync(0xffffffffu, e, 24) << 24;
+    if (c < ld_codes) *reinterpret_cast<uint4 *>(codes + (size_t)row * ld_codes + c) = codes16(v, inverse_scale(E), infinities);
+    if (lane == 0) *reinterpret_cast<uint32_t *>(scales + ((size_t)row * words + q) * 4) = word;
 }
 
-// One CTA: a 128 x 128 block, 16 elements of four rows per thread.
-template <typename T>
-__global__ void __launch_bounds__(256) quantize_tiles_kernel(const T *__restrict__ a, int rows, int cols,
-                                                             uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
-                                                             int pitch) {
-    __shared__ float warp_max[8];
-    const int r0 = blockIdx.y * 128 + (threadIdx.x >> 3), c = blockIdx.x * 128 + (threadIdx.x & 7) * 16;
-    float v[4][16];
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 32 * i;
-        load16(a + (size_t)(r < rows ? r : 0) * cols + c, r < rows ? cols - c : 0, true, v[i]);
-        m = fmaxf(m, amax16(v[i]));
-    }
+__device__ __forceinline__ float block_max(float m, float *warp_max) {
+    __syncthreads();  // warp_max may still be read
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = fmaxf(m, warp_max[i]);
+    return m;
+}
+
+// One CTA: a 128 x 128 block, 16 elements of four rows per thread, kept as
+// they are stored so that more CTAs fit an SM.
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_tiles_kernel(const T *__restrict__ a, int rows, int cols,
+                                                             uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
+                                                             int pitch) {
+    __shared__ float warp_max[8];
+    const int r0 = blockIdx.y * 128 + (threadIdx.x >> 3), c = blockIdx.x * 128 + (threadIdx.x & 7) * 16;
+    Raw16<T> raw[4];
+    float v[16], m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 32 * i;
+        raw[i].load(a + (size_t)(r < rows ? r : 0) * cols + c, r < rows ? cols - c : 0, true);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        raw[i].unpack(v);
+        m = fmaxf(m, amax16(v));
+    }
+    m = block_max(m, warp_max);
+    const bool infinities = isinf(m);
+    if (infinities) {  // the same for the whole block
+        m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            raw[i].unpack(v);
+            m = fmaxf(m, finite_amax16(v));
+        }
+        m = block_max(m, warp_max);
+    }
     const int E = scale_exponent(m);
     const float inv = inverse_scale(E);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = r0 + 32 * i;
-        if (r < rows && c < cols) *reinterpret_cast<uint4 *>(codes + (size_t)r * cols + c) = codes16(v[i], inv);
+        raw[i].unpack(v);
+        if (r < rows && c < cols) *reinterpret_cast<uint4 *>(codes + (size_t)r * cols + c) = codes16(v, inv, infinities);
     }
     uint8_t *srow = scales + (size_t)blockIdx.y * pitch;
     if (threadIdx.x == 0) srow[blockIdx.x] = (uint8_t)(E + 127);
@@ -112,11 +123,12 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const __nv_bfloat16 *__re
         out[row * ld + c] = c < cols ? a[row * cols + c] : __float2bfloat16_rn(0.f);
 }
 
-template <typename T, bool kColScale, int kRows>
+template <typename T, bool kColScale>
 cudaError_t quantize_rows(const T *a, long long lda, int rows, int cols, const float *colscale, uint8_t *codes,
                           long long ld_codes, uint8_t *scales, unsigned int *zero, int n_zero, cudaStream_t stream) {
     const int words = fp8_pitch(cols) / 4;
-    const long long blocks = ((long long)((rows + kRows - 1) / kRows) * words + 7) / 8;
+    const long long blocks = ((long long)rows * words + 7) / 8;
+    if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     const bool vec = (reinterpret_cast<uintptr_t>(a) & 15u) == 0 && (lda * sizeof(T)) % 16 == 0;
     const bool svec = (reinterpret_cast<uintptr_t>(colscale) & 15u) == 0;
@@ -129,21 +141,8 @@ cudaError_t quantize_rows(const T *a, long long lda, int rows, int cols, const f
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, kColScale, kRows>, a, lda, rows, cols, words, colscale, codes,
+    return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, kColScale>, a, lda, rows, cols, words, colscale, codes,
                               ld_codes, scales, vec, svec, zero, n_zero);
-}
-
-template <typename T>
-cudaError_t quantize_rows(const T *a, long long lda, int rows, int cols, const float *colscale, uint8_t *codes,
-                          long long ld_codes, uint8_t *scales, unsigned int *zero, int n_zero, cudaStream_t stream) {
-    const long long warps = (long long)rows * (fp8_pitch(cols) / 4);
-    if (warps == 0) return cudaSuccess;
-    // four rows per warp once that still gives every SM a CTA
-    if (warps >= 4 * 8 * 148)
-        return colscale ? quantize_rows<T, true, 4>(a, lda, rows, cols, colscale, codes, ld_codes, scales, zero, n_zero, stream)
-                        : quantize_rows<T, false, 4>(a, lda, rows, cols, colscale, codes, ld_codes, scales, zero, n_zero, stream);
-    return colscale ? quantize_rows<T, true, 1>(a, lda, rows, cols, colscale, codes, ld_codes, scales, zero, n_zero, stream)
-                    : quantize_rows<T, false, 1>(a, lda, rows, cols, colscale, codes, ld_codes, scales, zero, n_zero, stream);
 }
 
 }  // namespace
@@ -158,10 +157,14 @@ cudaError_t launch_fp8_pad_rows(const __nv_bfloat16 *a, int rows, int cols, __nv
 cudaError_t launch_fp8_quantize_rows(const void *a, wl_type type, long long lda, int rows, int cols,
                                      const float *colscale, uint8_t *codes, long long ld_codes, uint8_t *scales,
                                      unsigned int *zero, int n_zero, cudaStream_t stream) {
-    return type == WL_BF16 ? quantize_rows(static_cast<const __nv_bfloat16 *>(a), lda, rows, cols, colscale, codes,
-                                           ld_codes, scales, zero, n_zero, stream)
-                           : quantize_rows(static_cast<const float *>(a), lda, rows, cols, colscale, codes, ld_codes,
+    if (type == WL_F32)
+        return quantize_rows<float, false>(static_cast<const float *>(a), lda, rows, cols, nullptr, codes, ld_codes,
                                            scales, zero, n_zero, stream);
+    const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a);
+    return colscale ? quantize_rows<__nv_bfloat16, true>(x, lda, rows, cols, colscale, codes, ld_codes, scales, zero,
+                                                         n_zero, stream)
+                    : quantize_rows<__nv_bfloat16, false>(x, lda, rows, cols, nullptr, codes, ld_codes, scales, zero,
+                                                          n_zero, stream);
 }
 
 cudaError_t launch_fp8_quantize_tiles(const void *a, wl_type type, int rows, int cols, uint8_t *codes, uint8_t *scales,
