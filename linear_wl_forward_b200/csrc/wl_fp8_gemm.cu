@@ -24,7 +24,7 @@
 // Per CTA (384 threads):
 //   warp 0      TMA producer, three stages of two blocks (64 KB); both CTAs'
 //               copies complete on the leader's barrier
-//   warp 1      TMEM allocation; in the leader CTA, one lane issues every MMA
+//   warp 1      TMEM allocation; in the leader CTA, this warp issues every MMA
 //   warps 2, 3  scales of A and B: four blocks at a time into the MMA's layout
 //               (32 lanes x 16 bytes per 128 rows), copied to TMEM by the
 //               MMA warp (tcgen05.cp, replicated to the four lane quarters)
@@ -33,6 +33,7 @@
 
 #include "wl_common.cuh"
 #include "wl_fp8.h"
+#include "wl_fp8_device.cuh"
 
 namespace wl {
 
@@ -62,17 +63,6 @@ __device__ __forceinline__ uint32_t map_rank(const void *p, uint32_t rank) {
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
 }
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap, int c0, int c1, uint32_t bar) {
     asm volatile(
@@ -119,26 +109,6 @@ __device__ __forceinline__ void commit_pair(uint64_t *bar) {
         "h"((uint16_t)3)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32"
-        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr));
-}
-
-// Instruction descriptor of kind::mxf8f6f4: E4M3 A and B (formats 0), E8M0
-// scales (bit 23), N >> 3 (17-22), M >> 7 (27-28), the byte of the scale word
-// for B (4-5) and A (29-30); bit 16: B is N-major.
-__device__ __forceinline__ uint32_t idesc_mxf8(int M, int N, bool b_n_major, uint32_t sf) {
-    return (sf << 4) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
-           ((uint32_t)(M >> 7) << 27) | (sf << 29);
-}
-// Scales in shared memory: unswizzled, 8-row groups 128 bytes apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
-}
 
 // ---------------------------------------------------------------- schedule ----
 struct Tile {
@@ -154,11 +124,11 @@ __device__ __forceinline__ Tile tile_of(const Fp8GemmParams &p, int t) {
 // A tile's work in issue order, up to two blocks (one stage) at a time:
 // main(part, block, two) part by part, and before the last kLrLead stages of
 // them low(part, block, two) for the rank-r blocks of every part.  Stops when
-// either returns false.  Run by one thread, whose instructions bound how fast
-// the tensor pipe is fed: an MMA takes it about 64 cycles, a barrier wait 130
-// and a commit 65, against 448 cycles of MMAs per block, so one block per
-// stage would leave the pipe waiting (measured: 950 cycles per block with
-// per-block waits and bookkeeping).
+// either returns false.  The issuing warp's instructions bound how fast the
+// tensor pipe is fed: an MMA takes it about 40 cycles, a barrier wait 70 and a
+// commit 46, against 448 cycles of MMAs per block, so a stage holds two blocks
+// and the order is in the loops, not in per-block state (with both per block a
+// block took 950 cycles).
 template <typename Main, typename Low>
 __device__ __forceinline__ bool for_stages(const Fp8GemmParams &p, const Fp8Out &o, Main main, Low low) {
     int left = 0;
@@ -184,39 +154,6 @@ __device__ __forceinline__ int lr_blocks(const Fp8GemmParams &p, const Fp8Out &o
     for (int q = 0; q < o.nparts; ++q) lr += p.part[o.part0 + q].lr;
     return lr;
 }
-
-// Bounded wait of one thread; `cluster`: for barriers the other CTA arrives on.
-__device__ __forceinline__ bool thread_wait(uint64_t *bar, uint32_t parity, const Fp8GemmParams &p, volatile int *abort_flag,
-                                            bool cluster = false) {
-    if (cluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!(cluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) {
-        if (*abort_flag) return false;
-        if (globaltimer_ns() - t0 > p.timeout_ns) {
-            record_status(p.status, kStatusTimeout);
-            *abort_flag = 1;
-            return false;
-        }
-    }
-    return true;
-}
-
-// The same for a warp that goes on together.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Fp8GemmParams &p, volatile int *abort_flag) {
-    const bool ok = thread_wait(bar, parity, p, abort_flag);
-    return __all_sync(0xffffffffu, ok);
-}
-
-struct Ring {
-    uint32_t slot = 0, phase = 0, n;
-    __device__ explicit Ring(uint32_t n_) : n(n_) {}
-    __device__ void advance() {
-        if (++slot == n) {
-            slot = 0;
-            phase ^= 1u;
-        }
-    }
-};
 
 // The scale words of one chunk of B for output columns n0 .. n0 + 255.
 template <bool kT>
@@ -269,6 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
     uint64_t *drain = l_empty + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const WaitLimits limits{p.status, p.timeout_ns, abort_flag};
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -303,64 +241,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------ producer ----
-        if (lane == 0) {
-            Ring r(kFp8Stages);
-            uint32_t issued = 0;
-            const uint32_t stage0 = smem_addr(base), full0 = map_rank(full, 0);
-            bool ok = true;
-            for (int t = cluster; t < p.num_tiles && ok; t += nclusters) {
-                const Tile ti = tile_of(p, t);
-                const int m = ti.m0 + (int)rank * 128, n = ti.n0 + (int)rank * kHalf;
-                // both CTAs' bytes of a stage are expected by the leader
-                auto stage = [&](uint32_t bytes) -> bool {
-                    if (!thread_wait(&empty[r.slot], r.phase ^ 1u, p, abort_flag)) return false;
-                    if (rank == 0) mbar_arrive_expect_tx(&full[r.slot], 2 * bytes);
-                    return true;
-                };
-                ok = for_stages(
-                    p, p.out[ti.out],
-                    [&](int q, int kb, bool two) {
-                        if (!stage((kABytes + kBBytes) << two)) return false;
-                        const uint32_t bar = full0 + r.slot * 8;
-                        uint32_t sa = stage0 + r.slot * kFp8StageBytes;
-                        for (int c = kb * 128; c <= (kb + two) * 128; c += 128, sa += kFp8BlockBytes) {
-                            tma_load_2d_pair(sa, &p.tm_a[q], c, m, bar);
-                            tma_load_2d_pair(sa + kABytes, &p.tm_b[q], kT ? n : c, kT ? c : n, bar);
-                        }
-                        r.advance();
-                        ++issued;
-                        return true;
-                    },
-                    [&](int q, int j, bool two) {
-                        if (!stage((kABytes + kHalf * 128) << two)) return false;
-                        const uint32_t bar = full0 + r.slot * 8;
-                        uint32_t sa = stage0 + r.slot * kFp8StageBytes;
-                        for (int c = j * 64; c <= (j + two) * 64; c += 64, sa += kFp8BlockBytes) {
-                            tma_load_2d_pair(sa, &p.tm_t[q], c, m, bar);
-                            tma_load_2d_pair(sa + kABytes, &p.tm_u[q], c, n, bar);
-                        }
-                        r.advance();
-                        ++issued;
-                        return true;
-                    });
-            }
-            if (!ok && rank == 0) {
-                // Let the copies already issued land before the pair exits; their
-                // bytes are counted here, in the leader.
-                const uint32_t left = issued < kFp8Stages ? issued : kFp8Stages;
-                for (uint32_t i = issued - left; i < issued; ++i)
-                    mbar_wait(&full[i % kFp8Stages], (i / kFp8Stages) & 1u, p.status, 1000000ull);
-            }
+        Ring r(kFp8Stages);
+        uint32_t issued = 0;
+        const uint32_t stage0 = smem_addr(base), full0 = map_rank(full, 0);
+        bool ok = true;
+        for (int t = cluster; t < p.num_tiles && ok; t += nclusters) {
+            const Tile ti = tile_of(p, t);
+            const int m = ti.m0 + (int)rank * 128, n = ti.n0 + (int)rank * kHalf;
+            // one or two blocks of `step` columns into the next stage; both CTAs'
+            // bytes are expected by the leader
+            auto load = [&](const CUtensorMap *ma, const CUtensorMap *mb, int c, int step, bool two, bool rows_of_b, uint32_t b_bytes) {
+                if (!warp_wait(&empty[r.slot], r.phase ^ 1u, limits)) return false;
+                if (elect_one()) {
+                    const uint32_t bar = full0 + r.slot * 8;
+                    uint32_t sa = stage0 + r.slot * kFp8StageBytes;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[r.slot], (2 * (kABytes + b_bytes)) << two);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if (k == 1 && !two) break;
+                        tma_load_2d_pair(sa, ma, c, m, bar);
+                        tma_load_2d_pair(sa + kABytes, mb, rows_of_b ? n : c, rows_of_b ? c : n, bar);
+                        c += step;
+                        sa += kFp8BlockBytes;
+                    }
+                }
+                __syncwarp();
+                r.advance();
+                ++issued;
+                return true;
+            };
+            ok = for_stages(
+                p, p.out[ti.out],
+                [&](int q, int kb, bool two) { return load(&p.tm_a[q], &p.tm_b[q], kb * 128, 128, two, kT, kBBytes); },
+                [&](int q, int j, bool two) { return load(&p.tm_t[q], &p.tm_u[q], j * 64, 64, two, false, kHalf * 128); });
+        }
+        if (!ok && rank == 0 && lane == 0) {
+            // Let the copies already issued land before the pair exits; their
+            // bytes are counted here, in the leader.
+            const uint32_t left = issued < kFp8Stages ? issued : kFp8Stages;
+            for (uint32_t i = issued - left; i < issued; ++i)
+                mbar_wait(&full[i % kFp8Stages], (i / kFp8Stages) & 1u, p.status, 1000000ull);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ----------------------------------------------------- MMA issuer ---
-        if (rank == 0 && lane == 0) {
-            const uint32_t idesc_lr = idesc_bf16_f32(kFp8BM, kFp8BN);
-            const uint32_t idesc0 = idesc_mxf8(kFp8BM, kFp8BN, kT, 0), idesc_step = (1u << 4) | (1u << 29);
+        if (rank == 0) {
+            const uint32_t idesc_lr = idesc_bf16_f32(kFp8BM, kFp8BN), idesc0 = idesc_mxf8(kFp8BM, kFp8BN, kT);
             const uint64_t da0 = sw128_kmajor_desc(smem_addr(base)), db0 = sw128_kmajor_desc(smem_addr(base) + kABytes);
+            const uint64_t sd0 = scale_desc(smem_addr(sf_base));
+            constexpr uint64_t kNext = kFp8BlockBytes >> 4;  // a stage's second block
+            // 32 columns of the contraction further: 32 bytes inside the swizzled
+            // rows, or (N-major) 32 rows of 128 bytes
+            constexpr uint64_t kStepB = kT ? 256 : 2;
             Ring r(kFp8Stages), sr(kFp8SfSlots);
-            uint32_t it = 0, lr_count = 0, sf_slot = 0, sf_col = 0;
+            uint32_t it = 0, lr_count = 0, sf_slot = 0;
             bool ok = true;
             for (int t = cluster; t < p.num_tiles && ok; t += nclusters, ++it) {
                 const Tile ti = tile_of(p, t);
@@ -369,8 +303,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
                 const uint32_t d_main = tmem + reg * kRegionCols, d_lr = tmem + other * kRegionCols;
                 const uint32_t uses = it >> 1, other_uses = (it + 1) >> 1;  // of the regions, by earlier tiles
                 // the region's last main sum and the last rank-r term have been read
-                if (uses > 0) ok = thread_wait(&m_empty[reg], (uses - 1) & 1u, p, abort_flag, true);
-                if (ok && lr_count > 0) ok = thread_wait(l_empty, (lr_count - 1) & 1u, p, abort_flag, true);
+                if (uses > 0) ok = warp_wait<true>(&m_empty[reg], (uses - 1) & 1u, limits);
+                if (ok && lr_count > 0) ok = warp_wait<true>(l_empty, (lr_count - 1) & 1u, limits);
                 if (!ok) break;
                 tc_fence_after();
                 const int lr = lr_blocks(p, o);
@@ -379,68 +313,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
                 ok = for_stages(
                     p, o,
                     [&](int, int kb, bool two) {
-                        const uint32_t sf = (uint32_t)kb & 3u;
-                        if (sf == 0) {
-                            if (!thread_wait(&sf_full[sr.slot], sr.phase, p, abort_flag, true)) return false;
-                            tc_fence_after();
-                            sf_col = tmem + kSfCol + ((sf_slot ^= 16u));  // the other slot of scales
-                            const uint64_t ds = scale_desc(smem_addr(sf_base) + sr.slot * kFp8SfBytes);
-                            cp_scales_pair(sf_col, ds);
-                            cp_scales_pair(sf_col + 4, ds + (512 >> 4));
-                            cp_scales_pair(sf_col + 8, ds + (1024 >> 4));
-                            commit_pair(&sf_empty[sr.slot]);
-                            sr.advance();
+                        const bool chunk = (kb & 3) == 0;  // the next four blocks' scales
+                        if (chunk) {
+                            if (!warp_wait<true>(&sf_full[sr.slot], sr.phase, limits)) return false;
+                            sf_slot ^= 16u;
                         }
-                        if (!thread_wait(&full[r.slot], r.phase, p, abort_flag)) return false;
+                        if (!warp_wait(&full[r.slot], r.phase, limits)) return false;
                         tc_fence_after();
-                        const uint32_t idesc = idesc0 + sf * idesc_step;
+                        const uint32_t sf = tmem + kSfCol + sf_slot, idesc = idesc0 + (kb & 3) * kScaleByte;
                         const uint64_t da = da0 + r.slot * (kFp8StageBytes >> 4), db = db0 + r.slot * (kFp8StageBytes >> 4);
-                        // 32 columns of the contraction further: 32 bytes inside the
-                        // swizzled rows, or (N-major) 32 rows of 128 bytes
-                        mma_mxf8_pair(d_main, da, db, idesc, sf_col, sf_col + 4, acc);
-                        acc = 1;
+                        const uint64_t ds = sd0 + sr.slot * (kFp8SfBytes >> 4);
+                        if (elect_one()) {
+                            if (chunk) {
+                                cp_scales_pair(sf, ds);
+                                cp_scales_pair(sf + 4, ds + (512 >> 4));
+                                cp_scales_pair(sf + 8, ds + (1024 >> 4));
+                                commit_pair(&sf_empty[sr.slot]);
+                            }
+                            mma_mxf8_pair(d_main, da, db, idesc, sf, sf + 4, acc);
 #pragma unroll
-                        for (int k = 1; k < 4; ++k)
-                            mma_mxf8_pair(d_main, da + 2 * k, db + (kT ? 256 : 2) * k, idesc, sf_col, sf_col + 4, 1);
-                        if (two) {
-                            constexpr int next = kFp8BlockBytes >> 4;
+                            for (int k = 1; k < 4; ++k) mma_mxf8_pair(d_main, da + 2 * k, db + kStepB * k, idesc, sf, sf + 4, 1);
+                            if (two)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_mxf8_pair(d_main, da + next + 2 * k, db + next + (kT ? 256 : 2) * k, idesc + idesc_step,
-                                              sf_col, sf_col + 4, 1);
+                                for (int k = 0; k < 4; ++k)
+                                    mma_mxf8_pair(d_main, da + kNext + 2 * k, db + kNext + kStepB * k, idesc + kScaleByte, sf, sf + 4, 1);
+                            commit_pair(&empty[r.slot]);
                         }
-                        commit_pair(&empty[r.slot]);
+                        __syncwarp();
+                        acc = 1;
+                        if (chunk) sr.advance();
                         r.advance();
                         return true;
                     },
                     [&](int, int, bool two) {
                         const bool first = lr_left == lr;
-                        if (first && other_uses > 0) {
-                            if (!thread_wait(&m_empty[other], (other_uses - 1) & 1u, p, abort_flag, true)) return false;
-                        }
-                        if (!thread_wait(&full[r.slot], r.phase, p, abort_flag)) return false;
+                        if (first && other_uses > 0 && !warp_wait<true>(&m_empty[other], (other_uses - 1) & 1u, limits)) return false;
+                        if (!warp_wait(&full[r.slot], r.phase, limits)) return false;
                         tc_fence_after();
+                        lr_left -= 1 + two;
                         const uint64_t da = da0 + r.slot * (kFp8StageBytes >> 4), db = db0 + r.slot * (kFp8StageBytes >> 4);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f16_pair(d_lr, da + 2 * k, db + 2 * k, idesc_lr, !(first && k == 0));
-                        if (two) {
-                            constexpr int next = kFp8BlockBytes >> 4;
+                            for (int k = 0; k < 4; ++k) mma_f16_pair(d_lr, da + 2 * k, db + 2 * k, idesc_lr, !(first && k == 0));
+                            if (two)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) mma_f16_pair(d_lr, da + next + 2 * k, db + next + 2 * k, idesc_lr, 1);
+                                for (int k = 0; k < 4; ++k) mma_f16_pair(d_lr, da + kNext + 2 * k, db + kNext + 2 * k, idesc_lr, 1);
+                            commit_pair(&empty[r.slot]);
+                            if (lr_left == 0) commit_pair(l_full);
                         }
-                        commit_pair(&empty[r.slot]);
+                        __syncwarp();
                         r.advance();
-                        if ((lr_left -= 1 + two) == 0) commit_pair(l_full);
                         return true;
                     });
                 if (!ok) break;
-                commit_pair(&m_full[reg]);
+                if (elect_one()) commit_pair(&m_full[reg]);
+                __syncwarp();
                 lr_count += lr > 0;
             }
-            commit_pair(drain);
+            if (elect_one()) commit_pair(drain);
+            __syncwarp();
         }
-        __syncwarp();
     } else if (warp < 4) {
         // ------------------------------------------------------- scales -----
         Ring r(kFp8SfSlots);
@@ -462,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
                     } else {
                         b_scale_words<kT>(pt, o.N, ti.n0, c, lane, w);
                     }
-                    if (!warp_wait(&sf_empty[r.slot], r.phase ^ 1u, p, abort_flag)) {
+                    if (!warp_wait(&sf_empty[r.slot], r.phase ^ 1u, limits)) {
                         ok = false;
                         break;
                     }
@@ -496,7 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
             const int n0 = ti.n0 + half * kHalf;
             uint32_t d[kChunks][16];
             if (kMode != kFp8ColSums && lr > 0) {
-                if (!warp_wait(l_full, lr_count & 1u, p, abort_flag)) break;
+                if (!warp_wait(l_full, lr_count & 1u, limits)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) tmem_ld16(lane_addr + (reg ^ 1u) * kRegionCols + c * 16, d[c]);
@@ -511,7 +443,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) d[c][i] = 0;
             }
-            if (!warp_wait(&m_full[reg], (it >> 1) & 1u, p, abort_flag)) break;
+            if (!warp_wait(&m_full[reg], (it >> 1) & 1u, limits)) break;
             tc_fence_after();
             if (kMode == kFp8ColSums) {
                 const bool vec = (o.N & 7) == 0 && (reinterpret_cast<uintptr_t>(o.dy) & 15u) == 0;
@@ -602,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
     tc_fence_before();
     __syncthreads();
     // Every MMA issued has ended and every signal of theirs has arrived here.
-    if (warp == 1) mbar_wait(drain, 0, p.status, p.timeout_ns);
+    if (warp == 1) mbar_wait(drain, 0, p.status, kDrainNs);
     cluster_sync();  // neither CTA leaves while the other may signal it or its MMAs read here
     if (warp == 1) {
         tc_fence_after();

@@ -31,6 +31,7 @@
 
 #include "wl_common.cuh"
 #include "wl_fp8.h"
+#include "wl_fp8_device.cuh"
 #include "wl_fp8_encode.cuh"
 
 namespace wl {
@@ -68,26 +69,12 @@ __device__ __forceinline__ float ld_cluster(uint32_t local_addr, uint32_t rank) 
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
-    uint32_t u[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
-                 : "r"(taddr));
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
-}
-
 // Two E4M3 codes (low byte first) times a power of two, as a pair of bf16.
 __device__ __forceinline__ uint32_t expand_pair(uint32_t codes, float scale) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
     const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h));
     return pack_bf16x2(f.x * scale, f.y * scale);
-}
-
-__device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, const LowrankParams &p) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status, p.timeout_ns));
 }
 
 __device__ __forceinline__ void store8(__nv_bfloat16 *dst, const float (&v)[8]) {
@@ -152,6 +139,8 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
     uint64_t *ready = empty + kMaxStages;  // codes expanded
     uint64_t *done = ready + kMaxStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const WaitLimits limits{p.status, p.timeout_ns, abort_flag};
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = p.split;
@@ -177,6 +166,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
             mbar_init(&ready[i], kExpanders);
         }
         mbar_init(done, 1);
+        *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -197,68 +187,70 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
     const uint32_t b_off = a_bytes + (kCodes ? kCodeTile : 0);
     bool ok = true;
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t slot = 0, ph = 0, issued = 0;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(&empty[slot], ph ^ 1u, p.status, p.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t *st = base + (size_t)slot * p.stage_bytes;
-                mbar_arrive_expect_tx(&full[slot], (kCodes ? kCodeTile : a_bytes) + (uint32_t)(terms * boxes) * kBBox);
+        Ring r(p.stages);
+        uint32_t issued = 0;
+        const uint32_t bytes = (kCodes ? kCodeTile : a_bytes) + (uint32_t)(terms * boxes) * kBBox;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!(ok = warp_wait(&empty[r.slot], r.phase ^ 1u, limits))) break;
+            if (elect_one()) {
+                uint8_t *st = base + (size_t)r.slot * p.stage_bytes;
+                uint64_t *bar = &full[r.slot];
+                mbar_arrive_expect_tx(bar, bytes);
                 if (kMode == kLowrankRows) {
-                    tma_load_2d(st, &jb.tm_a, kb * 64, i0, &full[slot]);
+                    tma_load_2d(st, &jb.tm_a, kb * 64, i0, bar);
                 } else if (kMode == kLowrankCols) {
-                    tma_load_2d(st, &jb.tm_a, i0, kb * 64, &full[slot]);
-                    tma_load_2d(st + kBBox, &jb.tm_a, i0 + 64, kb * 64, &full[slot]);
+                    tma_load_2d(st, &jb.tm_a, i0, kb * 64, bar);
+                    tma_load_2d(st + kBBox, &jb.tm_a, i0 + 64, kb * 64, bar);
                 } else {
-                    tma_load_2d(st + kATile, &jb.tm_a, i0 / 4, kb * 64, &full[slot]);  // in words
+                    tma_load_2d(st + kATile, &jb.tm_a, i0 / 4, kb * 64, bar);  // in words
                 }
                 for (int b = 0; b < boxes; ++b) {
-                    tma_load_2d(st + b_off + b * kBBox, &jb.tm_b, j0 + b * 64, kb * 64, &full[slot]);
-                    if (kCodes) tma_load_2d(st + b_off + (boxes + b) * kBBox, &jb.tm_b2, j0 + b * 64, kb * 64, &full[slot]);
+                    tma_load_2d(st + b_off + b * kBBox, &jb.tm_b, j0 + b * 64, kb * 64, bar);
+                    if (kCodes) tma_load_2d(st + b_off + (boxes + b) * kBBox, &jb.tm_b2, j0 + b * 64, kb * 64, bar);
                 }
-                ++issued;
-                if (++slot == (uint32_t)p.stages) slot = 0, ph ^= 1u;
             }
-            if (!ok) {  // let the copies already issued land before the CTA exits
-                const uint32_t left = issued < (uint32_t)p.stages ? issued : p.stages;
-                for (uint32_t i = issued - left; i < issued; ++i)
-                    mbar_wait(&full[i % p.stages], (i / p.stages) & 1u, p.status, 1000000ull);
-            }
+            __syncwarp();
+            ++issued;
+            r.advance();
+        }
+        if (!ok && lane == 0) {  // let the copies already issued land before the CTA exits
+            const uint32_t left = issued < (uint32_t)p.stages ? issued : p.stages;
+            for (uint32_t i = issued - left; i < issued; ++i)
+                mbar_wait(&full[i % p.stages], (i / p.stages) & 1u, p.status, 1000000ull);
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            // fp32 sums of bf16 products; A M-major (bit 15) unless its rows run along i; B N-major (bit 16)
-            const uint32_t idesc = idesc_bf16_f32(128, n_mma) | (kMode == kLowrankRows ? 0u : 1u << 15) | 1u << 16;
-            const uint32_t s0 = smem_addr(base);
-            const uint64_t da0 = kMode == kLowrankRows ? sw128_kmajor_desc(s0) : mn_major_desc(s0);
-            const uint64_t db0 = mn_major_desc(s0 + b_off), db1 = mn_major_desc(s0 + b_off + (uint32_t)boxes * kBBox);
-            const uint64_t step = (uint32_t)p.stage_bytes >> 4;
-            uint32_t slot = 0, ph = 0, acc = 0;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(kCodes ? &ready[slot] : &full[slot], ph, p.status, p.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t da = da0 + slot * step, db = db0 + slot * step;
+        // fp32 sums of bf16 products; A M-major (bit 15) unless its rows run along i; B N-major (bit 16)
+        const uint32_t idesc = idesc_bf16_f32(128, n_mma) | (kMode == kLowrankRows ? 0u : 1u << 15) | 1u << 16;
+        const uint32_t s0 = smem_addr(base);
+        const uint64_t da0 = kMode == kLowrankRows ? sw128_kmajor_desc(s0) : mn_major_desc(s0);
+        const uint64_t db0 = mn_major_desc(s0 + b_off), low = ((uint32_t)boxes * kBBox) >> 4;  // B's low term
+        const uint64_t step = (uint32_t)p.stage_bytes >> 4;
+        constexpr uint64_t kStepA = kMode == kLowrankRows ? 2 : 128;  // 16 contraction rows on: 32 bytes, or 16 rows of 128
+        Ring r(p.stages);
+        uint32_t acc = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!(ok = warp_wait(kCodes ? &ready[r.slot] : &full[r.slot], r.phase, limits))) break;
+            tc_fence_after();
+            const uint64_t da = da0 + r.slot * step, db = db0 + r.slot * step;
+            if (elect_one()) {
+                tc_mma_f16(tmem, da, db, idesc, acc);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {  // 16 contraction rows on: 32 bytes, or 16 rows of 128
-                    tc_mma_f16(tmem, da + (kMode == kLowrankRows ? 2 : 128) * k, db + 128 * k, idesc, acc);
-                    acc = 1;
-                }
+                for (int k = 1; k < 4; ++k) tc_mma_f16(tmem, da + kStepA * k, db + 128 * k, idesc, 1);
                 if (kCodes) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) tc_mma_f16(tmem, da + 128 * k, db1 + slot * step + 128 * k, idesc, 1);
+                    for (int k = 0; k < 4; ++k) tc_mma_f16(tmem, da + kStepA * k, db + low + 128 * k, idesc, 1);
                 }
-                tc_commit(&empty[slot]);
-                if (++slot == (uint32_t)p.stages) slot = 0, ph ^= 1u;
+                tc_commit(&empty[r.slot]);
             }
+            __syncwarp();
+            acc = 1;
+            r.advance();
+        }
+        if (elect_one()) {
             tc_commit(done);
             // Outstanding MMAs end before TMEM is released, whatever happened.
-            if (!ok) mbar_wait(done, 0, p.status, 1000000ull);
+            if (!ok) mbar_wait(done, 0, p.status, kDrainNs);
         }
         __syncwarp();
     } else {
@@ -277,7 +269,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
             for (int kb = kb0; kb < kb1; ++kb) {
                 uint32_t next[2] = {127u, 127u};
                 if (kb + 1 < kb1) next[0] = scale_of(kb + 1, 0), next[1] = scale_of(kb + 1, 1);
-                if (!all_wait(&full[slot], ph, p)) {
+                if (!warp_wait(&full[slot], ph, limits)) {
                     ok = false;
                     break;
                 }
@@ -312,7 +304,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
         }
         if (quant) quantize_range(p.quant, kb0 * 64, min(kb1 * 64, p.quant.cols), unit, gridDim.x / S, tid);
         // MMAs done.  A CTA with an empty range of the contraction has no sums.
-        if (ok && warp < 6 && kb1 > kb0) ok = all_wait(done, 0, p);
+        if (ok && warp < 6 && kb1 > kb0) ok = warp_wait(done, 0, limits);
         tc_fence_after();
         const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -321,7 +313,11 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
             for (int c = 0; c < n_mma; c += 8) {
                 float v[8];
                 if (kb1 > kb0) {
-                    tmem_ld8(taddr + c, v);
+                    uint32_t u[8];
+                    tmem_ld8(taddr + c, u);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(u[k]);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) v[k] = 0.f;
@@ -441,7 +437,7 @@ cudaError_t launch_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms, 
     const size_t exchange = p.split > 1 ? (size_t)std::min((widest + 15) / 16 * 16, p.BN) * 512 : 0;
     while ((size_t)p.stages * p.stage_bytes < exchange) ++p.stages;
     // an MMA reads 128 rows of A, so the last stage's tile may end behind the stages
-    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + std::max<size_t>((3 * kMaxStages + 1) * 8 + 16, kATile);
+    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + std::max<size_t>((3 * kMaxStages + 1) * 8 + 32, kATile);
     if (p.stages > kMaxStages || smem > 227 * 1024) return cudaErrorInvalidValue;
     void (*const kernels[3])(LowrankParams) = {lowrank_kernel<kLowrankRows>, lowrank_kernel<kLowrankCols>,
                                                lowrank_kernel<kLowrankCodes>};

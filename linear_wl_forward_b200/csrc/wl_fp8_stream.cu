@@ -5,10 +5,9 @@
 // so a tile is 128 output rows, its accumulator column a token (Mp = M rounded
 // up to 16, at most 128), and a 16 KB block of weights (128 rows x 128
 // columns) costs four MMAs of N = Mp.  Reading the weights bounds it: at the
-// measured copy rate a block takes each of 148 SMs about 700 cycles.  The MMA
-// thread needs about 64 cycles per MMA, 130 per barrier wait and 65 per commit,
-// so a stage holds two blocks (one block per stage: 60 us against 47 for
-// Gemma-4's gate/up at one token).
+// measured copy rate a block takes each of 148 SMs about 700 cycles.  The
+// issuing warp's instructions come next (about 40 cycles per MMA, 70 per wait,
+// 46 per commit), so a stage holds two blocks.
 //
 // The call's work (per tile: the contraction in pairs of blocks, then U's
 // 64-column blocks in pairs) forms one list of units that is cut evenly over
@@ -24,6 +23,7 @@
 
 #include "wl_common.cuh"
 #include "wl_fp8.h"
+#include "wl_fp8_device.cuh"
 
 namespace wl {
 
@@ -45,26 +45,6 @@ __device__ __forceinline__ void mma_mxf8(uint32_t d, uint64_t a, uint64_t b, uin
 __device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *v) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "r"(taddr));
-}
-
-__device__ __forceinline__ bool thread_wait(uint64_t *bar, uint32_t parity, const Fp8StreamParams &p, volatile int *abort_flag) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (*abort_flag) return false;
-        if (globaltimer_ns() - t0 > p.timeout_ns) {
-            record_status(p.status, kStatusTimeout);
-            *abort_flag = 1;
-            return false;
-        }
-    }
-    return true;
-}
-
 // A run of units of one tile: [u0, u1) of the tile's own.
 struct Segment {
     int seg, tile, u0, u1, nu;  // nu: the tile's units
@@ -122,6 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *last_flag = abort_flag + 1;
+    const WaitLimits limits{p.status, p.timeout_ns, abort_flag};
 
     // TMEM columns: two sums of W0 x, one of U T, two slots of 8 for scales
     const uint32_t set_cols = (uint32_t)max(p.Mp, 32), d_col = 2 * set_cols, sf_col = 3 * set_cols;
@@ -156,124 +137,121 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
 
     if (warp == 0) {
         // ------------------------------------------------------ producer ----
-        if (lane == 0) {
-            // weights of the first `stages` units, then (x and T made) their
-            // operands, then the rest in order
-            const uint32_t total = (uint32_t)(end - begin);
-            uint32_t issued = 0;
-            bool ok = true;
-            if (!p.early) pdl_wait_primary();
-            for (int pass = 0; pass < 2 && ok; ++pass) {
-                // pass 0: weights of units [0, head); pass 1: everything else
-                const uint32_t head = p.early ? min(total, stages) : 0;
-                if (pass == 1 && p.early) pdl_wait_primary();
-                uint32_t i = 0, slot = 0, ph = 0;
-                for (long long u = begin; u < end && ok;) {
-                    const Segment s = segment_at(p, u, end);
-                    const Fp8StreamSeg &sg = p.seg[s.seg];
-                    const int n0 = s.tile * 128;
-                    for (int b = s.u0; b < s.u1; ++b, ++i) {
-                        if (pass == 0 && i >= head) break;
-                        const bool first_pass = i < head, low = b >= sg.kpairs;
-                        // the unit's one or two blocks, `step` columns each
-                        const int blk = 2 * (low ? b - sg.kpairs : b), step = low ? 64 : 128;
-                        const int two = blk + 1 < (low ? sg.lr : sg.nkb);
-                        uint8_t *st = base + slot * stage_bytes;
-                        if (pass == 0 || !first_pass) {
-                            if (!first_pass && !thread_wait(&empty[slot], ph ^ 1u, p, abort_flag)) {
-                                ok = false;
-                                break;
-                            }
-                            mbar_arrive_expect_tx(&full[slot], block_bytes << two);
-                            for (int k = 0; k <= two; ++k)
-                                tma_load_2d(st + k * block_bytes, low ? &p.tm_u[s.seg] : &p.tm_w[s.seg], (blk + k) * step, n0, &full[slot]);
-                            ++issued;
-                        }
-                        if (pass == 1)
-                            for (int k = 0; k <= two; ++k)
-                                tma_load_2d(st + k * block_bytes + kWBytes, low ? &p.tm_t[s.seg] : &p.tm_x, (blk + k) * step, 0, &full[slot]);
-                        if (++slot == stages) slot = 0, ph ^= 1u;
+        // weights of the first `stages` units, then (x and T made) their
+        // operands, then the rest in order
+        const uint32_t total = (uint32_t)(end - begin), head = p.early ? min(total, stages) : 0;
+        uint32_t issued = 0;
+        bool ok = true;
+        for (int pass = p.early ? 0 : 1; pass < 2 && ok; ++pass) {
+            // pass 0: weights of units [0, head); pass 1: everything else
+            if (pass == 1) pdl_wait_primary();
+            uint32_t i = 0, slot = 0, ph = 0;
+            for (long long u = begin; u < end && ok && (pass == 1 || i < head);) {
+                const Segment s = segment_at(p, u, end);
+                const Fp8StreamSeg &sg = p.seg[s.seg];
+                const int n0 = s.tile * 128;
+                for (int b = s.u0; b < s.u1 && (pass == 1 || i < head); ++b, ++i) {
+                    const bool weights = pass == 0 || i >= head, low = b >= sg.kpairs;
+                    // the unit's one or two blocks, `step` columns each
+                    const int blk = 2 * (low ? b - sg.kpairs : b), step = low ? 64 : 128;
+                    const int two = blk + 1 < (low ? sg.lr : sg.nkb);
+                    const CUtensorMap *mw = low ? &p.tm_u[s.seg] : &p.tm_w[s.seg], *mx = low ? &p.tm_t[s.seg] : &p.tm_x;
+                    if (i >= head && !warp_wait(&empty[slot], ph ^ 1u, limits)) {
+                        ok = false;
+                        break;
                     }
-                    if (pass == 0 && i >= head) break;
-                    u += s.u1 - s.u0;
+                    if (elect_one()) {
+                        uint8_t *st = base + slot * stage_bytes;
+                        if (weights) mbar_arrive_expect_tx(&full[slot], block_bytes << two);
+                        for (int k = 0; k <= two; ++k) {
+                            if (weights) tma_load_2d(st + k * block_bytes, mw, (blk + k) * step, n0, &full[slot]);
+                            if (pass == 1) tma_load_2d(st + k * block_bytes + kWBytes, mx, (blk + k) * step, 0, &full[slot]);
+                        }
+                    }
+                    __syncwarp();
+                    issued += weights;
+                    if (++slot == stages) slot = 0, ph ^= 1u;
                 }
+                u += s.u1 - s.u0;
             }
-            if (!ok) {  // let the copies already issued land before the CTA exits
-                const uint32_t left = issued < stages ? issued : stages;
-                for (uint32_t i = issued - left; i < issued; ++i)
-                    mbar_wait(&full[i % stages], (i / stages) & 1u, p.status, 1000000ull);
-            }
+        }
+        if (!ok && lane == 0) {  // let the copies already issued land before the CTA exits
+            const uint32_t left = issued < stages ? issued : stages;
+            for (uint32_t i = issued - left; i < issued; ++i)
+                mbar_wait(&full[i % stages], (i / stages) & 1u, p.status, 1000000ull);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ----------------------------------------------------- MMA issuer ---
-        if (lane == 0) {
-            // E4M3 operands (formats 0), E8M0 scales (bit 23), N >> 3, M >> 7 (27-28);
-            // the scale byte of a block: bits 4-5 (B), 29-30 (A)
-            const uint32_t idesc0 = ((uint32_t)(p.Mp >> 3) << 17) | (1u << 23) | (1u << 27);
-            const uint32_t idesc_lr = idesc_bf16_f32(128, p.Mp);
-            const uint64_t da0 = sw128_kmajor_desc(smem_addr(base)), db0 = sw128_kmajor_desc(smem_addr(base) + kWBytes);
-            const uint64_t sfd0 = (uint64_t)((smem_addr(sf_base) & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
-            uint32_t slot = 0, ph = 0, count = 0, chunk = 0;
-            bool ok = true;
-            for (long long u = begin; u < end && ok; ++count) {
-                const Segment s = segment_at(p, u, end);
-                const Fp8StreamSeg &sg = p.seg[s.seg];
-                const uint32_t set = count & 1u, d_main = tmem + set * set_cols;
-                if (count >= 2) ok = thread_wait(&acc_empty[set], ((count >> 1) - 1) & 1u, p, abort_flag);
+        const uint32_t idesc0 = idesc_mxf8(128, p.Mp), idesc_lr = idesc_bf16_f32(128, p.Mp);
+        const uint64_t da0 = sw128_kmajor_desc(smem_addr(base)), db0 = sw128_kmajor_desc(smem_addr(base) + kWBytes);
+        const uint64_t sd0 = scale_desc(smem_addr(sf_base)), next = block_bytes >> 4;
+        uint32_t slot = 0, ph = 0, count = 0, chunk = 0;
+        bool ok = true;
+        for (long long u = begin; u < end && ok; ++count) {
+            const Segment s = segment_at(p, u, end);
+            const Fp8StreamSeg &sg = p.seg[s.seg];
+            const uint32_t set = count & 1u, d_main = tmem + set * set_cols, d_lr = tmem + d_col;
+            if (count >= 2) ok = warp_wait(&acc_empty[set], ((count >> 1) - 1) & 1u, limits);
+            uint32_t acc = 0;
+            for (int b = s.u0; b < s.u1 && ok; ++b) {
+                const bool low = b >= sg.kpairs;
+                if (low && (b == s.u0 || b == sg.kpairs)) {
+                    acc = 0;
+                    // the only U T accumulator: read by the segment before
+                    if (count >= 1) ok = warp_wait(&acc_empty[set ^ 1u], ((count - 1) >> 1) & 1u, limits);
+                }
+                const bool scales = !low && (b == s.u0 || (b & 1) == 0);  // of four blocks
+                if (scales && ok) {
+                    ++chunk;
+                    ok = warp_wait(&sf_full[chunk & 1u], ((chunk - 1) >> 1) & 1u, limits);
+                }
+                if (!ok || !(ok = warp_wait(&full[slot], ph, limits))) break;
                 tc_fence_after();
-                uint32_t acc = 0, acc_lr = 0;
-                for (int b = s.u0; b < s.u1 && ok; ++b) {
-                    const bool low = b >= sg.kpairs;
-                    if (low && acc_lr == 0 && count >= 1) {  // the only U T accumulator: read by the segment before
-                        ok = thread_wait(&acc_empty[set ^ 1u], ((count - 1) >> 1) & 1u, p, abort_flag);
-                        if (!ok) break;
+                const uint64_t da = da0 + slot * (stage_bytes >> 4), db = db0 + slot * (stage_bytes >> 4);
+                if (low) {
+                    const bool two = 2 * (b - sg.kpairs) + 1 < sg.lr;
+                    if (elect_one()) {
+                        tc_mma_f16(d_lr, da, db, idesc_lr, acc);
+#pragma unroll
+                        for (int k = 1; k < 4; ++k) tc_mma_f16(d_lr, da + 2 * k, db + 2 * k, idesc_lr, 1);
+                        if (two)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) tc_mma_f16(d_lr, da + next + 2 * k, db + next + 2 * k, idesc_lr, 1);
+                        tc_commit(&empty[slot]);
                     }
-                    if (!low && (b == s.u0 || (b & 1) == 0)) {
-                        ++chunk;
-                        ok = thread_wait(&sf_full[chunk & 1u], ((chunk - 1) >> 1) & 1u, p, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t sd = sfd0 + (chunk & 1u) * (kSfBytes >> 4);
-                        cp_scales(tmem + sf_col + (chunk & 1u) * 8, sd);
-                        cp_scales(tmem + sf_col + (chunk & 1u) * 8 + 4, sd + (512 >> 4));
-                        tc_commit(&sf_empty[chunk & 1u]);
-                    }
-                    ok = thread_wait(&full[slot], ph, p, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t da = da0 + slot * (stage_bytes >> 4), db = db0 + slot * (stage_bytes >> 4);
-                    const uint64_t next = block_bytes >> 4;
-                    if (low) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            tc_mma_f16(tmem + d_col, da + 2 * k, db + 2 * k, idesc_lr, acc_lr);
-                            acc_lr = 1;
+                } else {
+                    const bool two = 2 * b + 1 < sg.nkb;
+                    const uint32_t c = tmem + sf_col + (chunk & 1u) * 8;
+                    const uint32_t idesc = idesc0 + (b & 1) * 2 * kScaleByte;  // blocks 2b, 2b + 1 of the chunk's four
+                    const uint64_t sd = sd0 + (chunk & 1u) * (kSfBytes >> 4);
+                    if (elect_one()) {
+                        if (scales) {
+                            cp_scales(c, sd);
+                            cp_scales(c + 4, sd + (512 >> 4));
+                            tc_commit(&sf_empty[chunk & 1u]);
                         }
-                        if (2 * (b - sg.kpairs) + 1 < sg.lr)
+                        mma_mxf8(d_main, da, db, idesc, c, c + 4, acc);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) tc_mma_f16(tmem + d_col, da + next + 2 * k, db + next + 2 * k, idesc_lr, 1);
-                    } else {
-                        const uint32_t c = tmem + sf_col + (chunk & 1u) * 8, step = (1u << 4) | (1u << 29);
-                        const uint32_t idesc = idesc0 + (b & 1) * 2 * step;  // blocks 2b, 2b + 1 of the chunk's four
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            mma_mxf8(d_main, da + 2 * k, db + 2 * k, idesc, c, c + 4, acc);
-                            acc = 1;
-                        }
-                        if (2 * b + 1 < sg.nkb)
+                        for (int k = 1; k < 4; ++k) mma_mxf8(d_main, da + 2 * k, db + 2 * k, idesc, c, c + 4, 1);
+                        if (two)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma_mxf8(d_main, da + next + 2 * k, db + next + 2 * k, idesc + step, c, c + 4, 1);
+                                mma_mxf8(d_main, da + next + 2 * k, db + next + 2 * k, idesc + kScaleByte, c, c + 4, 1);
+                        tc_commit(&empty[slot]);
                     }
-                    tc_commit(&empty[slot]);
-                    if (++slot == stages) slot = 0, ph ^= 1u;
                 }
-                if (ok) tc_commit(&acc_full[set]);
-                u += s.u1 - s.u0;
+                __syncwarp();
+                acc = 1;
+                if (++slot == stages) slot = 0, ph ^= 1u;
             }
+            if (ok && elect_one()) tc_commit(&acc_full[set]);
+            __syncwarp();
+            u += s.u1 - s.u0;
+        }
+        if (elect_one()) {
             tc_commit(drain);
-            mbar_wait(drain, 0, p.status, p.timeout_ns);  // before TMEM is released
+            mbar_wait(drain, 0, p.status, kDrainNs);  // before TMEM is released
         }
         __syncwarp();
     } else if (warp == 2) {
@@ -295,8 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
                     xw[i] = m < p.M ? __ldg(reinterpret_cast<const uint32_t *>(p.x_scales + (size_t)m * p.pitch + 4 * q)) : 0x7F7F7F7Fu;
                 }
                 if (chunk > 2) {
-                    ok = thread_wait(&sf_empty[chunk & 1u], ((chunk - 3) >> 1) & 1u, p, abort_flag);
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = warp_wait(&sf_empty[chunk & 1u], ((chunk - 3) >> 1) & 1u, limits);
                     if (!ok) break;
                 }
                 uint8_t *dst = sf_base + (chunk & 1u) * kSfBytes + lane * 16;
@@ -320,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
             const uint32_t set = count & 1u;
             const bool whole = s.u0 == 0 && s.u1 == s.nu;
             const bool has_z = s.u0 < sg.kpairs, has_d = s.u1 > sg.kpairs;
-            bool ok = thread_wait(&acc_full[set], (count >> 1) & 1u, p, abort_flag);
+            bool ok = warp_wait(&acc_full[set], (count >> 1) & 1u, limits);
             {
                 // the four warps meet below: they go on, or stop, together
                 uint32_t fail;
