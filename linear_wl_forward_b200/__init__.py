@@ -314,9 +314,9 @@ def quantize_fp8(a, block_rows=1, codes=None, scales=None, stream=None):
     u8 = torch.uint8
     with _On(dev, stream) as handle:
         if codes is None:
-            codes = torch.empty((R, C), dtype=u8, device=dev)
+            codes = torch.empty(R, C, dtype=u8, device=dev)
         if scales is None:
-            scales = torch.empty(shape, dtype=u8, device=dev)
+            scales = torch.empty(*shape, dtype=u8, device=dev)
         code = lib().wl_quantize_fp8(_ptr_on(dev, a, a.dtype, "a", a.shape), f32, R, C, block_rows,
                                      _ptr_on(dev, codes, u8, "codes", (R, C)),
                                      _ptr_on(dev, scales, u8, "scales", shape), handle)
@@ -337,7 +337,7 @@ def matmul_fp8(a, b, y=None, stream=None):
     pitch, u8, bf16 = fp8_scale_pitch(K), torch.uint8, torch.bfloat16
     with _On(dev, stream) as handle:
         if y is None:
-            y = torch.empty((M, N), dtype=bf16, device=dev)
+            y = torch.empty(M, N, dtype=bf16, device=dev)
         n = lib().wl_matmul_fp8_workspace(M, N, K)
         ws = _workspace(n, dev)
         code = lib().wl_matmul_fp8(_ptr_on(dev, ac, u8, "a codes", (M, K)), _ptr_on(dev, asc, u8, "a scales", (M, pitch)),
@@ -405,12 +405,12 @@ def stacked_forward_fp8(x, projs, ys=None, checkpoint=False, stream=None):
     M, K = x.shape
     with _On(dev, stream) as handle:
         if ys is None:
-            ys = [torch.empty((M, p[0].shape[0]), dtype=torch.bfloat16, device=dev) for p in projs]
+            ys = [torch.empty(M, p[0].shape[0], dtype=torch.bfloat16, device=dev) for p in projs]
         ckpt = None
         if checkpoint:
-            ckpt = Fp8Checkpoint(torch.empty((M, K), dtype=torch.uint8, device=dev),
-                                 torch.empty((M, fp8_scale_pitch(K)), dtype=torch.uint8, device=dev),
-                                 [torch.empty((M, p[3].shape[1]), dtype=torch.bfloat16, device=dev)
+            ckpt = Fp8Checkpoint(torch.empty(M, K, dtype=torch.uint8, device=dev),
+                                 torch.empty(M, fp8_scale_pitch(K), dtype=torch.uint8, device=dev),
+                                 [torch.empty(M, p[3].shape[1], dtype=torch.bfloat16, device=dev)
                                   if p[3] is not None and p[3].shape[1] else None for p in projs])
         xp, M, K, arr = _forward_fp8_args(x, projs, ys, ckpt.T if ckpt else None)
         n = lib().wl_stacked_forward_fp8_workspace(M, K, arr, len(projs))
@@ -435,7 +435,7 @@ class PreparedForwardFp8:
         dev = _need_cuda(x, "x")
         with _On(dev, None):
             if ys is None:
-                ys = [torch.empty((x.shape[0], p[0].shape[0]), dtype=torch.bfloat16, device=dev) for p in projs]
+                ys = [torch.empty(x.shape[0], p[0].shape[0], dtype=torch.bfloat16, device=dev) for p in projs]
             xp, M, K, arr = _forward_fp8_args(x, projs, ys, None)
             n = lib().wl_stacked_forward_fp8_workspace(M, K, arr, len(projs))
             ws = _workspace(n, dev)
@@ -486,14 +486,14 @@ def stacked_backward_fp8(ckpt, dys, projs, need_dx=True, need_params=True, strea
             w, N, r = _weight_fp8(dev, *p, K)
             ds = dU = dV = None
             if need_params:
-                ds = torch.empty((N,), dtype=torch.float32, device=dev)
+                ds = torch.empty(N, dtype=torch.float32, device=dev)
                 if r:
-                    dU = torch.empty((N, r), dtype=bf16, device=dev)
-                    dV = torch.empty((K, r), dtype=bf16, device=dev)
+                    dU = torch.empty(N, r, dtype=bf16, device=dev)
+                    dV = torch.empty(K, r, dtype=bf16, device=dev)
             per.append((ds, dU, dV))
             arr[i] = _GradFp8(*w, _ptr_on(dev, T, bf16, "T", (M, r)) if r else None, _ptr_on(dev, dy, bf16, "dy", (M, N)),
                               _ptr(ds), _ptr(dU), _ptr(dV), N, r)
-        dx = torch.empty((M, K), dtype=bf16, device=dev) if need_dx else None
+        dx = torch.empty(M, K, dtype=bf16, device=dev) if need_dx else None
         n = lib().wl_stacked_backward_fp8_workspace(M, K, arr, len(projs))
         ws = _workspace(n, dev)
         code = lib().wl_stacked_backward_fp8(xc, xs, M, K, arr, len(projs), _ptr(dx), _ptr(ws), n, handle)

@@ -84,13 +84,12 @@ struct LowrankParams {
 cudaError_t launch_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms, cudaStream_t stream);
 
 // -------------------------------------------------------------------- GEMM ----
-// Tensor-core product over CTA pairs: 256 x 224 output tiles,
+// Tensor-core product over CTA pairs: output tiles of 256 rows x 224, 128 or 64 columns (BN),
 //   out[m][n] = s[n] * sum over parts, k of A[m][k] B[n][k]  +  sum over parts, j of T[m][j] U[n][j]
 // with A in 8 bits (1 x 128 blocks along the contraction) and B in 8 bits
 // (128 x 128 blocks).  The forward has one output per projection, each with
 // one part; dx has one output whose parts are the projections.
 constexpr int kFp8BM = 256;      // rows per CTA pair, 128 per CTA
-constexpr int kFp8BN = 224;      // columns per CTA pair
 constexpr int kFp8GemmThreads = 384;
 constexpr int kFp8Stages = 3;
 constexpr int kFp8BlockBytes = 32768;  // 16 KB of A (or T), up to 16 KB of B (or U)
@@ -118,13 +117,13 @@ struct Fp8Out {
 
 struct Fp8GemmParams {
     CUtensorMap tm_a[kMaxSeg];  // codes, box 128 bytes x 128 rows
-    CUtensorMap tm_b[kMaxSeg];  // codes, box 128 bytes x 112 rows; transposed: x 128 rows
+    CUtensorMap tm_b[kMaxSeg];  // codes, box 128 bytes x BN / 2 rows; transposed: 128, 64 or 32 bytes x 128 rows
     CUtensorMap tm_t[kMaxSeg];  // bf16, box 64 x 128 rows
-    CUtensorMap tm_u[kMaxSeg];  // bf16, box 64 x 112 rows
+    CUtensorMap tm_u[kMaxSeg];  // bf16, box 64 x BN / 2 rows
     Fp8Part part[kMaxSeg];
     Fp8Out out[kMaxSeg];
     int nout;
-    int M;
+    int M, BN;
     int m_tiles, num_tiles;
     int *status;
     unsigned long long timeout_ns;
@@ -136,6 +135,8 @@ enum Fp8Mode {
     kFp8ColSums       // K-major, the epilogue forms column sums: ds
 };
 
+// BN for outputs of N[0..nout) columns and a contraction of `blocks` blocks.
+int fp8_gemm_columns(int M, const int *N, int nout, int blocks, int num_sms);
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, Fp8Mode mode, int num_sms, cudaStream_t stream);
 // ds[n] = sum over rows i < n_rows of sums[i][n].
 cudaError_t launch_fp8_sum_rows(const float *sums, int n_rows, int N, float *ds, cudaStream_t stream);

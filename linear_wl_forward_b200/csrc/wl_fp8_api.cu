@@ -137,19 +137,13 @@ wl_status set_part(Fp8GemmParams &g, int i, const Fp8Mat &A, int M, int a_cols, 
         g.tm_a[i] = g.tm_a[i - 1];
     else
         st = encode_map_2d_u8(&g.tm_a[i], A.codes, a_cols, M, A.ld, 128, 128);
-    if (st == WL_OK) st = encode_map_2d_u8(&g.tm_b[i], B.codes, b_cols, b_rows, B.ld, 128, transposed ? 128 : kFp8BN / 2);
+    if (st == WL_OK) st = encode_map_2d_u8(&g.tm_b[i], B.codes, b_cols, b_rows, B.ld, transposed ? (g.BN > 128 ? 128 : g.BN / 2) : 128,
+                                           transposed ? 128 : g.BN / 2);
     if (st == WL_OK && r > 0) st = encode_map_2d(&g.tm_t[i], T, r, M, r, 64, 128);
-    if (st == WL_OK && r > 0) st = encode_map_2d(&g.tm_u[i], U, r, lr_rows, r, 64, kFp8BN / 2);
+    if (st == WL_OK && r > 0) st = encode_map_2d(&g.tm_u[i], U, r, lr_rows, r, 64, g.BN / 2);
     return st;
 }
 
-void init_gemm(Fp8GemmParams &g, int M, int *status) {
-    std::memset(&g, 0, sizeof g);
-    g.M = M;
-    g.m_tiles = (M + kFp8BM - 1) / kFp8BM;
-    g.status = status;
-    g.timeout_ns = wait_limit_ns();
-}
 
 Fp8Out &add_out(Fp8GemmParams &g, int N, int part0, int nparts) {
     Fp8Out &o = g.out[g.nout++];
@@ -157,7 +151,7 @@ Fp8Out &add_out(Fp8GemmParams &g, int N, int part0, int nparts) {
     o.part0 = part0;
     o.nparts = nparts;
     o.tile_begin = g.num_tiles;
-    g.num_tiles += g.m_tiles * ((N + kFp8BN - 1) / kFp8BN);
+    g.num_tiles += g.m_tiles * ((N + g.BN - 1) / g.BN);
     return o;
 }
 
@@ -168,6 +162,16 @@ struct Device {
     int sms;
     int *status;
 };
+
+// Outputs of M rows x N[0..nout) columns over `blocks` blocks.
+void init_gemm(Fp8GemmParams &g, int M, const int *N, int nout, int blocks, const Device &dev) {
+    std::memset(&g, 0, sizeof g);
+    g.M = M;
+    g.BN = fp8_gemm_columns(M, N, nout, blocks, dev.sms);
+    g.m_tiles = (M + kFp8BM - 1) / kFp8BM;
+    g.status = dev.status;
+    g.timeout_ns = wait_limit_ns();
+}
 
 void init_lowrank(LowrankParams &p, const Device &dev) {
     std::memset(&p, 0, sizeof p);
@@ -268,7 +272,9 @@ wl_status forward_run(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, 
     if (launch_fp8_lowrank(lp, kLowrankRows, dev.sms, stream) != cudaSuccess) return WL_ERR_CUDA;
     if (few) return run_stream(X, M, K, projs, T, P, l.parts, l.counters, true, dev, stream);
     Fp8GemmParams g;
-    init_gemm(g, M, dev.status);
+    int N[kMaxSeg];
+    for (int i = 0; i < P; ++i) N[i] = projs[i].N;
+    init_gemm(g, M, N, P, (K + kFp8Block - 1) / kFp8Block, dev);
     for (int i = 0; i < P; ++i) {
         const wl_proj_fp8 &q = projs[i];
         if (q.N == 0) continue;
@@ -358,8 +364,13 @@ wl_status backward_run(const uint8_t *x_codes, const uint8_t *x_scales, int M, i
     if (st != WL_OK || M == 0) return st;
     const Fp8Mat X{x_codes, x_scales, K, fp8_pitch(K)};
     Fp8GemmParams gx, gs;
-    init_gemm(gx, M, dev.status);
-    init_gemm(gs, M, dev.status);
+    int N[kMaxSeg], blocks = 0;
+    for (int i = 0; i < P; ++i) {
+        N[i] = projs[i].N;
+        blocks += (N[i] + kFp8Block - 1) / kFp8Block;
+    }
+    init_gemm(gx, M, &K, 1, blocks, dev);
+    init_gemm(gs, M, N, P, (K + kFp8Block - 1) / kFp8Block, dev);
     LowrankParams le, lu, lv;
     init_lowrank(le, dev);
     init_lowrank(lu, dev);
@@ -510,7 +521,7 @@ wl_status wl_matmul_fp8(const uint8_t *a_codes, const uint8_t *a_scales, const u
         return run_stream(Fp8Mat{a_codes, a_scales, K, fp8_pitch(K)}, M, K, &q, &T, 1, l.parts, l.counters, false, dev, stream);
     }
     Fp8GemmParams g;
-    init_gemm(g, M, dev.status);
+    init_gemm(g, M, &N, 1, (K + kFp8Block - 1) / kFp8Block, dev);
     if ((st = set_part(g, 0, Fp8Mat{a_codes, a_scales, K, fp8_pitch(K)}, M, K, Fp8Mat{b_codes, b_scales, K, fp8_pitch(K)},
                        N, K, false, nullptr, nullptr, 0, 0)) != WL_OK)
         return st;

@@ -12,9 +12,10 @@
 //
 // A CTA pair owns a 256 x 224 tile: each CTA stages 128 rows of A and 112 of
 // B per block (30 KB against 448 tensor-core cycles; a 128 x 256 tile of one
-// CTA would stage 48 KB against 512, more than L2 delivers).  224 columns,
+// CTA would stage 48 KB against 512).  An SM takes in about 46 bytes per cycle,
+// so the loads (650 cycles per block) bound long products.  224 columns,
 // because two accumulators of that width and the scales fit the 512 columns
-// of TMEM.  The accumulators swap roles from tile to tile: tile i sums into
+// of TMEM; calls with few such tiles take 128 or 64 columns (fp8_gemm_columns).  The accumulators swap roles from tile to tile: tile i sums into
 // region i & 1 and its rank-r term goes to the other region, just before the
 // tile's last blocks, when the epilogue has drained tile i - 1 from there;
 // the epilogue moves the rank-r term into registers while those last blocks
@@ -29,6 +30,7 @@
 //               (32 lanes x 16 bytes per 128 rows), copied to TMEM by the
 //               MMA warp (tcgen05.cp, replicated to the four lane quarters)
 //   warps 4-11  epilogue: four lane quarters x two column halves
+#include <algorithm>
 #include <atomic>
 
 #include "wl_common.cuh"
@@ -39,12 +41,10 @@ namespace wl {
 
 namespace {
 
-constexpr uint32_t kRegionCols = kFp8BN;      // region r at columns r * 224
-constexpr uint32_t kSfCol = 2 * kFp8BN;       // two slots of scales, 16 columns apart: A (4 columns), B (8)
 constexpr uint32_t kABytes = 16384;
-constexpr int kHalf = kFp8BN / 2;             // columns per CTA's half of B, and per epilogue warp
-constexpr int kChunks = kHalf / 16;
-constexpr int kLrLead = 2;                    // main stages issued after the rank-r blocks
+constexpr int kLrLead = 2;           // main stages issued after the rank-r blocks
+constexpr int kStoreStride = 18;     // bf16 of a staged row of 16 outputs (nine banks apart)
+constexpr int kStoreBytes = 32 * kStoreStride * 2;  // per epilogue warp
 
 // ------------------------------------------------------ CTA-pair primitives ----
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -110,6 +110,15 @@ __device__ __forceinline__ void commit_pair(uint64_t *bar) {
         : "memory");
 }
 
+// N-major tile of `bytes` (128, 64 or 32) columns x 128 contraction rows, as
+// TMA leaves it with the swizzle of that width (modes 2, 4, 6): eight rows are
+// 8 * bytes apart.
+__device__ __forceinline__ uint64_t n_major_desc(uint32_t addr, uint32_t bytes) {
+    const uint64_t mode = bytes == 128 ? 2 : bytes == 64 ? 4 : 6;
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(8 * bytes >> 4) << 32 | (uint64_t)1 << 46 |
+           mode << 61;
+}
+
 // ---------------------------------------------------------------- schedule ----
 struct Tile {
     int out, m0, n0;
@@ -118,7 +127,7 @@ __device__ __forceinline__ Tile tile_of(const Fp8GemmParams &p, int t) {
     int o = 0;
     while (o + 1 < p.nout && t >= p.out[o + 1].tile_begin) ++o;
     const int local = t - p.out[o].tile_begin;
-    return {o, (local % p.m_tiles) * kFp8BM, (local / p.m_tiles) * kFp8BN};
+    return {o, (local % p.m_tiles) * kFp8BM, (local / p.m_tiles) * p.BN};
 }
 
 // A tile's work in issue order, up to two blocks (one stage) at a time:
@@ -186,16 +195,22 @@ __device__ __forceinline__ void b_scale_words(const Fp8Part &pt, int N, int n0, 
 
 }  // namespace
 
-template <int kMode>
+template <int kMode, int kBN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams p) {
     constexpr bool kT = kMode == kFp8Transposed;
-    constexpr uint32_t kBBytes = kT ? 16384 : kHalf * 128;
+    constexpr int kHalf = kBN / 2;  // columns per CTA's half of B, and per epilogue warp
+    constexpr int kChunks = kHalf / 16;
+    constexpr uint32_t kRow = kHalf > 64 ? 128 : kHalf;  // bytes of a row of N-major B
+    constexpr uint32_t kUBytes = kHalf * 128, kBBytes = kT ? kRow * 128 : kUBytes;
+    constexpr uint32_t kRegionCols = kBN;  // region r at columns r * kBN
+    constexpr uint32_t kSfCol = 2 * kBN;   // two slots of scales, 16 columns apart: A (4 columns), B (8)
     pdl_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *sf_base = base + kFp8Stages * kFp8StageBytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(sf_base + kFp8SfSlots * kFp8SfBytes);
+    uint8_t *store_base = sf_base + kFp8SfSlots * kFp8SfBytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(store_base + 8 * kStoreBytes);
     uint64_t *empty = full + kFp8Stages;
     uint64_t *sf_full = empty + kFp8Stages;
     uint64_t *sf_empty = sf_full + kFp8SfSlots;
@@ -273,7 +288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
             ok = for_stages(
                 p, p.out[ti.out],
                 [&](int q, int kb, bool two) { return load(&p.tm_a[q], &p.tm_b[q], kb * 128, 128, two, kT, kBBytes); },
-                [&](int q, int j, bool two) { return load(&p.tm_t[q], &p.tm_u[q], j * 64, 64, two, false, kHalf * 128); });
+                [&](int q, int j, bool two) { return load(&p.tm_t[q], &p.tm_u[q], j * 64, 64, two, false, kUBytes); });
         }
         if (!ok && rank == 0 && lane == 0) {
             // Let the copies already issued land before the pair exits; their
@@ -286,13 +301,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
     } else if (warp == 1) {
         // ----------------------------------------------------- MMA issuer ---
         if (rank == 0) {
-            const uint32_t idesc_lr = idesc_bf16_f32(kFp8BM, kFp8BN), idesc0 = idesc_mxf8(kFp8BM, kFp8BN, kT);
-            const uint64_t da0 = sw128_kmajor_desc(smem_addr(base)), db0 = sw128_kmajor_desc(smem_addr(base) + kABytes);
+            const uint32_t idesc_lr = idesc_bf16_f32(kFp8BM, kBN), idesc0 = idesc_mxf8(kFp8BM, kBN, kT);
+            const uint32_t sb = smem_addr(base) + kABytes;
+            const uint64_t da0 = sw128_kmajor_desc(smem_addr(base)), du0 = sw128_kmajor_desc(sb);
+            const uint64_t db0 = kT ? n_major_desc(sb, kRow) : du0;
             const uint64_t sd0 = scale_desc(smem_addr(sf_base));
             constexpr uint64_t kNext = kFp8BlockBytes >> 4;  // a stage's second block
             // 32 columns of the contraction further: 32 bytes inside the swizzled
-            // rows, or (N-major) 32 rows of 128 bytes
-            constexpr uint64_t kStepB = kT ? 256 : 2;
+            // rows, or (N-major) 32 rows
+            constexpr uint64_t kStepB = kT ? 2 * kRow : 2;
             Ring r(kFp8Stages), sr(kFp8SfSlots);
             uint32_t it = 0, lr_count = 0, sf_slot = 0;
             bool ok = true;
@@ -327,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
                             if (chunk) {
                                 cp_scales_pair(sf, ds);
                                 cp_scales_pair(sf + 4, ds + (512 >> 4));
-                                cp_scales_pair(sf + 8, ds + (1024 >> 4));
+                                if (kBN > 128) cp_scales_pair(sf + 8, ds + (1024 >> 4));
                                 commit_pair(&sf_empty[sr.slot]);
                             }
                             mma_mxf8_pair(d_main, da, db, idesc, sf, sf + 4, acc);
@@ -351,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
                         if (!warp_wait(&full[r.slot], r.phase, limits)) return false;
                         tc_fence_after();
                         lr_left -= 1 + two;
-                        const uint64_t da = da0 + r.slot * (kFp8StageBytes >> 4), db = db0 + r.slot * (kFp8StageBytes >> 4);
+                        const uint64_t da = da0 + r.slot * (kFp8StageBytes >> 4), db = du0 + r.slot * (kFp8StageBytes >> 4);
                         if (elect_one()) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k) mma_f16_pair(d_lr, da + 2 * k, db + 2 * k, idesc_lr, !(first && k == 0));
@@ -517,11 +534,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
                                 *reinterpret_cast<uint4 *>(yr + n + 8 * i) =
                                     make_uint4(pack_bf16x2(sc[8 * i], sc[8 * i + 1]), pack_bf16x2(sc[8 * i + 2], sc[8 * i + 3]),
                                                pack_bf16x2(sc[8 * i + 4], sc[8 * i + 5]), pack_bf16x2(sc[8 * i + 6], sc[8 * i + 7]));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (n + i < o.N) yr[n + i] = __float2bfloat16_rn(sc[i]);
                         }
+                    }
+                    if (!vec || n + 16 > o.N) {
+                        // rows that are not 16-byte aligned: 16 lanes per row
+                        __nv_bfloat16 *buf = reinterpret_cast<__nv_bfloat16 *>(store_base + (warp - 4) * kStoreBytes);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            reinterpret_cast<uint32_t *>(buf + lane * kStoreStride)[i] = pack_bf16x2(sc[2 * i], sc[2 * i + 1]);
+                        __syncwarp();
+                        const int col = lane & 15;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const int row = i + (lane >> 4), mr = m - lane + row;
+                            if (mr < p.M && n + col < o.N) o.y[(size_t)mr * o.N + n + col] = buf[row * kStoreStride + col];
+                        }
+                        __syncwarp();
                     }
                 }
             }
@@ -543,25 +571,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
 }
 
 namespace {
-constexpr size_t kGemmSmem = 1024 + kFp8Stages * kFp8StageBytes + kFp8SfSlots * kFp8SfBytes +
+constexpr size_t kGemmSmem = 1024 + kFp8Stages * kFp8StageBytes + kFp8SfSlots * kFp8SfBytes + 8 * kStoreBytes +
                              (2 * kFp8Stages + 2 * kFp8SfSlots + 7) * 8 + 16;
 static_assert(kGemmSmem <= 227 * 1024, "shared memory of one CTA");
+
+using GemmKernel = void (*)(Fp8GemmParams);
+template <int kMode>
+GemmKernel kernel_of(int bn) {
+    return bn == 224 ? fp8_gemm_kernel<kMode, 224> : bn == 128 ? fp8_gemm_kernel<kMode, 128> : fp8_gemm_kernel<kMode, 64>;
+}
 }  // namespace
+
+// The tile width with the least estimated cycles: waves of tiles over the CTA
+// pairs, a block of the contraction at the slowest of the MMAs (2 cycles per
+// column), the loads (46 bytes per cycle) and the issue (330 cycles), and about
+// 5000 cycles to start and drain a tile.  512 x 1152 over 8192: 12 tiles of 224
+// columns take 37 us, 36 of 64 columns 17.
+int fp8_gemm_columns(int M, const int *N, int nout, int blocks, int num_sms) {
+    const int m_tiles = (M + kFp8BM - 1) / kFp8BM, pairs = num_sms / 2;
+    int best = 224;
+    double least = 0;
+    for (int bn : {224, 128, 64}) {
+        long long tiles = 0;
+        for (int i = 0; i < nout; ++i) tiles += (long long)m_tiles * ((N[i] + bn - 1) / bn);
+        const double block = std::max({2.0 * bn, (16384 + 64.0 * bn) / 46, 330.0});
+        const double cost = (double)((tiles + pairs - 1) / pairs) * (blocks * block + 5000);
+        if (least == 0 || cost < least) {
+            least = cost;
+            best = bn;
+        }
+    }
+    return best;
+}
 
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, Fp8Mode mode, int num_sms, cudaStream_t stream) {
     if (p.num_tiles == 0) return cudaSuccess;
-    void (*const kernels[3])(Fp8GemmParams) = {fp8_gemm_kernel<kFp8Plain>, fp8_gemm_kernel<kFp8Transposed>,
-                                               fp8_gemm_kernel<kFp8ColSums>};
+    const GemmKernel kernel = mode == kFp8Plain ? kernel_of<kFp8Plain>(p.BN)
+                              : mode == kFp8Transposed ? kernel_of<kFp8Transposed>(p.BN) : kernel_of<kFp8ColSums>(p.BN);
     // Opt in to the large shared-memory carve-out once per device and kernel.
-    static std::atomic<bool> done[64][3] = {};
+    static std::atomic<bool> done[64][3][3] = {};
+    const int width = p.BN == 224 ? 0 : p.BN == 128 ? 1 : 2;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!done[dev][mode].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(kernels[mode], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
+    if (!done[dev][mode][width].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
         if (e != cudaSuccess) return e;
-        done[dev][mode].store(true, std::memory_order_release);
+        done[dev][mode][width].store(true, std::memory_order_release);
     }
     const int pairs = num_sms / 2 < p.num_tiles ? num_sms / 2 : p.num_tiles;
     cudaLaunchConfig_t cfg = {};
@@ -574,7 +631,7 @@ cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, Fp8Mode mode, int num_sms, c
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernels[mode], p);
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 namespace {

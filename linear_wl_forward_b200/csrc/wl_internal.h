@@ -128,7 +128,7 @@ wl_status encode_map_2d(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t
 // (a multiple of 16), no swizzle.
 wl_status encode_map_2d_u32(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, uint64_t ld_bytes,
                             uint32_t box_cols, uint32_t box_rows);
-// Bytes, 128-byte swizzling (box_cols <= 128); out-of-range reads give 0.
+// Bytes, rows of 128, 64 or 32 (box_cols) with the swizzle of that width; out-of-range reads give 0.
 wl_status encode_map_2d_u8(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, uint64_t ld_bytes,
                            uint32_t box_cols, uint32_t box_rows);
 // n fp32 values, boxes of `box`.

@@ -152,7 +152,9 @@ FORWARD = [
     (3, 272, [17, 0, 129], [8, 16, 0]), (5, 2064, [257], [72]), (8, 1024, [1152], [64]), (16, 1040, [1000, 8], [128, 256]),
     (17, 528, [130], [40]), (33, 144, [449], [8]), (64, 1152, [512, 512], [64, 64]), (100, 640, [225], [16]),
     (128, 512, [224], [0]), (129, 528, [300, 77], [16, 8]), (256, 256, [448], [64]), (333, 2000, [1001, 264, 77], [40, 0, 8]),
-    (600, 384, [700], [320]), (40, 256, [64], [512]), (1, 256, [96], [1024])]
+    (600, 384, [700], [320]), (40, 256, [64], [512]), (1, 256, [96], [1024]),
+    # tiles of 224 and of 128 columns, a second tile per CTA pair
+    (2560, 272, [1568], [72]), (2560, 400, [890], [8]), (2816, 1296, [1121, 1000], [136, 0])]
 
 
 @pytest.mark.parametrize("M,K,N,r", FORWARD)
@@ -181,7 +183,9 @@ def test_forward(M, K, N, r):
 @pytest.mark.parametrize("M,K,N,r", [
     (1, 16, [1], [8]), (1, 128, [128], [0]), (2, 1152, [1024, 256, 256], [16, 16, 16]), (5, 272, [17, 0, 129], [8, 16, 0]),
     (64, 1152, [512, 512], [64, 64]), (127, 528, [130], [40]), (200, 144, [449], [72]), (257, 640, [225, 31], [256, 8]),
-    (333, 2000, [301, 264, 77], [40, 0, 8]), (512, 384, [700], [320]), (130, 256, [96], [1024])])
+    (333, 2000, [301, 264, 77], [40, 0, 8]), (512, 384, [700], [320]), (130, 256, [96], [1024]),
+    # tiles of 224 and of 128 columns, a second tile per CTA pair
+    (2560, 1568, [300, 77], [72, 0]), (2560, 896, [140], [16]), (2560, 272, [1568], [16]), (2816, 2128, [400, 1121], [136, 8])])
 def test_backward(M, K, N, r):
     g = gen(M * 11 + K)
     x = tokens(g, M, K)
