@@ -143,6 +143,7 @@ cudaError_t launch_fp8_sum_rows(const float *sums, int n_rows, int N, float *ds,
 
 // ------------------------------------------------------- few-token stream ----
 constexpr int kFp8StreamMaxM = 128;
+constexpr int kFp8StreamMaxCluster = 16;
 constexpr int kFp8StreamMaxGrid = 148;  // CTAs, whatever the device: the cut is made before one is known, and no CTA waits for another
 
 struct Fp8StreamSeg {
@@ -168,9 +169,12 @@ struct Fp8StreamParams {
     int nseg, M;
     int early;  // the weights may be read before the wait for the previous kernel
     // plan
-    int Mp, stages, grid, by_tile, tiles;
-    long long units;
-    float *parts;            // [grid][2][Mp][128]
+    int Mp, stages, grid, tiles;
+    int whole;               // tiles [0, whole) go to one CTA (or cluster) each
+    int cluster;             // CTAs per whole tile; above 1 all tiles are whole
+    int cut_ctas;            // CTAs that share the others
+    long long units, cut_unit;  // units, and those of the whole tiles
+    float *parts;            // [cut_ctas][2][Mp][128]
     unsigned int *counters;  // [tiles], zero
     int *status;
     unsigned long long timeout_ns;

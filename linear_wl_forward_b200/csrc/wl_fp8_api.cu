@@ -474,7 +474,7 @@ MatmulLayout matmul_layout(int M, int N, int K, void *ws) {
         const int r = 0;
         Fp8StreamParams sp;
         plan_stream(sp, M, K, &N, &r, 1);
-        l.tiles = sp.by_tile ? 0 : sp.tiles;
+        l.tiles = sp.whole == sp.tiles ? 0 : sp.tiles;
         l.parts = a.take<float>(fp8_stream_part_floats(sp));
         l.counters = a.take<unsigned int>(l.tiles);
     }

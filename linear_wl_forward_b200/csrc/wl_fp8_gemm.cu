@@ -47,20 +47,6 @@ constexpr int kStoreStride = 18;     // bf16 of a staged row of 16 outputs (nine
 constexpr int kStoreBytes = 32 * kStoreStride * 2;  // per epilogue warp
 
 // ------------------------------------------------------ CTA-pair primitives ----
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-// shared::cluster address of `p` in the pair's CTA `rank`
-__device__ __forceinline__ uint32_t map_rank(const void *p, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-    return a;
-}
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }

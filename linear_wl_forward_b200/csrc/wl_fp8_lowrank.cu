@@ -54,21 +54,6 @@ __device__ __forceinline__ uint64_t mn_major_desc(uint32_t addr) {
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-__device__ __forceinline__ uint32_t ctarank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float ld_cluster(uint32_t local_addr, uint32_t rank) {
-    uint32_t a;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local_addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
-}
 // Two E4M3 codes (low byte first) times a power of two, as a pair of bf16.
 __device__ __forceinline__ uint32_t expand_pair(uint32_t codes, float scale) {
     uint32_t h;
@@ -144,7 +129,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = p.split;
-    const uint32_t rank = S > 1 ? ctarank() : 0;
+    const uint32_t rank = S > 1 ? cluster_ctarank() : 0;
     const int unit = blockIdx.x / S;
     int jx = 0;
     while (jx + 1 < p.njobs && unit >= p.job[jx + 1].tile_begin) ++jx;
@@ -332,12 +317,13 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
     }
     if (S > 1) {
         __syncwarp();
-        cluster_barrier();  // every CTA's sums are in its shared memory
+        cluster_sync();  // every CTA's sums are in its shared memory
         if (warp >= 2 && warp < 6 && ok) {
             const int tid_epilogue = threadIdx.x - 64;
             // groups of eight columns go round the ranks; with few rows several
             // threads take the columns of one row
             const int rows = min(128, jb.I - i0);
+            const float *sums = reinterpret_cast<const float *>(base);
             if (rows > 32) {
                 const int row = tid_epilogue;
                 for (int c = (int)rank * 8; c < width; c += 8 * S) {
@@ -346,14 +332,14 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
                         for (int s = 0; s < S; ++s)
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                v[k] += ld_cluster(smem_addr(base) + (uint32_t)((c + k) * 128 + row) * 4, s);
+                                v[k] += ld_cluster(sums + (c + k) * 128 + row, s);
                     write8(jb, i0 + row, j0 + c, v);
                 }
             } else {
                 const int groups = (width / 8 - (int)rank + S - 1) / S;
                 for (int t = tid_epilogue; t < rows * groups * 8; t += 128) {
                     const int row = t % rows, c = ((int)rank + t / rows / 8 * S) * 8 + t / rows % 8;
-                    const uint32_t at = smem_addr(base) + (uint32_t)(c * 128 + row) * 4;
+                    const float *at = sums + c * 128 + row;
                     float v = 0.f;
                     for (int s0 = 0; s0 < S; s0 += 4) {
                         float part[4];
@@ -370,7 +356,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
             }
         }
         __syncwarp();
-        cluster_barrier();  // no CTA leaves while its sums are read
+        cluster_sync();  // no CTA leaves while its sums are read
     }
     tc_fence_before();
     __syncthreads();

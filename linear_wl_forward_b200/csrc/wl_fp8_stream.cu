@@ -9,11 +9,14 @@
 // issuing warp's instructions come next (about 40 cycles per MMA, 70 per wait,
 // 46 per commit), so a stage holds two blocks.
 //
-// The call's work (per tile: the contraction in pairs of blocks, then U's
-// 64-column blocks in pairs) forms one list of units that is cut evenly over
-// the CTAs, one per SM, so the stream has no tail; a tile cut between CTAs is summed by the CTA that
-// completes it, from fp32 parts s * z + d in CTA order (reproducible).  Short
-// calls are cut at tiles instead, which needs no exchange (plan below).
+// A tile is a list of units (the contraction in pairs of blocks, then U's
+// 64-column blocks in pairs).  Every CTA, one per SM, takes the same number of
+// whole tiles; the tiles left over are cut evenly over the CTAs, so the stream
+// has no tail, and done first, so that the exchange hides behind the whole
+// ones: a cut tile is summed by the CTA that completes it, from fp32 parts
+// s * z + d in CTA order (reproducible).  A call with fewer tiles than SMs gives
+// each tile to a cluster (up to 16 CTAs), whose sums meet over distributed
+// shared memory, again in rank order.
 //
 //   warp 0  TMA producer (up to 6 stages of two blocks; weights are fetched before the wait
 //           for the kernel that makes x and T)
@@ -47,42 +50,61 @@ __device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
 }
 // A run of units of one tile: [u0, u1) of the tile's own.
 struct Segment {
-    int seg, tile, u0, u1, nu;  // nu: the tile's units
+    int seg, tile, u0, u1, nu;  // tile: of its projection; nu: the tile's units
     long long t0;               // first unit of the tile in the call's list
+    bool first;                 // the CTA's first piece of the cut tiles
 };
 
-__device__ __forceinline__ Segment segment_at(const Fp8StreamParams &p, long long u, long long end) {
+__device__ __forceinline__ Segment whole_tile(const Fp8StreamParams &p, int tile) {
     int sp = 0;
-    while (sp + 1 < p.nseg && u >= p.seg[sp + 1].unit_begin) ++sp;
+    while (sp + 1 < p.nseg && tile >= p.seg[sp + 1].tile_begin) ++sp;
     const Fp8StreamSeg &sg = p.seg[sp];
-    Segment s;
-    s.seg = sp;
-    s.nu = sg.units;
-    const long long local = u - sg.unit_begin;
-    s.tile = (int)(local / sg.units);
-    s.u0 = (int)(local - (long long)s.tile * sg.units);
-    s.u1 = (int)min((long long)sg.units, s.u0 + (end - u));
-    s.t0 = sg.unit_begin + (long long)s.tile * sg.units;
-    return s;
+    const int local = tile - sg.tile_begin;
+    return {sp, local, 0, sg.units, sg.units, sg.unit_begin + (long long)local * sg.units, false};
 }
 
-// First unit of CTA c.
-__device__ __forceinline__ long long range_begin(const Fp8StreamParams &p, int c) {
-    if (!p.by_tile) return p.units * c / (int)gridDim.x;
-    // whole tiles: tile t of the call starts CTA c's share
-    const int t = (int)((long long)p.tiles * c / (int)gridDim.x);
-    if (t >= p.tiles) return p.units;
-    int sp = 0;
-    while (sp + 1 < p.nseg && t >= p.seg[sp + 1].tile_begin) ++sp;
-    return p.seg[sp].unit_begin + (long long)(t - p.seg[sp].tile_begin) * p.seg[sp].units;
+// First unit of CTA c's share of the cut tiles.
+__device__ __forceinline__ long long cut_begin(const Fp8StreamParams &p, int c) {
+    return p.cut_unit + (p.units - p.cut_unit) * min(c, p.cut_ctas) / p.cut_ctas;
 }
 
-__device__ __forceinline__ int cta_of(const Fp8StreamParams &p, long long u) {
-    int c = (int)(u * (int)gridDim.x / p.units);
-    while (c + 1 < (int)gridDim.x && range_begin(p, c + 1) <= u) ++c;
-    while (c > 0 && range_begin(p, c) > u) --c;
+// The CTA whose share holds unit u of the cut tiles.
+__device__ __forceinline__ int cut_cta(const Fp8StreamParams &p, long long u) {
+    int c = (int)((u - p.cut_unit) * p.cut_ctas / (p.units - p.cut_unit));
+    while (c + 1 < p.cut_ctas && cut_begin(p, c + 1) <= u) ++c;
+    while (c > 0 && cut_begin(p, c) > u) --c;
     return c;
 }
+
+// The CTA's segments: its share of the cut tiles, then its whole tiles.
+struct Walk {
+    long long begin, u, end;
+    int tile;
+    __device__ explicit Walk(const Fp8StreamParams &p)
+        : begin(cut_begin(p, blockIdx.x)), u(begin), end(cut_begin(p, blockIdx.x + 1)), tile(blockIdx.x / p.cluster) {}
+    __device__ bool next(const Fp8StreamParams &p, Segment &s) {
+        if (u < end) {
+            int sp = 0;
+            while (sp + 1 < p.nseg && u >= p.seg[sp + 1].unit_begin) ++sp;
+            const Fp8StreamSeg &sg = p.seg[sp];
+            const int tile = (int)((u - sg.unit_begin) / sg.units);
+            s = {sp, tile, 0, 0, sg.units, sg.unit_begin + (long long)tile * sg.units, u == begin};
+            s.u0 = (int)(u - s.t0);
+            s.u1 = (int)min((long long)sg.units, s.u0 + (end - u));
+            u += s.u1 - s.u0;
+            return true;
+        }
+        if (tile >= p.whole) return false;
+        s = whole_tile(p, tile);
+        if (p.cluster > 1) {  // this rank's part of it
+            const int rank = (int)cluster_ctarank();
+            s.u0 = s.nu * rank / p.cluster;
+            s.u1 = s.nu * (rank + 1) / p.cluster;
+        }
+        tile += gridDim.x / p.cluster;
+        return true;
+    }
+};
 
 }  // namespace
 
@@ -104,11 +126,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
     volatile int *last_flag = abort_flag + 1;
     const WaitLimits limits{p.status, p.timeout_ns, abort_flag};
 
-    // TMEM columns: two sums of W0 x, one of U T, two slots of 8 for scales
+    // TMEM columns: two sums of W0 x, one of U T,
+    // two slots of 8 for scales
     const uint32_t set_cols = (uint32_t)max(p.Mp, 32), d_col = 2 * set_cols, sf_col = 3 * set_cols;
     const uint32_t tmem_cols = sf_col + 16 <= 128 ? 128 : sf_col + 16 <= 256 ? 256 : 512;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long begin = range_begin(p, blockIdx.x), end = range_begin(p, blockIdx.x + 1);
 
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < stages; ++i) {
@@ -139,15 +161,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
         // ------------------------------------------------------ producer ----
         // weights of the first `stages` units, then (x and T made) their
         // operands, then the rest in order
-        const uint32_t total = (uint32_t)(end - begin), head = p.early ? min(total, stages) : 0;
+        const uint32_t head = p.early ? stages : 0;
         uint32_t issued = 0;
         bool ok = true;
         for (int pass = p.early ? 0 : 1; pass < 2 && ok; ++pass) {
             // pass 0: weights of units [0, head); pass 1: everything else
             if (pass == 1) pdl_wait_primary();
             uint32_t i = 0, slot = 0, ph = 0;
-            for (long long u = begin; u < end && ok && (pass == 1 || i < head);) {
-                const Segment s = segment_at(p, u, end);
+            Walk walk(p);
+            for (Segment s; ok && (pass == 1 || i < head) && walk.next(p, s);) {
                 const Fp8StreamSeg &sg = p.seg[s.seg];
                 const int n0 = s.tile * 128;
                 for (int b = s.u0; b < s.u1 && (pass == 1 || i < head); ++b, ++i) {
@@ -172,7 +194,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
                     issued += weights;
                     if (++slot == stages) slot = 0, ph ^= 1u;
                 }
-                u += s.u1 - s.u0;
             }
         }
         if (!ok && lane == 0) {  // let the copies already issued land before the CTA exits
@@ -188,8 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
         const uint64_t sd0 = scale_desc(smem_addr(sf_base)), next = block_bytes >> 4;
         uint32_t slot = 0, ph = 0, count = 0, chunk = 0;
         bool ok = true;
-        for (long long u = begin; u < end && ok; ++count) {
-            const Segment s = segment_at(p, u, end);
+        Walk walk(p);
+        for (Segment s; ok && walk.next(p, s); ++count) {
             const Fp8StreamSeg &sg = p.seg[s.seg];
             const uint32_t set = count & 1u, d_main = tmem + set * set_cols, d_lr = tmem + d_col;
             if (count >= 2) ok = warp_wait(&acc_empty[set], ((count >> 1) - 1) & 1u, limits);
@@ -247,7 +268,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
             }
             if (ok && elect_one()) tc_commit(&acc_full[set]);
             __syncwarp();
-            u += s.u1 - s.u0;
         }
         if (elect_one()) {
             tc_commit(drain);
@@ -258,8 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
         // --------------------------------------------------------- scales ---
         uint32_t chunk = 0;
         bool ok = true;
-        for (long long u = begin; u < end && ok;) {
-            const Segment s = segment_at(p, u, end);
+        Walk walk(p);
+        for (Segment s; ok && walk.next(p, s);) {
             const Fp8StreamSeg &sg = p.seg[s.seg];
             const uint8_t *wrow = sg.w_scales + (size_t)s.tile * p.pitch;
             for (int b = s.u0; b < min(s.u1, sg.kpairs); b = (b & ~1) + 2) {
@@ -283,7 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sf_full[chunk & 1u]);
             }
-            u += s.u1 - s.u0;
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------- epilogue ---
@@ -291,12 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
         const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
         const size_t part_stride = (size_t)p.Mp * 128;
         uint32_t count = 0;
-        for (long long u = begin; u < end; ++count) {
-            const Segment s = segment_at(p, u, end);
+        Walk walk(p);
+        for (Segment s; walk.next(p, s); ++count) {
             const Fp8StreamSeg &sg = p.seg[s.seg];
             const uint32_t set = count & 1u;
             const bool whole = s.u0 == 0 && s.u1 == s.nu;
-            const bool has_z = s.u0 < sg.kpairs, has_d = s.u1 > sg.kpairs;
+            const bool has_z = s.u0 < min(s.u1, sg.kpairs), has_d = s.u1 > max(s.u0, sg.kpairs);  // neither: a rank without units
             bool ok = warp_wait(&acc_full[set], (count >> 1) & 1u, limits);
             {
                 // the four warps meet below: they go on, or stop, together
@@ -316,28 +335,47 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
             const bool in = n < sg.N;
             const float sc = sg.s && in ? __ldg(sg.s + n) : 1.f;
             // which of the CTA's two partial tiles this is: its first, or its last
-            float *part = p.parts + ((size_t)blockIdx.x * 2 + (u == begin ? 0 : 1)) * part_stride;
-            for (int c = 0; c < p.M; c += 8) {
-                uint32_t z[8], d[8];
-                if (has_z) tmem_ld8(lane_addr + set * set_cols + c, z);
-                if (has_d) tmem_ld8(lane_addr + d_col + c, d);
-                tmem_ld_wait();
+            // where a piece's sums go: the idle stages, for the cluster, or one of
+            // the CTA's two parts in memory
+            float *part = p.cluster > 1 ? reinterpret_cast<float *>(base)
+                                        : p.parts + ((size_t)blockIdx.x * 2 + (s.first ? 0 : 1)) * part_stride;
+            // 16 tokens per step; the stores are predicated, not branched around
+            auto drain_tokens = [&](auto store) {
+                for (int c = 0; c < p.M; c += 16) {
+                    uint32_t z[16], d[16];
+                    if (has_z) tmem_ld16(lane_addr + set * set_cols + c, z);
+                    if (has_d) tmem_ld16(lane_addr + d_col + c, d);
+                    tmem_ld_wait();
+                    float v[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float zf = has_z ? __uint_as_float(z[i]) : 0.f, df = has_d ? __uint_as_float(d[i]) : 0.f;
-                    const float v = has_z ? fmaf(sc, zf, df) : df;
-                    if (whole) {
-                        if (in && c + i < p.M) sg.y[(size_t)(c + i) * sg.N + n] = __float2bfloat16_rn(v);
-                    } else if (c + i < p.M) {
-                        part[(c + i) * 128 + row] = v;
+                    for (int i = 0; i < 16; ++i) {
+                        v[i] = has_d ? __uint_as_float(d[i]) : 0.f;
+                        if (has_z) v[i] = fmaf(sc, __uint_as_float(z[i]), v[i]);
                     }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) store(c + i, v[i]);
                 }
+            };
+            if (whole) {
+                __nv_bfloat16 *y = sg.y + n;
+                const size_t ld = sg.N;
+                const int tokens = in ? p.M : 0;
+                drain_tokens([&](int m, float v) {
+                    if (m < tokens) *y = __float2bfloat16_rn(v);
+                    y += ld;
+                });
+            } else {
+                float *q = part + row;
+                drain_tokens([&](int m, float v) {
+                    if (m < p.M) *q = v;
+                    q += 128;
+                });
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[set]);
-            if (!whole) {
-                const int c0 = cta_of(p, s.t0), c1 = cta_of(p, s.t0 + s.nu - 1);
+            if (!whole && p.cluster == 1) {
+                const int c0 = cut_cta(p, s.t0), c1 = cut_cta(p, s.t0 + s.nu - 1);
                 __threadfence();
                 asm volatile("bar.sync 2, 128;" ::: "memory");
                 if (threadIdx.x == 128)
@@ -346,29 +384,64 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
                 if (*last_flag) {
                     __threadfence();
                     // the tile is the last piece of its first CTA (or all of
-                    // that CTA's range so far), the first piece of the others
-                    const float *first = p.parts + ((size_t)c0 * 2 + (range_begin(p, c0) < s.t0 ? 1 : 0)) * part_stride + row;
-                    for (int m = 0; m < p.M; m += 4) {
-                        float v[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = m + i < p.M ? __ldcg(first + (m + i) * 128) : 0.f;
-                        for (int k = c0 + 1; k <= c1; ++k) {
-                            const float *q = p.parts + (size_t)k * 2 * part_stride + row;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (m + i < p.M) v[i] += __ldcg(q + (m + i) * 128);
-                        }
+                    // that CTA's share so far), the first piece of the others.
+                    // A lane adds four rows of a token, a warp every fourth
+                    // token, the parts of four tokens in flight at a time.
+                    const float *first = p.parts + ((size_t)c0 * 2 + (cut_begin(p, c0) < s.t0 ? 1 : 0)) * part_stride + lane * 4;
+                    const int rows0 = s.tile * 128 + lane * 4;
+                    for (int m0 = warp - 4; m0 < p.M; m0 += 16) {
+                        float4 v[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (in && m + i < p.M) sg.y[(size_t)(m + i) * sg.N + n] = __float2bfloat16_rn(v[i]);
+                            v[i] = m0 + 4 * i < p.M ? __ldcg(reinterpret_cast<const float4 *>(first + (m0 + 4 * i) * 128)) : make_float4(0, 0, 0, 0);
+#pragma unroll 4
+                        for (int k = c0 + 1; k <= c1; ++k) {
+                            const float *part_k = p.parts + (size_t)k * 2 * part_stride + lane * 4;
+                            float4 a[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                a[i] = m0 + 4 * i < p.M ? __ldcg(reinterpret_cast<const float4 *>(part_k + (m0 + 4 * i) * 128)) : make_float4(0, 0, 0, 0);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[i].x += a[i].x, v[i].y += a[i].y, v[i].z += a[i].z, v[i].w += a[i].w;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float r[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (m0 + 4 * i < p.M && rows0 + k < sg.N) sg.y[(size_t)(m0 + 4 * i) * sg.N + rows0 + k] = __float2bfloat16_rn(r[k]);
+                        }
                     }
                 }
                 asm volatile("bar.sync 2, 128;" ::: "memory");  // last_flag is used again
             }
-            u += s.u1 - s.u0;
         }
     }
 
+    if (p.cluster > 1) {
+        __syncwarp();
+        cluster_sync();  // every rank's sums are in its shared memory
+        if (warp >= 4) {
+            const Segment s = whole_tile(p, blockIdx.x / p.cluster);
+            const Fp8StreamSeg &sg = p.seg[s.seg];
+            const int row = threadIdx.x - 128, n = s.tile * 128 + row, C = p.cluster;
+            const float *sums = reinterpret_cast<const float *>(base) + row;
+            // tokens go round the ranks, four at a time
+            for (int m0 = (int)cluster_ctarank(); m0 < p.M; m0 += 4 * C) {
+                float v[4] = {};
+#pragma unroll 4
+                for (int r = 0; r < C; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (m0 + i * C < p.M) v[i] += ld_cluster(sums + (m0 + i * C) * 128, r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (m0 + i * C < p.M && n < sg.N) sg.y[(size_t)(m0 + i * C) * sg.N + n] = __float2bfloat16_rn(v[i]);
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while its sums are read
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -379,12 +452,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
 
 static int fp8_stream_stage(const Fp8StreamParams &p) { return 2 * ((int)kWBytes + p.Mp * 128); }
 
-// CTAs and the cut of the list.  Cutting at tiles leaves SMs idle when the
-// tiles are few; cutting evenly costs an exchange, about as long as five units
-// take one SM whose loads have the memory to themselves (about 500 cycles per
-// unit; 1400 when all 148 SMs stream).
+// More tiles than SMs: whole ones for every CTA, the rest cut.  Fewer: the
+// cluster size with the least estimated cycles among those that are resident
+// at once, a unit coming at 42 bytes per cycle and SM, or in 1400 cycles when
+// all SMs stream, and the exchange taking about 4000 and 30 per token.
+// (5376 x 21504 at one token: 42 tiles whole 37 us, cut over 148 CTAs with
+// their parts in memory 31, in clusters of three 22.)
 void plan_fp8_stream(Fp8StreamParams &p) {
-    constexpr int num_sms = kFp8StreamMaxGrid;
+    constexpr int kSms = kFp8StreamMaxGrid;
+    // clusters of 1, 2, .. 16 CTAs, one CTA per SM, that a B200 holds at once
+    static const int kResident[kFp8StreamMaxCluster] = {148, 74, 45, 33, 26, 22, 15, 15, 15, 11, 7, 7, 7, 7, 7, 7};
     long long units = 0;
     int tiles = 0, longest = 0;
     for (int i = 0; i < p.nseg; ++i) {
@@ -398,20 +475,43 @@ void plan_fp8_stream(Fp8StreamParams &p) {
         units += (long long)t * sg.units;
         longest = std::max(longest, sg.units);
     }
-    p.units = units;
+    p.units = p.cut_unit = units;
     p.tiles = tiles;
-    const int by_tile = std::min(tiles, num_sms), even = (int)std::min<long long>(units, num_sms);
-    auto block = [&](int ctas) { return std::max(500.0, 1400.0 * ctas / num_sms); };
-    const double cost_tile = (double)((tiles + by_tile - 1) / by_tile) * longest * block(by_tile);
-    const double cost_even = (double)((units + even - 1) / even) * block(even) + 2500;
-    p.by_tile = cost_tile <= cost_even;
-    p.grid = p.by_tile ? by_tile : even;
     p.Mp = (p.M + 15) / 16 * 16;
+    p.cluster = p.cut_ctas = 1;
+    if (tiles <= kSms) {
+        p.whole = tiles;
+        double least = 0;
+        for (int c = 1; c <= kFp8StreamMaxCluster && c <= longest; ++c) {
+            if (tiles > kResident[c - 1]) continue;
+            const double unit = std::max(fp8_stream_stage(p) / 42.0, 1400.0 * c * tiles / kSms);
+            const double cost = (longest + c - 1) / c * unit + (c > 1 ? 4000 + 30.0 * p.M : 0);
+            if (least == 0 || cost < least) {
+                least = cost;
+                p.cluster = c;
+            }
+        }
+        p.grid = tiles * p.cluster;
+    } else {
+        p.whole = tiles / kSms * kSms;
+        p.grid = kSms;
+        for (int i = 0; i < p.nseg; ++i) {
+            const Fp8StreamSeg &sg = p.seg[i];
+            const int end = i + 1 < p.nseg ? p.seg[i + 1].tile_begin : tiles;
+            if (p.whole >= sg.tile_begin && p.whole < end)
+                p.cut_unit = sg.unit_begin + (long long)(p.whole - sg.tile_begin) * sg.units;
+        }
+        // a share is a good part of a tile, the larger the more tokens a part holds
+        const long long share = std::max(2, longest / (p.M <= 16 ? 8 : 4));
+        p.cut_ctas = (int)std::min<long long>(kSms, std::max<long long>(1, (units - p.cut_unit) / share));
+    }
     // up to 32 tokens 150 KB hold enough in flight and leave room for the rank-r kernel beside
     p.stages = std::min(6, ((p.Mp <= 32 ? 150 : 200) * 1024) / fp8_stream_stage(p));
 }
 
-size_t fp8_stream_part_floats(const Fp8StreamParams &p) { return p.by_tile ? 0 : (size_t)p.grid * 2 * p.Mp * 128; }
+size_t fp8_stream_part_floats(const Fp8StreamParams &p) {
+    return p.whole == p.tiles ? 0 : (size_t)p.cut_ctas * 2 * p.Mp * 128;
+}
 
 cudaError_t launch_fp8_stream(const Fp8StreamParams &p, cudaStream_t stream) {
     if (p.units == 0) return cudaSuccess;
@@ -424,6 +524,7 @@ cudaError_t launch_fp8_stream(const Fp8StreamParams &p, cudaStream_t stream) {
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!done[dev].load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(fp8_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(fp8_stream_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         done[dev].store(true, std::memory_order_release);
     }
@@ -432,11 +533,14 @@ cudaError_t launch_fp8_stream(const Fp8StreamParams &p, cudaStream_t stream) {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, fp8_stream_kernel, p);
 }
 

@@ -153,6 +153,8 @@ FORWARD = [
     (17, 528, [130], [40]), (33, 144, [449], [8]), (64, 1152, [512, 512], [64, 64]), (100, 640, [225], [16]),
     (128, 512, [224], [0]), (129, 528, [300, 77], [16, 8]), (256, 256, [448], [64]), (333, 2000, [1001, 264, 77], [40, 0, 8]),
     (600, 384, [700], [320]), (40, 256, [64], [512]), (1, 256, [96], [1024]),
+    # few tokens: whole tiles for every CTA, and tiles cut between them
+    (2, 272, [19500, 300], [8, 16]), (20, 144, [40000], [0]), (1, 4112, [130], [0]), (128, 1040, [20000], [136]),
     # tiles of 224 and of 128 columns, a second tile per CTA pair
     (2560, 272, [1568], [72]), (2560, 400, [890], [8]), (2816, 1296, [1121, 1000], [136, 0])]
 
