@@ -357,6 +357,20 @@ wl_status wl_stacked_forward_fp8(const wl_bf16 *x, int M, int K, const wl_proj_f
  * the forward refuses. */
 size_t wl_stacked_forward_fp8_workspace(int M, int K, const wl_proj_fp8 *projs, int P);
 
+/* A forward call set up once for a program that repeats it on the same
+ * buffers (a decode step): the arguments are checked and the tensor maps
+ * made here, and running the plan only launches.  Same arguments and errors
+ * as wl_stacked_forward_fp8; WL_ERR_NOMEM if host memory runs out.  The plan
+ * belongs to the device that is current when it is made (it must be current
+ * when it runs) and keeps the addresses, not the memory.  Runs of one plan use
+ * one workspace, so they must not overlap on the GPU. */
+typedef struct wl_fp8_plan wl_fp8_plan;
+wl_status wl_plan_stacked_forward_fp8(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, int P,
+                                      uint8_t *x_codes, uint8_t *x_scales, void *workspace,
+                                      size_t workspace_bytes, wl_fp8_plan **plan);
+wl_status wl_run_fp8_plan(wl_fp8_plan *plan, void *stream);
+void wl_free_fp8_plan(wl_fp8_plan *plan); /* NULL is allowed */
+
 /* One projection of a backward call.  ds, dU, dV may be NULL (not wanted). */
 typedef struct {
     const uint8_t *codes, *scales; /* W0 as in wl_proj_fp8                      */

@@ -126,6 +126,11 @@ def lib():
         L.wl_stacked_forward_fp8_workspace.argtypes = [ci, ci, ctypes.POINTER(_ProjFp8), ci]
         L.wl_stacked_backward_fp8.argtypes = [vp, vp, ci, ci, ctypes.POINTER(_GradFp8), ci, vp, vp, sz, vp]
         L.wl_stacked_backward_fp8_workspace.argtypes = [ci, ci, ctypes.POINTER(_GradFp8), ci]
+        L.wl_plan_stacked_forward_fp8.argtypes = [vp, ci, ci, ctypes.POINTER(_ProjFp8), ci, vp, vp, vp, sz,
+                                                  ctypes.POINTER(vp)]
+        L.wl_run_fp8_plan.argtypes = [vp, vp]
+        L.wl_free_fp8_plan.argtypes = [vp]
+        L.wl_free_fp8_plan.restype = None
         for name in ("wl_matmul_fp8_workspace", "wl_stacked_forward_fp8_workspace",
                      "wl_stacked_backward_fp8_workspace"):
             getattr(L, name).restype = sz
@@ -144,7 +149,7 @@ def lib():
                      "wl_materialize_weight", "wl_describe_decode_plan", "wl_describe_rows_plan",
                      "wl_describe_nvfp4_plan",
                      "wl_quantize_nvfp4", "wl_quantize_fp8", "wl_matmul_fp8", "wl_stacked_forward_fp8",
-                     "wl_stacked_backward_fp8",
+                     "wl_stacked_backward_fp8", "wl_plan_stacked_forward_fp8", "wl_run_fp8_plan",
                      "wl_last_device_status", "wl_wait_probe", "wl_set_wait_limit", "wl_noalloc_last_status"):
             getattr(L, name).restype = ci
         _lib = L
@@ -422,12 +427,15 @@ def stacked_forward_fp8(x, projs, ys=None, checkpoint=False, stream=None):
 
 
 class PreparedForwardFp8:
-    """stacked_forward_fp8 with its tensors checked and its workspace
-    allocated once; calling it issues the forward on `stream` (default:
-    torch's current stream) and returns the list of y_p.  The tensors are kept
-    alive and their storage must not be replaced.  Calls of one handle share
-    its workspace, so they must not overlap on the GPU; handles do not share
-    anything."""
+    """stacked_forward_fp8 set up once (include/wl.h,
+    wl_plan_stacked_forward_fp8): its tensors are checked, its workspace is
+    allocated and its tensor maps are made here; calling it only launches, on
+    `stream` (default: torch's current stream), and returns the list of y_p.
+    The tensors are kept alive and their storage must not be replaced.  Calls
+    of one handle share its workspace, so they must not overlap on the GPU;
+    handles do not share anything."""
+
+    _plan = None
 
     def __init__(self, x, projs, ys=None):
         import torch
@@ -439,11 +447,14 @@ class PreparedForwardFp8:
             xp, M, K, arr = _forward_fp8_args(x, projs, ys, None)
             n = lib().wl_stacked_forward_fp8_workspace(M, K, arr, len(projs))
             ws = _workspace(n, dev)
+            plan = ctypes.c_void_p()
+            _check(lib().wl_plan_stacked_forward_fp8(xp, M, K, arr, len(projs), None, None, _ptr(ws), n,
+                                                     ctypes.byref(plan)), "wl_plan_stacked_forward_fp8")
         self.ys = ys
         self._keep = (x, projs, ws)
         self._device = dev
-        self._args = (xp, M, K, arr, len(projs), None, None, _ptr(ws), n)
-        self._fn = lib().wl_stacked_forward_fp8
+        self._plan = plan
+        self._run = lib().wl_run_fp8_plan
 
     def __call__(self, stream=None):
         import torch
@@ -452,8 +463,14 @@ class PreparedForwardFp8:
             with torch.cuda.device(self._device):
                 return self(stream)
         handle = torch._C._cuda_getCurrentRawStream(self._device.index) if stream is None else _stream_handle(stream)
-        _check(self._fn(*self._args, handle), "wl_stacked_forward_fp8")
+        code = self._run(self._plan, handle)
+        if code:
+            _check(code, "wl_run_fp8_plan")
         return self.ys
+
+    def __del__(self):
+        if self._plan is not None and _lib is not None:
+            _lib.wl_free_fp8_plan(self._plan)
 
 
 def prepare_stacked_fp8(x, projs, ys=None) -> PreparedForwardFp8:

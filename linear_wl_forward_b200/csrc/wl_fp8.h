@@ -24,12 +24,28 @@ struct Fp8Mat {
 
 // ----------------------------------------------------------- quantisation ----
 // 1 x 128 blocks of rows of `a` (bf16 or fp32, `lda` elements apart), each
-// element times colscale[column] first (nullptr: 1, bf16 only).  Rows of codes are ld_codes
-// bytes apart, a multiple of 16; columns from `cols` up to ld_codes get code 0.
-// `zero`: n_zero words that the launch also clears.
-cudaError_t launch_fp8_quantize_rows(const void *a, wl_type type, long long lda, int rows, int cols,
-                                     const float *colscale, uint8_t *codes, long long ld_codes,
-                                     uint8_t *scales, unsigned int *zero, int n_zero, cudaStream_t stream);
+// element times colscale[column] first (nullptr: 1; bf16 only).  Rows of codes
+// are ld_codes bytes apart, a multiple of 16; columns from `cols` up to
+// ld_codes get code 0.
+struct Fp8RowsJob {
+    const void *a;
+    long long lda;
+    int cols;
+    const float *colscale;
+    uint8_t *codes;
+    long long ld_codes;
+    uint8_t *scales;
+    long long warp_begin;  // filled by the launcher
+};
+// Up to kMaxSeg matrices of `rows` rows in one launch (all with column scales
+// or none), which also clears n_zero words at `zero`.
+struct Fp8RowsParams {
+    Fp8RowsJob job[kMaxSeg];
+    int njobs, rows;
+    unsigned int *zero;
+    int n_zero;
+};
+cudaError_t launch_fp8_quantize_rows(Fp8RowsParams &p, wl_type type, cudaStream_t stream);
 // 128 x 128 blocks; cols % 16 == 0, rows of codes cols bytes apart.
 cudaError_t launch_fp8_quantize_tiles(const void *a, wl_type type, int rows, int cols, uint8_t *codes,
                                       uint8_t *scales, cudaStream_t stream);
@@ -76,12 +92,13 @@ struct LowrankParams {
     LowrankJob job[kMaxSeg];
     int njobs;
     LowrankQuant quant;
-    int BN, split, stages, a_bytes, stage_bytes, tmem_cols;  // filled by the launcher
+    int BN, split, tiles, stages, a_bytes, stage_bytes, tmem_cols;  // plan
     int *status;
     unsigned long long timeout_ns;
 };
 
-cudaError_t launch_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms, cudaStream_t stream);
+void plan_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms);
+cudaError_t launch_fp8_lowrank(const LowrankParams &p, LowrankMode mode, cudaStream_t stream);
 
 // -------------------------------------------------------------------- GEMM ----
 // Tensor-core product over CTA pairs: output tiles of 256 rows x 224, 128 or 64 columns (BN),
@@ -138,8 +155,17 @@ enum Fp8Mode {
 // BN for outputs of N[0..nout) columns and a contraction of `blocks` blocks.
 int fp8_gemm_columns(int M, const int *N, int nout, int blocks, int num_sms);
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, Fp8Mode mode, int num_sms, cudaStream_t stream);
-// ds[n] = sum over rows i < n_rows of sums[i][n].
-cudaError_t launch_fp8_sum_rows(const float *sums, int n_rows, int N, float *ds, cudaStream_t stream);
+// ds[n] = sum over rows i < n_rows of sums[i][n], for several outputs in one launch.
+struct Fp8SumJob {
+    const float *sums;
+    float *ds;
+    int N, cta_begin;  // cta_begin: filled by the launcher
+};
+struct Fp8SumParams {
+    Fp8SumJob job[kMaxSeg];
+    int njobs, n_rows;
+};
+cudaError_t launch_fp8_sum_rows(Fp8SumParams &p, cudaStream_t stream);
 
 // ------------------------------------------------------- few-token stream ----
 constexpr int kFp8StreamMaxM = 128;

@@ -4,6 +4,8 @@
 
 #include <cstdint>
 #include <cstring>
+#include <memory>
+#include <new>
 
 #include "../../include/wl.h"
 #include "wl_fp8.h"
@@ -200,7 +202,7 @@ wl_status add_lowrank(LowrankParams &p, LowrankMode mode, const __nv_bfloat16 *A
     return st == WL_OK ? encode_map_2d(&j.tm_b, B, r, K, r, 64, 64) : st;
 }
 
-// Adds out = X^T (B + B_low) for X in 8 bits (K x I).
+// Adds out = X^T (B + B_low) for X in 8 bits (K x I), the same for every job.
 wl_status add_lowrank_codes(LowrankParams &p, const Fp8Mat &X, int I, int K, const __nv_bfloat16 *B,
                             const __nv_bfloat16 *B_low, int r, __nv_bfloat16 *out) {
     LowrankJob &j = p.job[p.njobs++];
@@ -211,18 +213,21 @@ wl_status add_lowrank_codes(LowrankParams &p, const Fp8Mat &X, int I, int K, con
     j.a_scales = X.scales;
     j.a_pitch = X.pitch;
     j.out = out;
-    wl_status st = encode_map_2d_u32(&j.tm_a, X.codes, I / 4, K, X.ld, 32, 64);
+    wl_status st = WL_OK;
+    if (p.njobs > 1)
+        j.tm_a = p.job[0].tm_a;
+    else
+        st = encode_map_2d_u32(&j.tm_a, X.codes, I / 4, K, X.ld, 32, 64);
     if (st == WL_OK) st = encode_map_2d(&j.tm_b, B, r, K, r, 64, 64);
     return st == WL_OK ? encode_map_2d(&j.tm_b2, B_low, r, K, r, 64, 64) : st;
 }
 
-// y_p = s_p (.) (X W_p^T) + T_p U_p^T on the few-token kernel.  parts and
-// counters as plan_stream's cut needs them, counters zero.
-wl_status run_stream(const Fp8Mat &X, int M, int K, const wl_proj_fp8 *projs, __nv_bfloat16 *const *T, int P,
-                     float *parts, unsigned int *counters, bool early, const Device &dev, cudaStream_t stream) {
+// The few-token kernel's parameters for y_p = s_p (.) (X W_p^T) + T_p U_p^T.
+// parts and counters as plan_stream's cut needs them, counters zero at launch.
+wl_status set_stream(Fp8StreamParams &sp, const Fp8Mat &X, int M, int K, const wl_proj_fp8 *projs,
+                     __nv_bfloat16 *const *T, int P, float *parts, unsigned int *counters, bool early, const Device &dev) {
     int N[kMaxSeg], r[kMaxSeg];
     for (int i = 0; i < P; ++i) N[i] = projs[i].N, r[i] = projs[i].r;
-    Fp8StreamParams sp;
     plan_stream(sp, M, K, N, r, P);
     sp.x_scales = X.scales;
     sp.early = early;
@@ -243,37 +248,68 @@ wl_status run_stream(const Fp8Mat &X, int M, int K, const wl_proj_fp8 *projs, __
         if (st == WL_OK && q.r > 0) st = encode_map_2d(&sp.tm_t[k], T[i], q.r, M, q.r, 64, sp.Mp);
         ++k;
     }
-    return st != WL_OK ? st : from_cuda(launch_fp8_stream(sp, stream));
+    return st;
 }
 
-wl_status forward_run(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, int P, uint8_t *x_codes,
-                      uint8_t *x_scales, const ForwardLayout &l, const Device &dev, cudaStream_t stream) {
-    const Fp8Mat X{x_codes ? x_codes : l.codes, x_scales ? x_scales : l.scales, K, fp8_pitch(K)};
-    const bool few = M <= kFp8StreamMaxM;
-    int tiles = 0;  // counters of the few-token kernel
-    for (int i = 0; i < P; ++i) tiles += (projs[i].N + 127) / 128;
+}  // namespace
+}  // namespace wl
+
+// Everything a forward call launches.
+struct wl_fp8_plan {
+    int M, K, P;
+    wl_proj_fp8 projs[WL_MAX_PROJ];
+    bool zeros;                // K == 0: outputs are zero
+    wl::Fp8RowsParams quant;   // njobs == 0: the rank-r launch quantises x, or nothing is to be done
+    wl::LowrankParams lowrank;
+    bool few;                  // which of the two products
+    wl::Fp8StreamParams stream;
+    wl::Fp8GemmParams gemm;
+};
+
+namespace wl {
+namespace {
+
+// Sets `f` up for a checked call; launches nothing.
+wl_status forward_plan(wl_fp8_plan &f, const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, int P, uint8_t *x_codes,
+                       uint8_t *x_scales, const ForwardLayout &l, const Device &dev) {
+    f.M = M;
+    f.K = K;
+    f.P = P;
+    f.quant.njobs = f.lowrank.njobs = f.stream.nseg = f.gemm.nout = 0;
+    f.stream.units = f.gemm.num_tiles = 0;
+    f.few = M <= kFp8StreamMaxM;
+    f.zeros = M > 0 && K == 0;
+    if (f.zeros) std::memcpy(f.projs, projs, sizeof(wl_proj_fp8) * P);
+    if (M == 0 || K == 0) return WL_OK;
+    uint8_t *codes = x_codes ? x_codes : l.codes, *scales = x_scales ? x_scales : l.scales;
+    const Fp8Mat X{codes, scales, K, fp8_pitch(K)};
+    int N[kMaxSeg], tiles = 0;  // tiles: counters of the few-token kernel
+    for (int i = 0; i < P; ++i) {
+        N[i] = projs[i].N;
+        tiles += (N[i] + 127) / 128;
+    }
     wl_status st;
-    LowrankParams lp;
-    init_lowrank(lp, dev);
+    init_lowrank(f.lowrank, dev);
     __nv_bfloat16 *T[kMaxSeg];
     for (int i = 0; i < P; ++i) {
         const wl_proj_fp8 &q = projs[i];
         T[i] = q.T ? bf16(q.T) : l.T[i];
         if (q.r > 0 && (q.T || q.N > 0) &&
-            (st = add_lowrank(lp, kLowrankRows, bf16(x), K, M, K, bf16(q.V), q.r, T[i], nullptr, lp.njobs > 0)) != WL_OK)
+            (st = add_lowrank(f.lowrank, kLowrankRows, bf16(x), K, M, K, bf16(q.V), q.r, T[i], nullptr, f.lowrank.njobs > 0)) != WL_OK)
             return st;
     }
-    uint8_t *codes = const_cast<uint8_t *>(X.codes), *scales = const_cast<uint8_t *>(X.scales);
-    if (few && lp.njobs > 0)  // one launch less in a decode step
-        lp.quant = LowrankQuant{bf16(x), codes, scales, M, K, l.counters, tiles};
-    else if (launch_fp8_quantize_rows(x, WL_BF16, K, M, K, nullptr, codes, K, scales, l.counters, few ? tiles : 0,
-                                      stream) != cudaSuccess)
-        return WL_ERR_CUDA;
-    if (launch_fp8_lowrank(lp, kLowrankRows, dev.sms, stream) != cudaSuccess) return WL_ERR_CUDA;
-    if (few) return run_stream(X, M, K, projs, T, P, l.parts, l.counters, true, dev, stream);
-    Fp8GemmParams g;
-    int N[kMaxSeg];
-    for (int i = 0; i < P; ++i) N[i] = projs[i].N;
+    plan_fp8_lowrank(f.lowrank, kLowrankRows, dev.sms);
+    if (f.few && f.lowrank.njobs > 0) {  // one launch less in a decode step
+        f.lowrank.quant = LowrankQuant{bf16(x), codes, scales, M, K, l.counters, tiles};
+    } else {
+        f.quant.job[0] = Fp8RowsJob{x, K, K, nullptr, codes, K, scales, 0};
+        f.quant.njobs = 1;
+        f.quant.rows = M;
+        f.quant.zero = l.counters;
+        f.quant.n_zero = f.few ? tiles : 0;
+    }
+    if (f.few) return set_stream(f.stream, X, M, K, projs, T, P, l.parts, l.counters, true, dev);
+    Fp8GemmParams &g = f.gemm;
     init_gemm(g, M, N, P, (K + kFp8Block - 1) / kFp8Block, dev);
     for (int i = 0; i < P; ++i) {
         const wl_proj_fp8 &q = projs[i];
@@ -285,7 +321,32 @@ wl_status forward_run(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, 
         o.s = q.s;
         o.y = bf16(q.y);
     }
-    return from_cuda(launch_fp8_gemm(g, kFp8Plain, dev.sms, stream));
+    return WL_OK;
+}
+
+wl_status forward_prepare(wl_fp8_plan &f, const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, int P,
+                          uint8_t *x_codes, uint8_t *x_scales, void *ws, size_t ws_bytes, Device &dev) {
+    wl_status st = forward_check(x, M, K, projs, P, x_codes, x_scales);
+    if (st != WL_OK) return st;
+    const ForwardLayout l = forward_layout(M, K, projs, P, ws);
+    if (M > 0 && K > 0 && (st = check_workspace(ws, ws_bytes, l.bytes)) != WL_OK) return st;
+    if ((st = device_info(&dev.sms, &dev.status)) != WL_OK) return st;
+    return forward_plan(f, x, M, K, projs, P, x_codes, x_scales, l, dev);
+}
+
+wl_status forward_launch(wl_fp8_plan &f, const Device &dev, cudaStream_t stream) {
+    if (f.zeros) {
+        for (int i = 0; i < f.P; ++i) {
+            const wl_proj_fp8 &q = f.projs[i];
+            if (q.N > 0 && cudaMemsetAsync(q.y, 0, (size_t)f.M * q.N * 2, stream) != cudaSuccess) return WL_ERR_CUDA;
+            if (q.T && q.r > 0 && cudaMemsetAsync(q.T, 0, (size_t)f.M * q.r * 2, stream) != cudaSuccess)
+                return WL_ERR_CUDA;
+        }
+        return WL_OK;
+    }
+    if (f.quant.njobs > 0 && launch_fp8_quantize_rows(f.quant, WL_BF16, stream) != cudaSuccess) return WL_ERR_CUDA;
+    if (launch_fp8_lowrank(f.lowrank, kLowrankRows, stream) != cudaSuccess) return WL_ERR_CUDA;
+    return from_cuda(f.few ? launch_fp8_stream(f.stream, stream) : launch_fp8_gemm(f.gemm, kFp8Plain, dev.sms, stream));
 }
 
 // --------------------------------------------------------------- backward ----
@@ -371,6 +432,10 @@ wl_status backward_run(const uint8_t *x_codes, const uint8_t *x_scales, int M, i
     }
     init_gemm(gx, M, &K, 1, blocks, dev);
     init_gemm(gs, M, N, P, (K + kFp8Block - 1) / kFp8Block, dev);
+    Fp8RowsParams quant = {};
+    quant.rows = M;
+    Fp8SumParams sums = {};
+    sums.n_rows = (M + 31) / 32;
     LowrankParams le, lu, lv;
     init_lowrank(le, dev);
     init_lowrank(lu, dev);
@@ -402,22 +467,24 @@ wl_status backward_run(const uint8_t *x_codes, const uint8_t *x_scales, int M, i
             Fp8Out &o = add_out(gs, q.N, k, 1);
             o.dy = bf16(q.dy);
             o.sums = l.sums[i];
+            sums.job[sums.njobs++] = Fp8SumJob{l.sums[i], q.ds, q.N, 0};
         }
         if (want_dx) {
             const long long ldg = round16(q.N);
-            if (launch_fp8_quantize_rows(q.dy, WL_BF16, q.N, M, q.N, q.s, l.g_codes[i], ldg, l.g_scales[i], nullptr, 0,
-                                         stream) !=
-                cudaSuccess)
-                return WL_ERR_CUDA;
+            quant.job[quant.njobs++] = Fp8RowsJob{q.dy, q.N, q.N, q.s, l.g_codes[i], ldg, l.g_scales[i], 0};
             if ((st = set_part(gx, parts, Fp8Mat{l.g_codes[i], l.g_scales[i], ldg, fp8_pitch(q.N)}, M, q.N, W, q.N, K, true,
                                l.E[i], bf16(q.V), q.r, K)) != WL_OK)
                 return st;
             ++parts;
         }
     }
-    if (launch_fp8_lowrank(le, kLowrankRows, dev.sms, stream) != cudaSuccess ||
-        launch_fp8_lowrank(lu, kLowrankCols, dev.sms, stream) != cudaSuccess ||
-        launch_fp8_lowrank(lv, kLowrankCodes, dev.sms, stream) != cudaSuccess)
+    plan_fp8_lowrank(le, kLowrankRows, dev.sms);
+    plan_fp8_lowrank(lu, kLowrankCols, dev.sms);
+    plan_fp8_lowrank(lv, kLowrankCodes, dev.sms);
+    if (launch_fp8_quantize_rows(quant, WL_BF16, stream) != cudaSuccess ||
+        launch_fp8_lowrank(le, kLowrankRows, stream) != cudaSuccess ||
+        launch_fp8_lowrank(lu, kLowrankCols, stream) != cudaSuccess ||
+        launch_fp8_lowrank(lv, kLowrankCodes, stream) != cudaSuccess)
         return WL_ERR_CUDA;
     if (parts > 0) {
         Fp8Out &o = add_out(gx, K, 0, parts);
@@ -425,11 +492,7 @@ wl_status backward_run(const uint8_t *x_codes, const uint8_t *x_scales, int M, i
         if (launch_fp8_gemm(gx, kFp8Transposed, dev.sms, stream) != cudaSuccess) return WL_ERR_CUDA;
     }
     if (launch_fp8_gemm(gs, kFp8ColSums, dev.sms, stream) != cudaSuccess) return WL_ERR_CUDA;
-    for (int i = 0; i < P; ++i)
-        if (projs[i].ds && K > 0 && projs[i].N > 0 &&
-            launch_fp8_sum_rows(l.sums[i], (M + 31) / 32, projs[i].N, projs[i].ds, stream) != cudaSuccess)
-            return WL_ERR_CUDA;
-    return WL_OK;
+    return from_cuda(launch_fp8_sum_rows(sums, stream));
 }
 
 }  // namespace
@@ -450,9 +513,12 @@ wl_status wl_quantize_fp8(const void *a, wl_type type, int rows, int cols, int b
     wl_status st = device_info(&sms, &status);
     if (st != WL_OK) return st;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-    return from_cuda(block_rows == 1
-                         ? launch_fp8_quantize_rows(a, type, cols, rows, cols, nullptr, codes, cols, scales, nullptr, 0, stream)
-                         : launch_fp8_quantize_tiles(a, type, rows, cols, codes, scales, stream));
+    if (block_rows == kFp8Block) return from_cuda(launch_fp8_quantize_tiles(a, type, rows, cols, codes, scales, stream));
+    Fp8RowsParams p = {};
+    p.job[0] = Fp8RowsJob{a, cols, cols, nullptr, codes, cols, scales, 0};
+    p.njobs = 1;
+    p.rows = rows;
+    return from_cuda(launch_fp8_quantize_rows(p, type, stream));
 }
 
 }  // extern "C"
@@ -518,7 +584,9 @@ wl_status wl_matmul_fp8(const uint8_t *a_codes, const uint8_t *a_scales, const u
         q.y = y;
         q.N = N;
         __nv_bfloat16 *T = nullptr;
-        return run_stream(Fp8Mat{a_codes, a_scales, K, fp8_pitch(K)}, M, K, &q, &T, 1, l.parts, l.counters, false, dev, stream);
+        Fp8StreamParams sp;
+        st = set_stream(sp, Fp8Mat{a_codes, a_scales, K, fp8_pitch(K)}, M, K, &q, &T, 1, l.parts, l.counters, false, dev);
+        return st != WL_OK ? st : from_cuda(launch_fp8_stream(sp, stream));
     }
     Fp8GemmParams g;
     init_gemm(g, M, &N, 1, (K + kFp8Block - 1) / kFp8Block, dev);
@@ -537,25 +605,35 @@ size_t wl_stacked_forward_fp8_workspace(int M, int K, const wl_proj_fp8 *projs, 
 
 wl_status wl_stacked_forward_fp8(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, int P, uint8_t *x_codes,
                                  uint8_t *x_scales, void *workspace, size_t workspace_bytes, void *stream_ptr) {
-    using namespace wl;
-    wl_status st = forward_check(x, M, K, projs, P, x_codes, x_scales);
-    if (st != WL_OK || M == 0) return st;
-    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-    if (K == 0) {  // x W0^T = 0 and x V = 0
-        for (int i = 0; i < P; ++i) {
-            const wl_proj_fp8 &q = projs[i];
-            if (q.N > 0 && cudaMemsetAsync(q.y, 0, (size_t)M * q.N * 2, stream) != cudaSuccess) return WL_ERR_CUDA;
-            if (q.T && q.r > 0 && cudaMemsetAsync(q.T, 0, (size_t)M * q.r * 2, stream) != cudaSuccess)
-                return WL_ERR_CUDA;
-        }
-        return WL_OK;
-    }
-    const ForwardLayout l = forward_layout(M, K, projs, P, workspace);
-    if ((st = check_workspace(workspace, workspace_bytes, l.bytes)) != WL_OK) return st;
-    Device dev;
-    if ((st = device_info(&dev.sms, &dev.status)) != WL_OK) return st;
-    return forward_run(x, M, K, projs, P, x_codes, x_scales, l, dev, stream);
+    wl_fp8_plan f;
+    wl::Device dev;
+    wl_status st = wl::forward_prepare(f, x, M, K, projs, P, x_codes, x_scales, workspace, workspace_bytes, dev);
+    return st != WL_OK ? st : wl::forward_launch(f, dev, static_cast<cudaStream_t>(stream_ptr));
 }
+
+wl_status wl_plan_stacked_forward_fp8(const wl_bf16 *x, int M, int K, const wl_proj_fp8 *projs, int P,
+                                      uint8_t *x_codes, uint8_t *x_scales, void *workspace, size_t workspace_bytes,
+                                      wl_fp8_plan **plan) {
+    if (!plan) return WL_ERR_INVALID_ARG;
+    *plan = nullptr;
+    std::unique_ptr<wl_fp8_plan> f(new (std::nothrow) wl_fp8_plan);
+    if (!f) return WL_ERR_NOMEM;
+    wl::Device dev;
+    wl_status st = wl::forward_prepare(*f, x, M, K, projs, P, x_codes, x_scales, workspace, workspace_bytes, dev);
+    if (st == WL_OK) *plan = f.release();
+    return st;
+}
+
+wl_status wl_run_fp8_plan(wl_fp8_plan *plan, void *stream) {
+    if (!plan) return WL_ERR_INVALID_ARG;
+    wl::Device dev;
+    wl_status st = wl::device_info(&dev.sms, &dev.status);
+    if (st != WL_OK) return st;
+    plan->lowrank.timeout_ns = plan->stream.timeout_ns = plan->gemm.timeout_ns = wl::wait_limit_ns();
+    return wl::forward_launch(*plan, dev, static_cast<cudaStream_t>(stream));
+}
+
+void wl_free_fp8_plan(wl_fp8_plan *plan) { delete plan; }
 
 size_t wl_stacked_backward_fp8_workspace(int M, int K, const wl_grad_fp8 *projs, int P) {
     using namespace wl;

@@ -624,27 +624,42 @@ namespace {
 // 32 columns x 32 partial sums per step and CTA, so a warp reads 128 bytes of
 // a row; each thread adds every 32nd row, then the 32 sums of a column meet in
 // a fixed order.
-__global__ void __launch_bounds__(1024) sum_rows_kernel(const float *__restrict__ sums, int n_rows, int N,
-                                                        float *__restrict__ ds) {
+__global__ void __launch_bounds__(1024) sum_rows_kernel(const __grid_constant__ Fp8SumParams p) {
     __shared__ float part[32][33];
-    pdl_launch_dependents();
     pdl_wait_primary();
-    const int n = blockIdx.x * 32 + threadIdx.x;
+    pdl_launch_dependents();
+    int jx = 0;
+    while (jx + 1 < p.njobs && (int)blockIdx.x >= p.job[jx + 1].cta_begin) ++jx;
+    const Fp8SumJob &jb = p.job[jx];
+    const int n0 = ((int)blockIdx.x - jb.cta_begin) * 32, n = n0 + threadIdx.x;
     float a = 0.f;
-    if (n < N)
-        for (int i = threadIdx.y; i < n_rows; i += 32) a += sums[(size_t)i * N + n];
+    if (n < jb.N)
+        for (int i = threadIdx.y; i < p.n_rows; i += 32) a += jb.sums[(size_t)i * jb.N + n];
     part[threadIdx.y][threadIdx.x] = a;
     __syncthreads();
     const float v = warp_sum(part[threadIdx.x][threadIdx.y]);
-    const int m = blockIdx.x * 32 + threadIdx.y;
-    if (threadIdx.x == 0 && m < N) ds[m] = v;
+    const int m = n0 + threadIdx.y;
+    if (threadIdx.x == 0 && m < jb.N) jb.ds[m] = v;
 }
 }  // namespace
 
-cudaError_t launch_fp8_sum_rows(const float *sums, int n_rows, int N, float *ds, cudaStream_t stream) {
-    if (N == 0) return cudaSuccess;
-    sum_rows_kernel<<<(N + 31) / 32, dim3(32, 32), 0, stream>>>(sums, n_rows, N, ds);
-    return cudaGetLastError();
+cudaError_t launch_fp8_sum_rows(Fp8SumParams &p, cudaStream_t stream) {
+    int ctas = 0;
+    for (int i = 0; i < p.njobs; ++i) {
+        p.job[i].cta_begin = ctas;
+        ctas += (p.job[i].N + 31) / 32;
+    }
+    if (ctas == 0) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(32, 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sum_rows_kernel, p);
 }
 
 }  // namespace wl

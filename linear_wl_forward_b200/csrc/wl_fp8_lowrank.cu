@@ -16,7 +16,7 @@
 // contraction; the CTAs of a cluster (1 to 16) share a tile's contraction
 // and add their sums over distributed shared memory in rank order, so there
 // are no partial results in memory and the result is reproducible.  The tile
-// width and the split are chosen by a cost estimate (plan below): a tile of N
+// width and the split are chosen by a cost estimate (choose_tiles): a tile of N
 // columns stages (128 + N) x 128 bytes per 64 columns of the contraction
 // against 2 N tensor-core cycles, so wide tiles are fed best; short products
 // are cut instead, to put every SM to work.
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
 // issuing thread (450 cycles), plus 5000 for the start and the drain and, with
 // a split, the exchange of 128 x BN sums (60 cycles per column; measured:
 // 128 x 256 tiles cut in four took 63 us where whole ones take 28).
-static void plan(LowrankParams &p, int terms, int num_sms) {
+static void choose_tiles(LowrankParams &p, int terms, int num_sms) {
     double best = 0;
     for (int bn = 256; bn >= 64; bn /= 2)
         for (int s = 1; s <= kMaxSplit; s *= 2) {
@@ -396,35 +396,38 @@ static void plan(LowrankParams &p, int terms, int num_sms) {
         }
 }
 
-cudaError_t launch_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms, cudaStream_t stream) {
-    if (p.njobs == 0) return cudaSuccess;
+void plan_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms) {
+    if (p.njobs == 0) return;
     const int terms = mode == kLowrankCodes ? 2 : 1;
     int rows = 0;
     for (int i = 0; i < p.njobs; ++i) rows = std::max(rows, lowrank_a_rows(p.job[i].I));
     p.a_bytes = mode == kLowrankRows ? rows * 128 : (int)kATile;
-    if (p.quant.a && rows > 128) return cudaErrorInvalidValue;
-    plan(p, terms, num_sms);
-    int tiles = 0, widest = 0;
+    choose_tiles(p, terms, num_sms);
+    int widest = 0, longest = 0;
+    p.tiles = 0;
     for (int i = 0; i < p.njobs; ++i) {
-        p.job[i].tile_begin = tiles;
-        tiles += (p.job[i].I + 127) / 128 * ((p.job[i].r + p.BN - 1) / p.BN);
-        widest = std::max(widest, p.job[i].r);
+        LowrankJob &j = p.job[i];
+        j.tile_begin = p.tiles;
+        p.tiles += (j.I + 127) / 128 * ((j.r + p.BN - 1) / p.BN);
+        widest = std::max(widest, j.r);
+        longest = std::max(longest, (j.kb + p.split - 1) / p.split);
     }
-    const int boxes = (std::min(widest, p.BN) + 63) / 64;
-    p.stage_bytes = (int)(p.a_bytes + (mode == kLowrankCodes ? kCodeTile : 0) + terms * boxes * kBBox);
+    const int cols = std::min((widest + 15) / 16 * 16, p.BN);
+    p.stage_bytes = (int)(p.a_bytes + (mode == kLowrankCodes ? kCodeTile : 0) + terms * ((cols + 63) / 64) * kBBox);
     // narrow tiles leave room for a second CTA on the SM, or for the kernel that follows
-    int longest = 0;
-    for (int i = 0; i < p.njobs; ++i) longest = std::max(longest, (p.job[i].kb + p.split - 1) / p.split);
     p.stages = std::min(kMaxStages, (p.BN > 64 ? 200 * 1024 : p.a_bytes < (int)kATile ? 60 * 1024 : 100 * 1024) / p.stage_bytes);
     p.stages = std::max(2, std::min(p.stages, longest));
-    p.tmem_cols = 32;
-    while (p.tmem_cols < std::min((widest + 15) / 16 * 16, p.BN)) p.tmem_cols *= 2;
     // the exchange of a split tile reuses the stages
-    const size_t exchange = p.split > 1 ? (size_t)std::min((widest + 15) / 16 * 16, p.BN) * 512 : 0;
-    while ((size_t)p.stages * p.stage_bytes < exchange) ++p.stages;
+    while (p.split > 1 && p.stages * p.stage_bytes < cols * 512) ++p.stages;
+    p.tmem_cols = 32;
+    while (p.tmem_cols < cols) p.tmem_cols *= 2;
+}
+
+cudaError_t launch_fp8_lowrank(const LowrankParams &p, LowrankMode mode, cudaStream_t stream) {
+    if (p.njobs == 0) return cudaSuccess;
     // an MMA reads 128 rows of A, so the last stage's tile may end behind the stages
     const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + std::max<size_t>((3 * kMaxStages + 1) * 8 + 32, kATile);
-    if (p.stages > kMaxStages || smem > 227 * 1024) return cudaErrorInvalidValue;
+    if (p.stages > kMaxStages || smem > 227 * 1024 || (p.quant.a && p.a_bytes > (int)kATile)) return cudaErrorInvalidValue;
     void (*const kernels[3])(LowrankParams) = {lowrank_kernel<kLowrankRows>, lowrank_kernel<kLowrankCols>,
                                                lowrank_kernel<kLowrankCodes>};
     static std::atomic<bool> done[64][3] = {};
@@ -439,7 +442,7 @@ cudaError_t launch_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms, 
         done[dev][mode].store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * p.split));
+    cfg.gridDim = dim3((unsigned)(p.tiles * p.split));
     cfg.blockDim = dim3(threads_of(mode));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;

@@ -24,28 +24,31 @@ namespace {
 // neighbouring rows of the same columns, so the scales (twice the data's bytes
 // per element) come from L1.
 template <typename T, bool kColScale>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict__ a, long long lda, int rows, int cols,
-                                                            int words, const float *__restrict__ colscale,
-                                                            uint8_t *__restrict__ codes, long long ld_codes,
-                                                            uint8_t *__restrict__ scales, bool vec, bool svec,
-                                                            unsigned int *__restrict__ zero, int n_zero) {
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constant__ Fp8RowsParams p) {
     // Dependents start once everything before this kernel is complete, so they
     // may read its predecessors' results without waiting for this kernel.
     pdl_wait_primary();
     pdl_launch_dependents();
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n_zero; i += (long long)gridDim.x * 256) zero[i] = 0;
-    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < p.n_zero; i += (long long)gridDim.x * 256) p.zero[i] = 0;
+    long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    if (w >= (long long)rows * words) return;
-    const int row = kColScale ? (int)(w % rows) : (int)(w / words), q = kColScale ? (int)(w / rows) : (int)(w % words);
-    const int c = q * 512 + lane * 16;
+    int jx = 0;
+    while (jx + 1 < p.njobs && w >= p.job[jx + 1].warp_begin) ++jx;
+    const Fp8RowsJob &jb = p.job[jx];
+    const int words = WL_FP8_SCALE_PITCH(jb.cols) / 4;
+    w -= jb.warp_begin;
+    if (w >= (long long)p.rows * words) return;
+    const int row = kColScale ? (int)(w % p.rows) : (int)(w / words), q = kColScale ? (int)(w / p.rows) : (int)(w % words);
+    const int c = q * 512 + lane * 16, left = jb.cols - c;
+    const T *a = static_cast<const T *>(jb.a) + (size_t)row * jb.lda + c;
     Raw16<T> raw;
-    raw.load(a + (size_t)row * lda + c, cols - c, vec);
+    raw.load(a, left, (reinterpret_cast<uintptr_t>(a) & 15u) == 0);
     float v[16];
     raw.unpack(v);
     if (kColScale) {
+        const float *cs = jb.colscale + c;
         Raw16<float> s;
-        s.load(colscale + c, cols - c, svec);
+        s.load(cs, left, (reinterpret_cast<uintptr_t>(cs) & 15u) == 0);
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] *= s.f[i];
     }
@@ -54,8 +57,9 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict_
     const uint32_t e = (uint32_t)(E + 127);
     const uint32_t word = __shfl_sync(0xffffffffu, e, 0) | __shfl_sync(0xffffffffu, e, 8) << 8 |
                           __shfl_sync(0xffffffffu, e, 16) << 16 | __shfl_sync(0xffffffffu, e, 24) << 24;
-    if (c < ld_codes) *reinterpret_cast<uint4 *>(codes + (size_t)row * ld_codes + c) = codes16(v, inverse_scale(E), infinities);
-    if (lane == 0) *reinterpret_cast<uint32_t *>(scales + ((size_t)row * words + q) * 4) = word;
+    if (c < jb.ld_codes)
+        *reinterpret_cast<uint4 *>(jb.codes + (size_t)row * jb.ld_codes + c) = codes16(v, inverse_scale(E), infinities);
+    if (lane == 0) *reinterpret_cast<uint32_t *>(jb.scales + ((size_t)row * words + q) * 4) = word;
 }
 
 __device__ __forceinline__ float block_max(float m, float *warp_max) {
@@ -123,28 +127,6 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const __nv_bfloat16 *__re
         out[row * ld + c] = c < cols ? a[row * cols + c] : __float2bfloat16_rn(0.f);
 }
 
-template <typename T, bool kColScale>
-cudaError_t quantize_rows(const T *a, long long lda, int rows, int cols, const float *colscale, uint8_t *codes,
-                          long long ld_codes, uint8_t *scales, unsigned int *zero, int n_zero, cudaStream_t stream) {
-    const int words = fp8_pitch(cols) / 4;
-    const long long blocks = ((long long)rows * words + 7) / 8;
-    if (blocks == 0) return cudaSuccess;
-    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-    const bool vec = (reinterpret_cast<uintptr_t>(a) & 15u) == 0 && (lda * sizeof(T)) % 16 == 0;
-    const bool svec = (reinterpret_cast<uintptr_t>(colscale) & 15u) == 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, kColScale>, a, lda, rows, cols, words, colscale, codes,
-                              ld_codes, scales, vec, svec, zero, n_zero);
-}
-
 }  // namespace
 
 cudaError_t launch_fp8_pad_rows(const __nv_bfloat16 *a, int rows, int cols, __nv_bfloat16 *out, long long ld,
@@ -154,17 +136,27 @@ cudaError_t launch_fp8_pad_rows(const __nv_bfloat16 *a, int rows, int cols, __nv
     return cudaGetLastError();
 }
 
-cudaError_t launch_fp8_quantize_rows(const void *a, wl_type type, long long lda, int rows, int cols,
-                                     const float *colscale, uint8_t *codes, long long ld_codes, uint8_t *scales,
-                                     unsigned int *zero, int n_zero, cudaStream_t stream) {
-    if (type == WL_F32)
-        return quantize_rows<float, false>(static_cast<const float *>(a), lda, rows, cols, nullptr, codes, ld_codes,
-                                           scales, zero, n_zero, stream);
-    const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a);
-    return colscale ? quantize_rows<__nv_bfloat16, true>(x, lda, rows, cols, colscale, codes, ld_codes, scales, zero,
-                                                         n_zero, stream)
-                    : quantize_rows<__nv_bfloat16, false>(x, lda, rows, cols, nullptr, codes, ld_codes, scales, zero,
-                                                          n_zero, stream);
+cudaError_t launch_fp8_quantize_rows(Fp8RowsParams &p, wl_type type, cudaStream_t stream) {
+    long long warps = 0;
+    for (int i = 0; i < p.njobs; ++i) {
+        p.job[i].warp_begin = warps;
+        warps += (long long)p.rows * (fp8_pitch(p.job[i].cols) / 4);
+    }
+    if (warps == 0) return cudaSuccess;
+    const long long blocks = (warps + 7) / 8;
+    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, type == WL_F32             ? quantize_rows_kernel<float, false>
+                                    : p.job[0].colscale != nullptr ? quantize_rows_kernel<__nv_bfloat16, true>
+                                                                   : quantize_rows_kernel<__nv_bfloat16, false>, p);
 }
 
 cudaError_t launch_fp8_quantize_tiles(const void *a, wl_type type, int rows, int cols, uint8_t *codes, uint8_t *scales,
