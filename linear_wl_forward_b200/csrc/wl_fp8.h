@@ -141,6 +141,7 @@ struct Fp8GemmParams {
     Fp8Out out[kMaxSeg];
     int nout;
     int M, BN;
+    int split;        // CTA pairs that share a tile
     int m_tiles, num_tiles;
     int *status;
     unsigned long long timeout_ns;
@@ -152,8 +153,9 @@ enum Fp8Mode {
     kFp8ColSums       // K-major, the epilogue forms column sums: ds
 };
 
-// BN for outputs of N[0..nout) columns and a contraction of `blocks` blocks.
-int fp8_gemm_columns(int M, const int *N, int nout, int blocks, int num_sms);
+// Sets BN, split and m_tiles for M rows (set), outputs of N[0..nout) columns and
+// a contraction of `blocks` blocks.
+void plan_fp8_gemm(Fp8GemmParams &p, const int *N, int nout, int blocks, bool may_split, int num_sms);
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, Fp8Mode mode, int num_sms, cudaStream_t stream);
 // ds[n] = sum over rows i < n_rows of sums[i][n], for several outputs in one launch.
 struct Fp8SumJob {

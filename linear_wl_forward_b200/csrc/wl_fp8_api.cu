@@ -166,11 +166,10 @@ struct Device {
 };
 
 // Outputs of M rows x N[0..nout) columns over `blocks` blocks.
-void init_gemm(Fp8GemmParams &g, int M, const int *N, int nout, int blocks, const Device &dev) {
+void init_gemm(Fp8GemmParams &g, int M, const int *N, int nout, int blocks, bool may_split, const Device &dev) {
     std::memset(&g, 0, sizeof g);
     g.M = M;
-    g.BN = fp8_gemm_columns(M, N, nout, blocks, dev.sms);
-    g.m_tiles = (M + kFp8BM - 1) / kFp8BM;
+    plan_fp8_gemm(g, N, nout, blocks, may_split, dev.sms);
     g.status = dev.status;
     g.timeout_ns = wait_limit_ns();
 }
@@ -310,7 +309,7 @@ wl_status forward_plan(wl_fp8_plan &f, const wl_bf16 *x, int M, int K, const wl_
     }
     if (f.few) return set_stream(f.stream, X, M, K, projs, T, P, l.parts, l.counters, true, dev);
     Fp8GemmParams &g = f.gemm;
-    init_gemm(g, M, N, P, (K + kFp8Block - 1) / kFp8Block, dev);
+    init_gemm(g, M, N, P, (K + kFp8Block - 1) / kFp8Block, true, dev);
     for (int i = 0; i < P; ++i) {
         const wl_proj_fp8 &q = projs[i];
         if (q.N == 0) continue;
@@ -430,8 +429,8 @@ wl_status backward_run(const uint8_t *x_codes, const uint8_t *x_scales, int M, i
         N[i] = projs[i].N;
         blocks += (N[i] + kFp8Block - 1) / kFp8Block;
     }
-    init_gemm(gx, M, &K, 1, blocks, dev);
-    init_gemm(gs, M, N, P, (K + kFp8Block - 1) / kFp8Block, dev);
+    init_gemm(gx, M, &K, 1, blocks, true, dev);
+    init_gemm(gs, M, N, P, (K + kFp8Block - 1) / kFp8Block, false, dev);
     Fp8RowsParams quant = {};
     quant.rows = M;
     Fp8SumParams sums = {};
@@ -589,7 +588,7 @@ wl_status wl_matmul_fp8(const uint8_t *a_codes, const uint8_t *a_scales, const u
         return st != WL_OK ? st : from_cuda(launch_fp8_stream(sp, stream));
     }
     Fp8GemmParams g;
-    init_gemm(g, M, &N, 1, (K + kFp8Block - 1) / kFp8Block, dev);
+    init_gemm(g, M, &N, 1, (K + kFp8Block - 1) / kFp8Block, true, dev);
     if ((st = set_part(g, 0, Fp8Mat{a_codes, a_scales, K, fp8_pitch(K)}, M, K, Fp8Mat{b_codes, b_scales, K, fp8_pitch(K)},
                        N, K, false, nullptr, nullptr, 0, 0)) != WL_OK)
         return st;

@@ -22,6 +22,12 @@
 // run, which frees that region for tile i + 1.  So the tensor pipe waits for
 // no epilogue on long contractions.
 //
+// A product with few tiles is cut along its contraction: the pairs of a cluster
+// share a tile and add their sums over distributed shared memory in rank order.
+//
+// A product with few tiles is cut along its contraction: the pairs of a cluster
+// share a tile and add their sums over distributed shared memory in rank order.
+//
 // Per CTA (384 threads):
 //   warp 0      TMA producer, three stages of two blocks (64 KB); both CTAs'
 //               copies complete on the leader's barrier
@@ -88,11 +94,11 @@ __device__ __forceinline__ void cp_scales_pair(uint32_t taddr, uint64_t desc) {
 }
 // Arrives on the barrier at this offset in both CTAs once the tcgen05
 // operations issued so far have ended.
-__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+__device__ __forceinline__ void commit_pair(uint64_t *bar, uint16_t pair_mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_addr(bar)),
-        "h"((uint16_t)3)
+        "h"(pair_mask)
         : "memory");
 }
 
@@ -124,14 +130,34 @@ __device__ __forceinline__ Tile tile_of(const Fp8GemmParams &p, int t) {
 // commit 46, against 448 cycles of MMAs per block, so a stage holds two blocks
 // and the order is in the loops, not in per-block state (with both per block a
 // block took 950 cycles).
+// `r`: the stages that this pair runs, and where the rank-r blocks come.
+struct Stages {
+    int begin, end, low_at;
+};
+
+__device__ __forceinline__ Stages stages_of(const Fp8GemmParams &p, const Fp8Out &o, int pair) {
+    int total = 0;
+    for (int q = 0; q < o.nparts; ++q) total += (p.part[o.part0 + q].nkb + 1) >> 1;
+    Stages r;
+    r.begin = total * pair / p.split;
+    r.end = total * (pair + 1) / p.split;
+    r.low_at = pair == p.split - 1 ? max(r.begin, total - kLrLead) : -1;  // with the last range
+    return r;
+}
+
 template <typename Main, typename Low>
-__device__ __forceinline__ bool for_stages(const Fp8GemmParams &p, const Fp8Out &o, Main main, Low low) {
-    int left = 0;
-    for (int q = 0; q < o.nparts; ++q) left += (p.part[o.part0 + q].nkb + 1) >> 1;
-    for (int q = o.part0; q < o.part0 + o.nparts; ++q) {
+__device__ __forceinline__ bool for_stages(const Fp8GemmParams &p, const Fp8Out &o, const Stages &r, Main main, Low low) {
+    int i = 0;
+    for (int q = o.part0; q < o.part0 + o.nparts && i < r.end; ++q) {
         const int nkb = p.part[q].nkb;
-        for (int kb = 0; kb < nkb; kb += 2, --left) {
-            if (left == kLrLead || (left < kLrLead && kb == 0 && q == o.part0)) {
+        int kb = 0;
+        if (i < r.begin) {  // skip to the range
+            const int skip = min(r.begin - i, (nkb + 1) >> 1);
+            i += skip;
+            kb = 2 * skip;
+        }
+        for (; kb < nkb && i < r.end; kb += 2, ++i) {
+            if (i == r.low_at) {
                 for (int l = o.part0; l < o.part0 + o.nparts; ++l) {
                     const int lr = p.part[l].lr;
                     for (int j = 0; j < lr; j += 2)
@@ -182,8 +208,7 @@ __device__ __forceinline__ void b_scale_words(const Fp8Part &pt, int N, int n0, 
 }  // namespace
 
 template <int kMode, int kBN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
-    fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams p) {
+__global__ void __launch_bounds__(kFp8GemmThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams p) {
     constexpr bool kT = kMode == kFp8Transposed;
     constexpr int kHalf = kBN / 2;  // columns per CTA's half of B, and per epilogue warp
     constexpr int kChunks = kHalf / 16;
@@ -210,8 +235,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
     const WaitLimits limits{p.status, p.timeout_ns, abort_flag};
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
-    const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+    // this CTA in its pair, its pair in the cluster
+    const uint32_t rank = cluster_ctarank() & 1u, leader = cluster_ctarank() & ~1u;
+    const int pair = (int)(leader >> 1);
+    const uint16_t pair_mask = (uint16_t)(3u << leader);
+    const int cluster = blockIdx.x / (2 * p.split), nclusters = gridDim.x / (2 * p.split);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kFp8Stages; ++i) {
@@ -244,7 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
         // ------------------------------------------------------ producer ----
         Ring r(kFp8Stages);
         uint32_t issued = 0;
-        const uint32_t stage0 = smem_addr(base), full0 = map_rank(full, 0);
+        const uint32_t stage0 = smem_addr(base), full0 = map_rank(full, leader);
         bool ok = true;
         for (int t = cluster; t < p.num_tiles && ok; t += nclusters) {
             const Tile ti = tile_of(p, t);
@@ -271,8 +299,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
                 ++issued;
                 return true;
             };
+            const Fp8Out &o = p.out[ti.out];
             ok = for_stages(
-                p, p.out[ti.out],
+                p, o, stages_of(p, o, pair),
                 [&](int q, int kb, bool two) { return load(&p.tm_a[q], &p.tm_b[q], kb * 128, 128, two, kT, kBBytes); },
                 [&](int q, int j, bool two) { return load(&p.tm_t[q], &p.tm_u[q], j * 64, 64, two, false, kUBytes); });
         }
@@ -310,13 +339,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
                 if (ok && lr_count > 0) ok = warp_wait<true>(l_empty, (lr_count - 1) & 1u, limits);
                 if (!ok) break;
                 tc_fence_after();
-                const int lr = lr_blocks(p, o);
+                const Stages range = stages_of(p, o, pair);
+                const int lr = range.low_at >= 0 ? lr_blocks(p, o) : 0;
                 int lr_left = lr;
                 uint32_t acc = 0;
                 ok = for_stages(
-                    p, o,
+                    p, o, range,
                     [&](int, int kb, bool two) {
-                        const bool chunk = (kb & 3) == 0;  // the next four blocks' scales
+                        const bool chunk = (kb & 3) == 0 || acc == 0;  // the next four blocks' scales
                         if (chunk) {
                             if (!warp_wait<true>(&sf_full[sr.slot], sr.phase, limits)) return false;
                             sf_slot ^= 16u;
@@ -331,7 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
                                 cp_scales_pair(sf, ds);
                                 cp_scales_pair(sf + 4, ds + (512 >> 4));
                                 if (kBN > 128) cp_scales_pair(sf + 8, ds + (1024 >> 4));
-                                commit_pair(&sf_empty[sr.slot]);
+                                commit_pair(&sf_empty[sr.slot], pair_mask);
                             }
                             mma_mxf8_pair(d_main, da, db, idesc, sf, sf + 4, acc);
 #pragma unroll
@@ -340,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
                                     mma_mxf8_pair(d_main, da + kNext + 2 * k, db + kNext + kStepB * k, idesc + kScaleByte, sf, sf + 4, 1);
-                            commit_pair(&empty[r.slot]);
+                            commit_pair(&empty[r.slot], pair_mask);
                         }
                         __syncwarp();
                         acc = 1;
@@ -361,19 +391,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
                             if (two)
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) mma_f16_pair(d_lr, da + kNext + 2 * k, db + kNext + 2 * k, idesc_lr, 1);
-                            commit_pair(&empty[r.slot]);
-                            if (lr_left == 0) commit_pair(l_full);
+                            commit_pair(&empty[r.slot], pair_mask);
+                            if (lr_left == 0) commit_pair(l_full, pair_mask);
                         }
                         __syncwarp();
                         r.advance();
                         return true;
                     });
                 if (!ok) break;
-                if (elect_one()) commit_pair(&m_full[reg]);
+                if (elect_one()) commit_pair(&m_full[reg], pair_mask);
                 __syncwarp();
                 lr_count += lr > 0;
             }
-            if (elect_one()) commit_pair(drain);
+            if (elect_one()) commit_pair(drain, pair_mask);
             __syncwarp();
         }
     } else if (warp < 4) {
@@ -383,9 +413,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
         for (int t = cluster; t < p.num_tiles && ok; t += nclusters) {
             const Tile ti = tile_of(p, t);
             const Fp8Out &o = p.out[ti.out];
-            for (int q = 0; q < o.nparts && ok; ++q) {
+            const Stages range = stages_of(p, o, pair);
+            for (int q = 0, i = 0; q < o.nparts && ok; ++q) {
                 const Fp8Part &pt = p.part[o.part0 + q];
-                for (int c = 0; 4 * c < pt.nkb; ++c) {
+                // stages i + 2c and i + 2c + 1 take chunk c
+                const int stages = (pt.nkb + 1) >> 1, first = max(range.begin - i, 0), last = min(range.end - i, stages);
+                i += stages;
+                for (int c = first >> 1; first < last && 2 * c < last; ++c) {
                     uint32_t w[8];
                     if (warp == 2) {
 #pragma unroll
@@ -410,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) arrive_cluster(map_rank(&sf_full[r.slot], 0));
+                    if (lane == 0) arrive_cluster(map_rank(&sf_full[r.slot], leader));
                     r.advance();
                 }
             }
@@ -419,14 +453,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
         // ------------------------------------------------------- epilogue ---
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
-        const uint32_t m_empty_l = map_rank(m_empty, 0);
-        const uint32_t l_empty_l = map_rank(l_empty, 0);
+        const uint32_t m_empty_l = map_rank(m_empty, leader);
+        const uint32_t l_empty_l = map_rank(l_empty, leader);
         uint32_t it = 0, lr_count = 0;
         for (int t = cluster; t < p.num_tiles; t += nclusters, ++it) {
             const Tile ti = tile_of(p, t);
             const Fp8Out &o = p.out[ti.out];
             const uint32_t reg = it & 1u;
-            const int lr = lr_blocks(p, o);
+            const int lr = pair == p.split - 1 ? lr_blocks(p, o) : 0;
             const int m = ti.m0 + (int)rank * 128 + quarter * 32 + lane;
             const int n0 = ti.n0 + half * kHalf;
             uint32_t d[kChunks][16];
@@ -513,6 +547,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 16; ++i) sc[i] = fmaf(sc[i], __uint_as_float(v[i]), __uint_as_float(d[c][i]));
+                    if (p.split > 1) {  // into the idle stages, [column][row]
+                        float *sums = reinterpret_cast<float *>(base) + (half * kHalf + c * 16) * 128 + quarter * 32 + lane;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) sums[i * 128] = sc[i];
+                        continue;
+                    }
                     if (m < p.M) {
                         if (vec && n + 16 <= o.N) {
 #pragma unroll
@@ -545,11 +585,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8GemmThreads, 1)
         }
     }
 
+    if (kMode != kFp8ColSums && p.split > 1) {
+        __syncwarp();
+        cluster_sync();  // every pair's sums are in its shared memory
+        if (warp >= 4) {
+            // groups of 16 columns go round the pairs; a thread adds eight columns of a row
+            const Tile ti = tile_of(p, cluster);
+            const Fp8Out &o = p.out[ti.out];
+            const int tid = threadIdx.x - 128, row = tid & 127, m = ti.m0 + (int)rank * 128 + row;
+            const bool vec = (o.N & 7) == 0 && (reinterpret_cast<uintptr_t>(o.y) & 15u) == 0;
+            for (int g = pair; g < kBN / 16; g += p.split) {
+                const int c = g * 16 + (tid >> 7) * 8, n = ti.n0 + c;
+                const float *sums = reinterpret_cast<const float *>(base) + c * 128 + row;
+                float v[8] = {};
+#pragma unroll 2
+                for (int s = 0; s < p.split; ++s) {
+                    float a[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) a[i] = ld_cluster(sums + i * 128, 2 * s + rank);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] += a[i];
+                }
+                if (m >= p.M) continue;
+                __nv_bfloat16 *y = o.y + (size_t)m * o.N + n;
+                if (vec && n + 8 <= o.N) {
+                    *reinterpret_cast<uint4 *>(y) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (n + i < o.N) y[i] = __float2bfloat16_rn(v[i]);
+                }
+            }
+        }
+        __syncwarp();
+    }
     tc_fence_before();
     __syncthreads();
     // Every MMA issued has ended and every signal of theirs has arrived here.
     if (warp == 1) mbar_wait(drain, 0, p.status, kDrainNs);
-    cluster_sync();  // neither CTA leaves while the other may signal it or its MMAs read here
+    cluster_sync();  // no CTA leaves while another may signal it, its MMAs read there or its sums are read
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);
@@ -568,26 +643,33 @@ GemmKernel kernel_of(int bn) {
 }
 }  // namespace
 
-// The tile width with the least estimated cycles: waves of tiles over the CTA
-// pairs, a block of the contraction at the slowest of the MMAs (2 cycles per
-// column), the loads (46 bytes per cycle) and the issue (330 cycles), and about
-// 5000 cycles to start and drain a tile.  512 x 1152 over 8192: 12 tiles of 224
-// columns take 37 us, 36 of 64 columns 17.
-int fp8_gemm_columns(int M, const int *N, int nout, int blocks, int num_sms) {
-    const int m_tiles = (M + kFp8BM - 1) / kFp8BM, pairs = num_sms / 2;
-    int best = 224;
+// The tile width and cut with the least estimated cycles: waves of tiles over
+// the CTA pairs, a block of the contraction at the slowest of the MMAs (2 cycles
+// per column), the loads (42 bytes per cycle) and the issue (330 cycles), about
+// 5000 cycles to start and drain a tile, and for a cut tile, all pairs of whose
+// clusters have to be resident, 3000 and 25 per column for the exchange.
+// 512 x 1152 over 8192: 12 whole tiles of 224 columns take 37 us.
+void plan_fp8_gemm(Fp8GemmParams &p, const int *N, int nout, int blocks, bool may_split, int num_sms) {
+    // clusters of 1, 2, .. 8 pairs that a B200 holds at once
+    static const int kResident[8] = {74, 33, 22, 15, 11, 7, 7, 7};
+    const int m_tiles = (p.M + kFp8BM - 1) / kFp8BM, pairs = num_sms / 2;
     double least = 0;
     for (int bn : {224, 128, 64}) {
         long long tiles = 0;
         for (int i = 0; i < nout; ++i) tiles += (long long)m_tiles * ((N[i] + bn - 1) / bn);
-        const double block = std::max({2.0 * bn, (16384 + 64.0 * bn) / 46, 330.0});
-        const double cost = (double)((tiles + pairs - 1) / pairs) * (blocks * block + 5000);
-        if (least == 0 || cost < least) {
-            least = cost;
-            best = bn;
+        const double block = std::max({2.0 * bn, (16384 + 64.0 * bn) / 42, 330.0});
+        for (int s = 1; s <= 8; ++s) {
+            if (s > 1 && (!may_split || tiles > kResident[s - 1] || blocks < 4 * s)) break;
+            const double cost = (double)((tiles + pairs - 1) / pairs) * ((blocks + s - 1) / s * block + 5000) +
+                                (s > 1 ? 3000 + 25.0 * bn : 0);
+            if (least == 0 || cost < least) {
+                least = cost;
+                p.BN = bn;
+                p.split = s;
+            }
         }
     }
-    return best;
+    p.m_tiles = m_tiles;
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, Fp8Mode mode, int num_sms, cudaStream_t stream) {
@@ -603,20 +685,25 @@ cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, Fp8Mode mode, int num_sms, c
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!done[dev][mode][width].load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         done[dev][mode][width].store(true, std::memory_order_release);
     }
-    const int pairs = num_sms / 2 < p.num_tiles ? num_sms / 2 : p.num_tiles;
+    // a cut tile has a cluster of its own
+    const int clusters = p.split == 1 && num_sms / 2 < p.num_tiles ? num_sms / 2 : p.num_tiles;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * pairs);
+    cfg.gridDim = dim3(2 * p.split * clusters);
     cfg.blockDim = dim3(kFp8GemmThreads);
     cfg.dynamicSmemBytes = kGemmSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2 * p.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 

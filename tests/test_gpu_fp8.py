@@ -155,6 +155,8 @@ FORWARD = [
     (600, 384, [700], [320]), (40, 256, [64], [512]), (1, 256, [96], [1024]),
     # few tokens: whole tiles for every CTA, and tiles cut between them
     (2, 272, [19500, 300], [8, 16]), (20, 144, [40000], [0]), (1, 4112, [130], [0]), (128, 1040, [20000], [136]),
+    # tiles cut along the contraction
+    (200, 8208, [300], [72]), (513, 4112, [600, 31], [8, 0]), (140, 21504, [64], [256]),
     # tiles of 224 and of 128 columns, a second tile per CTA pair
     (2560, 272, [1568], [72]), (2560, 400, [890], [8]), (2816, 1296, [1121, 1000], [136, 0])]
 
@@ -186,6 +188,8 @@ def test_forward(M, K, N, r):
     (1, 16, [1], [8]), (1, 128, [128], [0]), (2, 1152, [1024, 256, 256], [16, 16, 16]), (5, 272, [17, 0, 129], [8, 16, 0]),
     (64, 1152, [512, 512], [64, 64]), (127, 528, [130], [40]), (200, 144, [449], [72]), (257, 640, [225, 31], [256, 8]),
     (333, 2000, [301, 264, 77], [40, 0, 8]), (512, 384, [700], [320]), (130, 256, [96], [1024]),
+    # dx cut along the contraction
+    (150, 304, [4000, 130], [8, 0]), (513, 272, [700, 900, 1300], [16, 0, 72]), (40, 64, [9000], [256]),
     # tiles of 224 and of 128 columns, a second tile per CTA pair
     (2560, 1568, [300, 77], [72, 0]), (2560, 896, [140], [16]), (2560, 272, [1568], [16]), (2816, 2128, [400, 1121], [136, 8])])
 def test_backward(M, K, N, r):
