@@ -32,6 +32,7 @@ struct Arena {
 };
 
 constexpr int kWsAlign = 16;
+constexpr int kMaxSize = 1 << 30;  // rows or columns: indexes past them still fit an int
 
 wl_status check_workspace(const void *ws, size_t have, size_t need) {
     if (need == 0) return WL_OK;
@@ -46,9 +47,10 @@ wl_status check_sizes(int M, int K, const Proj *projs, int P) {
     if (P < 1) return WL_ERR_INVALID_ARG;
     if (P > WL_MAX_PROJ) return WL_ERR_UNSUPPORTED;
     if (M < 0 || K < 0) return WL_ERR_INVALID_ARG;
+    if (M > kMaxSize || K > kMaxSize) return WL_ERR_UNSUPPORTED;
     for (int i = 0; i < P; ++i) {
         if (projs[i].N < 0 || projs[i].r < 0) return WL_ERR_INVALID_ARG;
-        if (projs[i].r > WL_MAX_RANK) return WL_ERR_UNSUPPORTED;
+        if (projs[i].r > WL_MAX_RANK || projs[i].N > kMaxSize) return WL_ERR_UNSUPPORTED;
     }
     if (K % 16 != 0) return WL_ERR_ALIGNMENT;
     for (int i = 0; i < P; ++i)
@@ -505,6 +507,7 @@ wl_status wl_quantize_fp8(const void *a, wl_type type, int rows, int cols, int b
     if (type != WL_BF16 && type != WL_F32) return WL_ERR_INVALID_ARG;
     if (block_rows != 1 && block_rows != kFp8Block) return WL_ERR_INVALID_ARG;
     if (rows < 0 || cols < 0) return WL_ERR_INVALID_ARG;
+    if (rows > kMaxSize || cols > kMaxSize) return WL_ERR_UNSUPPORTED;
     if (rows > 0 && cols > 0 && (!a || !codes || !scales)) return WL_ERR_INVALID_ARG;
     if (cols % 16 != 0 || !aligned(a, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return WL_ERR_ALIGNMENT;
     if (rows == 0 || cols == 0) return WL_OK;
@@ -559,6 +562,7 @@ wl_status wl_matmul_fp8(const uint8_t *a_codes, const uint8_t *a_scales, const u
                         size_t workspace_bytes, void *stream_ptr) {
     using namespace wl;
     if (M < 0 || N < 0 || K < 0) return WL_ERR_INVALID_ARG;
+    if (M > kMaxSize || N > kMaxSize || K > kMaxSize) return WL_ERR_UNSUPPORTED;
     if (M > 0 && N > 0) {
         if (!y) return WL_ERR_INVALID_ARG;
         if (K > 0 && (!a_codes || !a_scales || !b_codes || !b_scales)) return WL_ERR_INVALID_ARG;

@@ -305,12 +305,18 @@ __global__ void __launch_bounds__(kFp8GemmThreads, 1) fp8_gemm_kernel(const __gr
                 [&](int q, int kb, bool two) { return load(&p.tm_a[q], &p.tm_b[q], kb * 128, 128, two, kT, kBBytes); },
                 [&](int q, int j, bool two) { return load(&p.tm_t[q], &p.tm_u[q], j * 64, 64, two, false, kUBytes); });
         }
-        if (!ok && rank == 0 && lane == 0) {
-            // Let the copies already issued land before the pair exits; their
-            // bytes are counted here, in the leader.
-            const uint32_t left = issued < kFp8Stages ? issued : kFp8Stages;
-            for (uint32_t i = issued - left; i < issued; ++i)
-                mbar_wait(&full[i % kFp8Stages], (i / kFp8Stages) & 1u, p.status, 1000000ull);
+        if (!ok && lane == 0) {
+            // Let the copies already issued land before the pair exits.  Their
+            // bytes are counted in the leader; the other CTA gives its own time.
+            if (rank == 0) {
+                const uint32_t left = issued < kFp8Stages ? issued : kFp8Stages;
+                for (uint32_t i = issued - left; i < issued; ++i)
+                    mbar_wait(&full[i % kFp8Stages], (i / kFp8Stages) & 1u, p.status, 1000000ull);
+            } else {
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 1000000ull) {
+                }
+            }
         }
         __syncwarp();
     } else if (warp == 1) {

@@ -234,8 +234,9 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
         }
         if (elect_one()) {
             tc_commit(done);
-            // Outstanding MMAs end before TMEM is released, whatever happened.
-            if (!ok) mbar_wait(done, 0, p.status, kDrainNs);
+            // Outstanding MMAs end before TMEM is released, whether or not the
+            // epilogue waited for them.
+            mbar_wait(done, 0, p.status, kDrainNs);
         }
         __syncwarp();
     } else {

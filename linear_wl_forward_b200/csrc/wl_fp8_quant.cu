@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const T *__restrict
                                                              uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                                                              int pitch) {
     __shared__ float warp_max[8];
-    const int r0 = blockIdx.y * 128 + (threadIdx.x >> 3), c = blockIdx.x * 128 + (threadIdx.x & 7) * 16;
+    const int col_blocks = (cols + 127) / 128, rb = blockIdx.x / col_blocks, cb = blockIdx.x % col_blocks;
+    const int r0 = rb * 128 + (threadIdx.x >> 3), c = cb * 128 + (threadIdx.x & 7) * 16;
     Raw16<T> raw[4];
     float v[16], m = 0.f;
 #pragma unroll
@@ -112,10 +113,10 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const T *__restrict
         raw[i].unpack(v);
         if (r < rows && c < cols) *reinterpret_cast<uint4 *>(codes + (size_t)r * cols + c) = codes16(v, inv, infinities);
     }
-    uint8_t *srow = scales + (size_t)blockIdx.y * pitch;
-    if (threadIdx.x == 0) srow[blockIdx.x] = (uint8_t)(E + 127);
-    if (blockIdx.x == gridDim.x - 1) {  // bytes behind the last block
-        const int b = gridDim.x + threadIdx.x;
+    uint8_t *srow = scales + (size_t)rb * pitch;
+    if (threadIdx.x == 0) srow[cb] = (uint8_t)(E + 127);
+    if (cb == col_blocks - 1) {  // bytes behind the last block
+        const int b = col_blocks + threadIdx.x;
         if (b < pitch) srow[b] = 127;
     }
 }
@@ -162,9 +163,9 @@ cudaError_t launch_fp8_quantize_rows(Fp8RowsParams &p, wl_type type, cudaStream_
 cudaError_t launch_fp8_quantize_tiles(const void *a, wl_type type, int rows, int cols, uint8_t *codes, uint8_t *scales,
                                       cudaStream_t stream) {
     if (rows == 0 || cols == 0) return cudaSuccess;
-    // rows on the y axis: at most 65535 blocks, 8 M rows
-    dim3 grid((cols + 127) / 128, (rows + 127) / 128);
-    if (grid.y > 65535) return cudaErrorInvalidValue;
+    const long long blocks = (long long)((cols + 127) / 128) * ((rows + 127) / 128);
+    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)blocks;
     if (type == WL_BF16)
         quantize_tiles_kernel<<<grid, 256, 0, stream>>>(static_cast<const __nv_bfloat16 *>(a), rows, cols, codes, scales,
                                                         fp8_pitch(cols));
