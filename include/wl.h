@@ -345,8 +345,10 @@ typedef struct {
  *     bytes, 16-byte aligned, contents arbitrary; calls that overlap on the
  *     GPU need one each, and a captured graph keeps using the one it was
  *     captured with.
- * Any M >= 0.  Unlike the bf16 calls it may directly follow the kernel that
- * writes its weights.  Errors: those of wl_stacked_forward;
+ * Any M >= 0.  Results are reproducible for a given call; with and without a
+ * checkpoint a short call takes different kernels, whose sums differ in their
+ * order.  Unlike the bf16 calls it may directly follow the kernel that writes
+ * its weights.  Errors: those of wl_stacked_forward;
  * WL_ERR_ALIGNMENT for K % 16 != 0, r % 8 != 0 or misaligned pointers;
  * WL_ERR_INVALID_ARG for a workspace that is too small or only one of
  * x_codes and x_scales. */

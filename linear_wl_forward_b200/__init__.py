@@ -237,10 +237,21 @@ def fp8_scale_pitch(cols: int) -> int:
     return 4 * ((cols + 511) // 512)
 
 
+def _handle_on(device, stream):
+    """The current stream's handle; None when `device`, or a stream that was
+    given, has to be made current first (_On).  The handle alone: making a
+    Stream object costs as much as the launch."""
+    import torch
+
+    if stream is None and device.index == torch.cuda.current_device():
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return None
+
+
 class _On:
     """Makes `device` current and, when a stream (torch stream or raw handle)
     is given, that stream too, so that what the call allocates belongs to the
-    stream it runs on.  Gives the stream's handle."""
+    stream it runs on."""
 
     __slots__ = ("device", "stream", "stack")
 
@@ -251,22 +262,18 @@ class _On:
         import torch
 
         device, stream = self.device, self.stream
-        if stream is not None or device.index != torch.cuda.current_device():
-            with contextlib.ExitStack() as stack:
-                stack.enter_context(torch.cuda.device(device))
-                if stream is not None:
-                    if isinstance(stream, int):
-                        stream = torch.cuda.ExternalStream(stream, device=device)
-                    elif stream.device != device:
-                        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-                    stack.enter_context(torch.cuda.stream(stream))
-                self.stack = stack.pop_all()
-        # the handle alone: making a Stream object costs as much as the launch
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        with contextlib.ExitStack() as stack:
+            stack.enter_context(torch.cuda.device(device))
+            if stream is not None:
+                if isinstance(stream, int):
+                    stream = torch.cuda.ExternalStream(stream, device=device)
+                elif stream.device != device:
+                    raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+                stack.enter_context(torch.cuda.stream(stream))
+            self.stack = stack.pop_all()
 
     def __exit__(self, *exc):
-        if self.stack is not None:
-            self.stack.close()
+        self.stack.close()
 
 
 def _ptr_on(device, t, dtype, name, shape):
@@ -317,15 +324,17 @@ def quantize_fp8(a, block_rows=1, codes=None, scales=None, stream=None):
     R, C = a.shape
     shape = (-(-R // block_rows), fp8_scale_pitch(C))
     u8 = torch.uint8
-    with _On(dev, stream) as handle:
-        if codes is None:
-            codes = torch.empty(R, C, dtype=u8, device=dev)
-        if scales is None:
-            scales = torch.empty(*shape, dtype=u8, device=dev)
-        code = lib().wl_quantize_fp8(_ptr_on(dev, a, a.dtype, "a", a.shape), f32, R, C, block_rows,
-                                     _ptr_on(dev, codes, u8, "codes", (R, C)),
-                                     _ptr_on(dev, scales, u8, "scales", shape), handle)
-    _check(code, "wl_quantize_fp8")
+    handle = _handle_on(dev, stream)
+    if handle is None:
+        with _On(dev, stream):
+            return quantize_fp8(a, block_rows, codes, scales)
+    if codes is None:
+        codes = torch.empty(R, C, dtype=u8, device=dev)
+    if scales is None:
+        scales = torch.empty(*shape, dtype=u8, device=dev)
+    _check(lib().wl_quantize_fp8(_ptr_on(dev, a, a.dtype, "a", a.shape), f32, R, C, block_rows,
+                                 _ptr_on(dev, codes, u8, "codes", (R, C)), _ptr_on(dev, scales, u8, "scales", shape),
+                                 handle), "wl_quantize_fp8")
     return codes, scales
 
 
@@ -340,16 +349,17 @@ def matmul_fp8(a, b, y=None, stream=None):
     _need_cuda(bc, "b codes")
     (M, K), N = ac.shape, bc.shape[0]
     pitch, u8, bf16 = fp8_scale_pitch(K), torch.uint8, torch.bfloat16
-    with _On(dev, stream) as handle:
-        if y is None:
-            y = torch.empty(M, N, dtype=bf16, device=dev)
-        n = lib().wl_matmul_fp8_workspace(M, N, K)
-        ws = _workspace(n, dev)
-        code = lib().wl_matmul_fp8(_ptr_on(dev, ac, u8, "a codes", (M, K)), _ptr_on(dev, asc, u8, "a scales", (M, pitch)),
-                                   _ptr_on(dev, bc, u8, "b codes", (N, K)),
-                                   _ptr_on(dev, bsc, u8, "b scales", (-(-N // 128), pitch)),
-                                   _ptr_on(dev, y, bf16, "y", (M, N)), M, N, K, _ptr(ws), n, handle)
-    _check(code, "wl_matmul_fp8")
+    handle = _handle_on(dev, stream)
+    if handle is None:
+        with _On(dev, stream):
+            return matmul_fp8(a, b, y)
+    if y is None:
+        y = torch.empty(M, N, dtype=bf16, device=dev)
+    n = lib().wl_matmul_fp8_workspace(M, N, K)
+    ws = _workspace(n, dev)
+    _check(lib().wl_matmul_fp8(_ptr_on(dev, ac, u8, "a codes", (M, K)), _ptr_on(dev, asc, u8, "a scales", (M, pitch)),
+                               _ptr_on(dev, bc, u8, "b codes", (N, K)), _ptr_on(dev, bsc, u8, "b scales", (-(-N // 128), pitch)),
+                               _ptr_on(dev, y, bf16, "y", (M, N)), M, N, K, _ptr(ws), n, handle), "wl_matmul_fp8")
     return y
 
 
@@ -370,13 +380,11 @@ def _weight_fp8(dev, codes, scales, s, U, V, K):
 
     if (U is None) != (V is None):
         raise ValueError("U and V must both be given or both be None")
-    _need_cuda(codes, "codes")
     N, u8, bf16 = codes.shape[0], torch.uint8, torch.bfloat16
     r = 0
     up = vp = None
     if U is not None:
-        _need_cuda(U, "U")
-        r = U.shape[1]
+        r = U.shape[-1]
         up, vp = _ptr_on(dev, U, bf16, "U", (N, r)), _ptr_on(dev, V, bf16, "V", (K, r))
     return (_ptr_on(dev, codes, u8, "codes", (N, K)),
             _ptr_on(dev, scales, u8, "scales", (-(-N // 128), fp8_scale_pitch(K))),
@@ -406,23 +414,25 @@ def stacked_forward_fp8(x, projs, ys=None, checkpoint=False, stream=None):
     bf16); with checkpoint=True, (ys, Fp8Checkpoint) for stacked_backward_fp8."""
     import torch
 
-    dev = _need_cuda(x, "x")
+    dev, u8, bf16 = _need_cuda(x, "x"), torch.uint8, torch.bfloat16
     M, K = x.shape
-    with _On(dev, stream) as handle:
-        if ys is None:
-            ys = [torch.empty(M, p[0].shape[0], dtype=torch.bfloat16, device=dev) for p in projs]
-        ckpt = None
-        if checkpoint:
-            ckpt = Fp8Checkpoint(torch.empty(M, K, dtype=torch.uint8, device=dev),
-                                 torch.empty(M, fp8_scale_pitch(K), dtype=torch.uint8, device=dev),
-                                 [torch.empty(M, p[3].shape[1], dtype=torch.bfloat16, device=dev)
-                                  if p[3] is not None and p[3].shape[1] else None for p in projs])
-        xp, M, K, arr = _forward_fp8_args(x, projs, ys, ckpt.T if ckpt else None)
-        n = lib().wl_stacked_forward_fp8_workspace(M, K, arr, len(projs))
-        ws = _workspace(n, dev)
-        code = lib().wl_stacked_forward_fp8(xp, M, K, arr, len(projs), _ptr(ckpt.codes) if ckpt else None,
-                                            _ptr(ckpt.scales) if ckpt else None, _ptr(ws), n, handle)
-    _check(code, "wl_stacked_forward_fp8")
+    handle = _handle_on(dev, stream)
+    if handle is None:
+        with _On(dev, stream):
+            return stacked_forward_fp8(x, projs, ys, checkpoint)
+    if ys is None:
+        ys = [torch.empty(M, p[0].shape[0], dtype=bf16, device=dev) for p in projs]
+    ckpt = None
+    if checkpoint:
+        ckpt = Fp8Checkpoint(torch.empty(M, K, dtype=u8, device=dev), torch.empty(M, fp8_scale_pitch(K), dtype=u8, device=dev),
+                             [torch.empty(M, p[3].shape[-1], dtype=bf16, device=dev)
+                              if p[3] is not None and p[3].shape[-1] else None for p in projs])
+    xp, M, K, arr = _forward_fp8_args(x, projs, ys, ckpt.T if ckpt else None)
+    n = lib().wl_stacked_forward_fp8_workspace(M, K, arr, len(projs))
+    ws = _workspace(n, dev)
+    _check(lib().wl_stacked_forward_fp8(xp, M, K, arr, len(projs), _ptr(ckpt.codes) if ckpt else None,
+                                        _ptr(ckpt.scales) if ckpt else None, _ptr(ws), n, handle),
+           "wl_stacked_forward_fp8")
     return (ys, ckpt) if checkpoint else ys
 
 
@@ -462,8 +472,7 @@ class PreparedForwardFp8:
         if self._device.index != torch.cuda.current_device():
             with torch.cuda.device(self._device):
                 return self(stream)
-        handle = torch._C._cuda_getCurrentRawStream(self._device.index) if stream is None else _stream_handle(stream)
-        code = self._run(self._plan, handle)
+        code = self._run(self._plan, _handle_on(self._device, stream) if stream is None else _stream_handle(stream))
         if code:
             _check(code, "wl_run_fp8_plan")
         return self.ys
@@ -494,27 +503,30 @@ def stacked_backward_fp8(ckpt, dys, projs, need_dx=True, need_params=True, strea
     if not len(projs) == len(dys) == len(ckpt.T):
         raise ValueError(f"{len(projs)} projections, {len(dys)} gradients, {len(ckpt.T)} T")
     u8, bf16 = torch.uint8, torch.bfloat16
-    with _On(dev, stream) as handle:
-        xc = _ptr_on(dev, ckpt.codes, u8, "checkpoint codes", (M, K))
-        xs = _ptr_on(dev, ckpt.scales, u8, "checkpoint scales", (M, fp8_scale_pitch(K)))
-        arr = (_GradFp8 * max(len(projs), 1))()
-        per = []
-        for i, (p, dy, T) in enumerate(zip(projs, dys, ckpt.T)):
-            w, N, r = _weight_fp8(dev, *p, K)
-            ds = dU = dV = None
-            if need_params:
-                ds = torch.empty(N, dtype=torch.float32, device=dev)
-                if r:
-                    dU = torch.empty(N, r, dtype=bf16, device=dev)
-                    dV = torch.empty(K, r, dtype=bf16, device=dev)
-            per.append((ds, dU, dV))
-            arr[i] = _GradFp8(*w, _ptr_on(dev, T, bf16, "T", (M, r)) if r else None, _ptr_on(dev, dy, bf16, "dy", (M, N)),
-                              _ptr(ds), _ptr(dU), _ptr(dV), N, r)
-        dx = torch.empty(M, K, dtype=bf16, device=dev) if need_dx else None
-        n = lib().wl_stacked_backward_fp8_workspace(M, K, arr, len(projs))
-        ws = _workspace(n, dev)
-        code = lib().wl_stacked_backward_fp8(xc, xs, M, K, arr, len(projs), _ptr(dx), _ptr(ws), n, handle)
-    _check(code, "wl_stacked_backward_fp8")
+    handle = _handle_on(dev, stream)
+    if handle is None:
+        with _On(dev, stream):
+            return stacked_backward_fp8(ckpt, dys, projs, need_dx, need_params)
+    xc = _ptr_on(dev, ckpt.codes, u8, "checkpoint codes", (M, K))
+    xs = _ptr_on(dev, ckpt.scales, u8, "checkpoint scales", (M, fp8_scale_pitch(K)))
+    arr = (_GradFp8 * max(len(projs), 1))()
+    per = []
+    for i, (p, dy, T) in enumerate(zip(projs, dys, ckpt.T)):
+        w, N, r = _weight_fp8(dev, *p, K)
+        ds = dU = dV = None
+        if need_params:
+            ds = torch.empty(N, dtype=torch.float32, device=dev)
+            if r:
+                dU = torch.empty(N, r, dtype=bf16, device=dev)
+                dV = torch.empty(K, r, dtype=bf16, device=dev)
+        per.append((ds, dU, dV))
+        arr[i] = _GradFp8(*w, _ptr_on(dev, T, bf16, "T", (M, r)) if r else None, _ptr_on(dev, dy, bf16, "dy", (M, N)),
+                          _ptr(ds), _ptr(dU), _ptr(dV), N, r)
+    dx = torch.empty(M, K, dtype=bf16, device=dev) if need_dx else None
+    n = lib().wl_stacked_backward_fp8_workspace(M, K, arr, len(projs))
+    ws = _workspace(n, dev)
+    _check(lib().wl_stacked_backward_fp8(xc, xs, M, K, arr, len(projs), _ptr(dx), _ptr(ws), n, handle),
+           "wl_stacked_backward_fp8")
     return dx, per
 
 

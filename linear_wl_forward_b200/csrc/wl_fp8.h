@@ -213,4 +213,28 @@ void plan_fp8_stream(Fp8StreamParams &p);
 size_t fp8_stream_part_floats(const Fp8StreamParams &p);
 cudaError_t launch_fp8_stream(const Fp8StreamParams &p, cudaStream_t stream);
 
+// -------------------------------------------------- short calls, one launch ----
+constexpr int kFp8RowsMaxK = 2048;
+
+struct Fp8RowsSeg {
+    const uint8_t *codes, *w_scales;
+    const float *s;
+    const __nv_bfloat16 *U, *V;
+    __nv_bfloat16 *y;  // M x N
+    int N, r;
+    int cta_begin;     // plan
+};
+
+struct Fp8RowsForward {
+    Fp8RowsSeg seg[kMaxSeg];
+    int nseg;
+    int M, K, pitch;
+    const __nv_bfloat16 *x;
+    int blocks, grid;  // plan: 16-row blocks per CTA, CTAs
+};
+
+// False if the call is not short enough; needs everything but the plan.
+bool plan_fp8_rows(Fp8RowsForward &p);
+cudaError_t launch_fp8_rows(const Fp8RowsForward &p, cudaStream_t stream);
+
 }  // namespace wl

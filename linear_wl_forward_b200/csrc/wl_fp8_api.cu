@@ -262,7 +262,9 @@ struct wl_fp8_plan {
     bool zeros;                // K == 0: outputs are zero
     wl::Fp8RowsParams quant;   // njobs == 0: the rank-r launch quantises x, or nothing is to be done
     wl::LowrankParams lowrank;
-    bool few;                  // which of the two products
+    bool rows;                 // a short call: one launch
+    wl::Fp8RowsForward short_call;
+    bool few;                  // which of the two products otherwise
     wl::Fp8StreamParams stream;
     wl::Fp8GemmParams gemm;
 };
@@ -279,9 +281,27 @@ wl_status forward_plan(wl_fp8_plan &f, const wl_bf16 *x, int M, int K, const wl_
     f.quant.njobs = f.lowrank.njobs = f.stream.nseg = f.gemm.nout = 0;
     f.stream.units = f.gemm.num_tiles = 0;
     f.few = M <= kFp8StreamMaxM;
+    f.rows = false;
     f.zeros = M > 0 && K == 0;
     if (f.zeros) std::memcpy(f.projs, projs, sizeof(wl_proj_fp8) * P);
     if (M == 0 || K == 0) return WL_OK;
+    bool saved = x_codes != nullptr;  // a checkpoint is wanted
+    Fp8RowsForward &sc = f.short_call;
+    sc.nseg = 0;
+    for (int i = 0; i < P; ++i) {
+        const wl_proj_fp8 &q = projs[i];
+        saved = saved || (q.T && q.r > 0);
+        if (q.N > 0)
+            sc.seg[sc.nseg++] = Fp8RowsSeg{q.codes, q.scales, q.s, bf16(q.U), bf16(q.V), bf16(q.y), q.N, q.r, 0};
+    }
+    sc.M = M;
+    sc.K = K;
+    sc.pitch = fp8_pitch(K);
+    sc.x = bf16(x);
+    if (!saved && plan_fp8_rows(sc)) {
+        f.rows = true;
+        return WL_OK;
+    }
     uint8_t *codes = x_codes ? x_codes : l.codes, *scales = x_scales ? x_scales : l.scales;
     const Fp8Mat X{codes, scales, K, fp8_pitch(K)};
     int N[kMaxSeg], tiles = 0;  // tiles: counters of the few-token kernel
@@ -345,6 +365,7 @@ wl_status forward_launch(wl_fp8_plan &f, const Device &dev, cudaStream_t stream)
         }
         return WL_OK;
     }
+    if (f.rows) return from_cuda(launch_fp8_rows(f.short_call, stream));
     if (f.quant.njobs > 0 && launch_fp8_quantize_rows(f.quant, WL_BF16, stream) != cudaSuccess) return WL_ERR_CUDA;
     if (launch_fp8_lowrank(f.lowrank, kLowrankRows, stream) != cudaSuccess) return WL_ERR_CUDA;
     return from_cuda(f.few ? launch_fp8_stream(f.stream, stream) : launch_fp8_gemm(f.gemm, kFp8Plain, dev.sms, stream));

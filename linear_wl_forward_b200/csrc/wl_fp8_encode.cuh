@@ -16,6 +16,11 @@ __device__ __forceinline__ int scale_exponent(float amax) {
     return E < -127 ? -127 : E;
 }
 
+// 2^(e - 127) of a scale byte: e = 0 is the subnormal 2^-127, 255 the NaN scale.
+__device__ __forceinline__ float scale_value(uint32_t e) {
+    return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7FC00000u : e << 23);
+}
+
 // 2^-E; E in [-127, 120].
 __device__ __forceinline__ float inverse_scale(int E) { return __uint_as_float((uint32_t)(127 - E) << 23); }
 

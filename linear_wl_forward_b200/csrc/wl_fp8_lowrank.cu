@@ -264,9 +264,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
                 for (int s = 0; s < 2; ++s) {
                     const int k = s * 32 + k0;
                     const uint4 c = *reinterpret_cast<const uint4 *>(st + kATile + k * 128 + seg * 16);
-                    // 2^(e - 127); e = 0 is the subnormal 2^-127, e = 255 the NaN scale
-                    const float sc = e[s] == 0 ? __uint_as_float(0x00400000u)
-                                               : e[s] == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(e[s] << 23);
+                    const float sc = scale_value(e[s]);
                     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
                     uint32_t o[8];
 #pragma unroll

@@ -153,7 +153,8 @@ def test_captured_and_replayed(M, K, N, r):
     eager = []
     for x, dy in zip(xs, dys):
         ys, ckpt = wl.stacked_forward_fp8(x, dev, checkpoint=True)
-        eager.append((ys, ckpt, wl.stacked_backward_fp8(ckpt, dy, dev)))
+        # (a short call without a checkpoint has a kernel of its own)
+        eager.append((ys, ckpt, wl.stacked_backward_fp8(ckpt, dy, dev), wl.stacked_forward_fp8(x, dev)))
     x, dy = xs[0].clone(), [d.clone() for d in dys[0]]
     handle = wl.prepare_stacked_fp8(x, dev)
     handle()
@@ -173,8 +174,8 @@ def test_captured_and_replayed(M, K, N, r):
         for gr, ys, ckpt, dx, per, hy in graphs:
             gr.replay()
             torch.cuda.synchronize()
-            ey, eckpt, (edx, eper) = eager[i]
-            assert all(torch.equal(a, b) for a, b in zip(ys + hy, ey + ey))
+            ey, eckpt, (edx, eper), eplain = eager[i]
+            assert all(torch.equal(a, b) for a, b in zip(ys + hy, ey + eplain))
             assert torch.equal(ckpt.codes, eckpt.codes) and torch.equal(dx, edx)
             for p, q in zip(per, eper):
                 assert all((a is None and b is None) or torch.equal(a, b) for a, b in zip(p, q))
