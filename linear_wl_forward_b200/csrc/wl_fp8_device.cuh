@@ -57,6 +57,12 @@ __device__ __forceinline__ float ld_cluster(const float *p, uint32_t rank) {
     return v;
 }
 
+// TMEM and kernels that share an SM: an allocation waits until there is room,
+// so a CTA that holds TMEM must never wait for another CTA or kernel.  The
+// kernels that leave room for a neighbour therefore allocate after their wait
+// for the previous kernel (which may itself be waiting for TMEM) and release
+// before they meet the other CTAs of their cluster.
+
 // What a kernel's waits need: where errors go, when to give up, and a flag in
 // shared memory by which one warp's time-out stops the others.
 struct WaitLimits {

@@ -154,6 +154,12 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
         *abort_flag = 0;
         fence_barrier_init();
     }
+    __syncthreads();
+    // Dependents start once everything before this kernel is complete.
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    if (kMode == kLowrankRows && p.quant.a)
+        for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < p.quant.n_zero; i += gridDim.x * blockDim.x) p.quant.zero[i] = 0;
     if (warp == 1) {
         tmem_alloc(tmem_slot, p.tmem_cols);
         tmem_relinquish();
@@ -162,11 +168,6 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // Dependents start once everything before this kernel is complete.
-    pdl_wait_primary();
-    pdl_launch_dependents();
-    if (kMode == kLowrankRows && p.quant.a)
-        for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < p.quant.n_zero; i += gridDim.x * blockDim.x) p.quant.zero[i] = 0;
 
     const uint32_t a_bytes = kMode == kLowrankRows ? (uint32_t)p.a_bytes : kATile;
     const uint32_t b_off = a_bytes + (kCodes ? kCodeTile : 0);
@@ -314,6 +315,12 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
                 }
             }
     }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, p.tmem_cols);
+    }
     if (S > 1) {
         __syncwarp();
         cluster_sync();  // every CTA's sums are in its shared memory
@@ -356,12 +363,6 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
         }
         __syncwarp();
         cluster_sync();  // no CTA leaves while its sums are read
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, p.tmem_cols);
     }
 }
 

@@ -147,15 +147,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, tmem_cols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    if (warp != 0) pdl_wait_primary();
+    uint32_t tmem = 0;
+    if (warp != 0) {
+        pdl_wait_primary();
+        if (warp == 1) {
+            tmem_alloc(tmem_slot, tmem_cols);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        asm volatile("bar.sync 3, 224;" ::: "memory");  // all but the producer, which is under way
+        tc_fence_after();
+        tmem = *tmem_slot;
+    }
 
     if (warp == 0) {
         // ------------------------------------------------------ producer ----
@@ -418,6 +422,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
         }
     }
 
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, tmem_cols);
+    }
     if (p.cluster > 1) {
         __syncwarp();
         cluster_sync();  // every rank's sums are in its shared memory
@@ -441,12 +451,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
         }
         __syncwarp();
         cluster_sync();  // no CTA leaves while its sums are read
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, tmem_cols);
     }
 }
 
