@@ -37,8 +37,8 @@ struct Fp8RowsJob {
     uint8_t *scales;
     long long warp_begin;  // filled by the launcher
 };
-// Up to kMaxSeg matrices of `rows` rows in one launch (all with column scales
-// or none), which also clears n_zero words at `zero`.
+// One matrix, or up to kMaxSeg bf16 ones with column scales, of `rows` rows in
+// one launch, which also clears n_zero words at `zero`.
 struct Fp8RowsParams {
     Fp8RowsJob job[kMaxSeg];
     int njobs, rows;

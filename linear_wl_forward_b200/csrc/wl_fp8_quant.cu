@@ -9,6 +9,8 @@
 //
 // Both kernels read each element once and write one byte for it; the memory
 // traffic bounds them.
+#include <algorithm>
+
 #include "wl_common.cuh"
 #include "wl_fp8.h"
 #include "wl_fp8_encode.cuh"
@@ -23,7 +25,7 @@ namespace {
 // than their loads in flight give.  With column scales neighbouring warps take
 // neighbouring rows of the same columns, so the scales (twice the data's bytes
 // per element) come from L1.
-template <typename T, bool kColScale>
+template <typename T, bool kColScale, bool kMany>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constant__ Fp8RowsParams p) {
     // Dependents start once everything before this kernel is complete, so they
     // may read its predecessors' results without waiting for this kernel.
@@ -33,7 +35,8 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constan
     long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     int jx = 0;
-    while (jx + 1 < p.njobs && w >= p.job[jx + 1].warp_begin) ++jx;
+    if (kMany)
+        while (jx + 1 < p.njobs && w >= p.job[jx + 1].warp_begin) ++jx;
     const Fp8RowsJob &jb = p.job[jx];
     const int words = WL_FP8_SCALE_PITCH(jb.cols) / 4;
     w -= jb.warp_begin;
@@ -76,48 +79,51 @@ __device__ __forceinline__ float block_max(float m, float *warp_max) {
 // One CTA: a 128 x 128 block, 16 elements of four rows per thread, kept as
 // they are stored so that more CTAs fit an SM.
 template <typename T>
-__global__ void __launch_bounds__(256) quantize_tiles_kernel(const T *__restrict__ a, int rows, int cols,
+__global__ void __launch_bounds__(256, 3) quantize_tiles_kernel(const T *__restrict__ a, int rows, int cols,
                                                              uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                                                              int pitch) {
     __shared__ float warp_max[8];
-    const int col_blocks = (cols + 127) / 128, rb = blockIdx.x / col_blocks, cb = blockIdx.x % col_blocks;
-    const int r0 = rb * 128 + (threadIdx.x >> 3), c = cb * 128 + (threadIdx.x & 7) * 16;
-    Raw16<T> raw[4];
-    float v[16], m = 0.f;
+    const int c = blockIdx.x * 128 + (threadIdx.x & 7) * 16;
+    // a grid has at most 65535 rows of CTAs
+    for (int rb = blockIdx.y; rb < (rows + 127) / 128; rb += gridDim.y) {
+        const int r0 = rb * 128 + (threadIdx.x >> 3);
+        Raw16<T> raw[4];
+        float v[16], m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 32 * i;
-        raw[i].load(a + (size_t)(r < rows ? r : 0) * cols + c, r < rows ? cols - c : 0, true);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        raw[i].unpack(v);
-        m = fmaxf(m, amax16(v));
-    }
-    m = block_max(m, warp_max);
-    const bool infinities = isinf(m);
-    if (infinities) {  // the same for the whole block
-        m = 0.f;
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + 32 * i;
+            raw[i].load(a + (size_t)(r < rows ? r : 0) * cols + c, r < rows ? cols - c : 0, true);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             raw[i].unpack(v);
-            m = fmaxf(m, finite_amax16(v));
+            m = fmaxf(m, amax16(v));
         }
         m = block_max(m, warp_max);
-    }
-    const int E = scale_exponent(m);
-    const float inv = inverse_scale(E);
+        const bool infinities = isinf(m);
+        if (infinities) {  // the same for the whole block
+            m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 32 * i;
-        raw[i].unpack(v);
-        if (r < rows && c < cols) *reinterpret_cast<uint4 *>(codes + (size_t)r * cols + c) = codes16(v, inv, infinities);
-    }
-    uint8_t *srow = scales + (size_t)rb * pitch;
-    if (threadIdx.x == 0) srow[cb] = (uint8_t)(E + 127);
-    if (cb == col_blocks - 1) {  // bytes behind the last block
-        const int b = col_blocks + threadIdx.x;
-        if (b < pitch) srow[b] = 127;
+            for (int i = 0; i < 4; ++i) {
+                raw[i].unpack(v);
+                m = fmaxf(m, finite_amax16(v));
+            }
+            m = block_max(m, warp_max);
+        }
+        const int E = scale_exponent(m);
+        const float inv = inverse_scale(E);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + 32 * i;
+            raw[i].unpack(v);
+            if (r < rows && c < cols) *reinterpret_cast<uint4 *>(codes + (size_t)r * cols + c) = codes16(v, inv, infinities);
+        }
+        uint8_t *srow = scales + (size_t)rb * pitch;
+        if (threadIdx.x == 0) srow[blockIdx.x] = (uint8_t)(E + 127);
+        if (blockIdx.x == gridDim.x - 1) {  // bytes behind the last block
+            const int b = gridDim.x + threadIdx.x;
+            if (b < pitch) srow[b] = 127;
+        }
     }
 }
 
@@ -155,17 +161,18 @@ cudaError_t launch_fp8_quantize_rows(Fp8RowsParams &p, wl_type type, cudaStream_
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, type == WL_F32             ? quantize_rows_kernel<float, false>
-                                    : p.job[0].colscale != nullptr ? quantize_rows_kernel<__nv_bfloat16, true>
-                                                                   : quantize_rows_kernel<__nv_bfloat16, false>, p);
+    // several matrices are only ever gradients with their column scales
+    void (*const kernel)(Fp8RowsParams) = type == WL_F32 ? quantize_rows_kernel<float, false, false>
+                                          : p.job[0].colscale == nullptr ? quantize_rows_kernel<__nv_bfloat16, false, false>
+                                                                         : quantize_rows_kernel<__nv_bfloat16, true, true>;
+    if (p.njobs > 1 && p.job[0].colscale == nullptr) return cudaErrorInvalidValue;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 cudaError_t launch_fp8_quantize_tiles(const void *a, wl_type type, int rows, int cols, uint8_t *codes, uint8_t *scales,
                                       cudaStream_t stream) {
     if (rows == 0 || cols == 0) return cudaSuccess;
-    const long long blocks = (long long)((cols + 127) / 128) * ((rows + 127) / 128);
-    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-    const unsigned grid = (unsigned)blocks;
+    const dim3 grid((cols + 127) / 128, std::min((rows + 127) / 128, 65535));
     if (type == WL_BF16)
         quantize_tiles_kernel<<<grid, 256, 0, stream>>>(static_cast<const __nv_bfloat16 *>(a), rows, cols, codes, scales,
                                                         fp8_pitch(cols));
