@@ -344,7 +344,8 @@ typedef struct {
  *   workspace : at least wl_stacked_forward_fp8_workspace(M, K, projs, P)
  *     bytes, 16-byte aligned, contents arbitrary; calls that overlap on the
  *     GPU need one each, and a captured graph keeps using the one it was
- *     captured with.
+ *     captured with.  (The library's first call on a device must not be
+ *     captured: it allocates the status words.)
  * Any M >= 0.  Results are reproducible for a given call; with and without a
  * checkpoint a short call takes different kernels, whose sums differ in their
  * order.  Unlike the bf16 calls it may directly follow the kernel that writes
