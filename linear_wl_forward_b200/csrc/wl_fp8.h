@@ -78,8 +78,8 @@ struct LowrankJob {
     int tile_begin;
 };
 
-// Rows mode, I <= 128: the launch also quantises its A (rows x cols, bf16,
-// dense) in 1 x 128 blocks and clears n_zero words; a == nullptr: nothing.
+// Rows mode, every job with this A: the launch also quantises A (rows x cols,
+// bf16, dense) in 1 x 128 blocks and clears n_zero words; a == nullptr: nothing.
 struct LowrankQuant {
     const __nv_bfloat16 *a;
     uint8_t *codes, *scales;

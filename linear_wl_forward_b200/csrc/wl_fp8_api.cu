@@ -320,8 +320,10 @@ wl_status forward_plan(wl_fp8_plan &f, const wl_bf16 *x, int M, int K, const wl_
             return st;
     }
     plan_fp8_lowrank(f.lowrank, kLowrankRows, dev.sms);
-    if (f.few && f.lowrank.njobs > 0) {  // one launch less in a decode step
-        f.lowrank.quant = LowrankQuant{bf16(x), codes, scales, M, K, l.counters, tiles};
+    // One launch less where x is small: beside 2 M elements the few warps that
+    // quantise there would be slower than a launch of their own.
+    if (f.lowrank.njobs > 0 && (f.few || (long long)M * K <= 2 << 20)) {
+        f.lowrank.quant = LowrankQuant{bf16(x), codes, scales, M, K, l.counters, f.few ? tiles : 0};
     } else {
         f.quant.job[0] = Fp8RowsJob{x, K, K, nullptr, codes, K, scales, 0};
         f.quant.njobs = 1;

@@ -427,7 +427,7 @@ cudaError_t launch_fp8_lowrank(const LowrankParams &p, LowrankMode mode, cudaStr
     if (p.njobs == 0) return cudaSuccess;
     // an MMA reads 128 rows of A, so the last stage's tile may end behind the stages
     const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + std::max<size_t>((3 * kMaxStages + 1) * 8 + 32, kATile);
-    if (p.stages > kMaxStages || smem > 227 * 1024 || (p.quant.a && p.a_bytes > (int)kATile)) return cudaErrorInvalidValue;
+    if (p.stages > kMaxStages || smem > 227 * 1024 || (p.quant.a && mode != kLowrankRows)) return cudaErrorInvalidValue;
     void (*const kernels[3])(LowrankParams) = {lowrank_kernel<kLowrankRows>, lowrank_kernel<kLowrankCols>,
                                                lowrank_kernel<kLowrankCodes>};
     static std::atomic<bool> done[64][3] = {};
