@@ -25,9 +25,9 @@ struct Arena {
     explicit Arena(void *p) : base(static_cast<uint8_t *>(p)) {}
     template <typename T>
     T *take(size_t n) {
-        T *p = reinterpret_cast<T *>(base + used);
+        const size_t at = used;
         used += (n * sizeof(T) + 255) & ~size_t(255);
-        return base ? p : nullptr;
+        return base ? reinterpret_cast<T *>(base + at) : nullptr;
     }
 };
 
@@ -147,7 +147,6 @@ wl_status set_part(Fp8GemmParams &g, int i, const Fp8Mat &A, int M, int a_cols, 
     if (st == WL_OK && r > 0) st = encode_map_2d(&g.tm_u[i], U, r, lr_rows, r, 64, g.BN / 2);
     return st;
 }
-
 
 Fp8Out &add_out(Fp8GemmParams &g, int N, int part0, int nparts) {
     Fp8Out &o = g.out[g.nout++];

@@ -15,15 +15,13 @@
 // CTA would stage 48 KB against 512).  An SM takes in about 46 bytes per cycle,
 // so the loads (650 cycles per block) bound long products.  224 columns,
 // because two accumulators of that width and the scales fit the 512 columns
-// of TMEM; calls with few such tiles take 128 or 64 columns (fp8_gemm_columns).  The accumulators swap roles from tile to tile: tile i sums into
-// region i & 1 and its rank-r term goes to the other region, just before the
-// tile's last blocks, when the epilogue has drained tile i - 1 from there;
-// the epilogue moves the rank-r term into registers while those last blocks
-// run, which frees that region for tile i + 1.  So the tensor pipe waits for
-// no epilogue on long contractions.
-//
-// A product with few tiles is cut along its contraction: the pairs of a cluster
-// share a tile and add their sums over distributed shared memory in rank order.
+// of TMEM; calls with few such tiles take 128 or 64 columns (plan_fp8_gemm).
+// The accumulators swap roles from tile to tile: tile i sums into region i & 1
+// and its rank-r term goes to the other region, just before the tile's last
+// blocks, when the epilogue has drained tile i - 1 from there; the epilogue
+// moves the rank-r term into registers while those last blocks run, which
+// frees that region for tile i + 1.  So the tensor pipe waits for no epilogue
+// on long contractions.
 //
 // A product with few tiles is cut along its contraction: the pairs of a cluster
 // share a tile and add their sums over distributed shared memory in rank order.
@@ -122,15 +120,7 @@ __device__ __forceinline__ Tile tile_of(const Fp8GemmParams &p, int t) {
     return {o, (local % p.m_tiles) * kFp8BM, (local / p.m_tiles) * p.BN};
 }
 
-// A tile's work in issue order, up to two blocks (one stage) at a time:
-// main(part, block, two) part by part, and before the last kLrLead stages of
-// them low(part, block, two) for the rank-r blocks of every part.  Stops when
-// either returns false.  The issuing warp's instructions bound how fast the
-// tensor pipe is fed: an MMA takes it about 40 cycles, a barrier wait 70 and a
-// commit 46, against 448 cycles of MMAs per block, so a stage holds two blocks
-// and the order is in the loops, not in per-block state (with both per block a
-// block took 950 cycles).
-// `r`: the stages that this pair runs, and where the rank-r blocks come.
+// The stages that a pair runs, and the one before which the rank-r blocks come.
 struct Stages {
     int begin, end, low_at;
 };
@@ -145,6 +135,14 @@ __device__ __forceinline__ Stages stages_of(const Fp8GemmParams &p, const Fp8Out
     return r;
 }
 
+// A tile's work in issue order, up to two blocks (one stage) at a time:
+// main(part, block, two) part by part, and before the last kLrLead stages of
+// them low(part, block, two) for the rank-r blocks of every part.  Stops when
+// either returns false.  The issuing warp's instructions bound how fast the
+// tensor pipe is fed: an MMA takes it about 40 cycles, a barrier wait 70 and a
+// commit 46, against 448 cycles of MMAs per block, so a stage holds two blocks
+// and the order is in the loops, not in per-block state (with both per block a
+// block took 950 cycles).
 template <typename Main, typename Low>
 __device__ __forceinline__ bool for_stages(const Fp8GemmParams &p, const Fp8Out &o, const Stages &r, Main main, Low low) {
     int i = 0;

@@ -137,14 +137,20 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
                 }
             }
         }
+        // over the lanes that share the columns (every groups-th)
 #pragma unroll
-        for (int m = 0; m < kM; ++m)
+        for (int o = 16; o > 0; o >>= 1)
+            if (o >= groups) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float a = acc[m][i];
-                for (int o = groups; o < 32; o <<= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-                if (lane < groups) tp[(warp * kM + m) * 32 + j + i] = a;
+                for (int m = 0; m < kM; ++m)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[m][i] += __shfl_xor_sync(0xffffffffu, acc[m][i], o);
             }
+        if (lane < groups)
+#pragma unroll
+            for (int m = 0; m < kM; ++m)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) tp[(warp * kM + m) * 32 + j + i] = acc[m][i];
     }
 
     // W0 x
@@ -227,14 +233,15 @@ size_t rows_smem(const Fp8RowsForward &p) {
 }  // namespace
 
 // Calls that take this kernel: what every CTA repeats (x, V) has to stay small
-// beside a launch.  Gemma-3-1B's q/k/v at one token: 5.8 us, against 9.1 in two
-// launches.
+// beside a launch.  1536 x 1152 with rank 16, against two launches, us: one token
+// 5.3 / 9.7, four 6.5 / 9.8, eight 10.9 / 10.0; 2048 x 2048 with rank 32 at one
+// token 9.0 / 9.9, at four 11.1 / 10.1; without ranks 4.0 to 7.1 / 8.3.
 bool plan_fp8_rows(Fp8RowsForward &p) {
     if (p.M < 1 || p.M > kTokens || p.K > kFp8RowsMaxK) return false;
     int blocks = 0;
     for (int i = 0; i < p.nseg; ++i) {
         const Fp8RowsSeg &sg = p.seg[i];
-        if (sg.r > 32 || (long long)p.K * sg.r > 64 * 1024) return false;
+        if (sg.r > 32 || (long long)tokens_of(p.M) * p.K * sg.r > 96 * 1024) return false;
         blocks += (sg.N + 15) / 16;
     }
     if (blocks > 4 * kFp8StreamMaxGrid) return false;

@@ -150,7 +150,7 @@ def test_matmul_nan_stays_in_its_row():
 FORWARD = [
     # short calls: every token count, ranks up to 32, one to four row blocks per CTA
     (1, 1152, [1024, 256, 256], [16, 16, 16]), (2, 1152, [4096, 4096], [16, 8]), (3, 2048, [70, 3], [32, 0]),
-    (4, 16, [200], [24]), (5, 2032, [2500], [32]), (8, 400, [9000, 17], [8, 24]), (7, 1040, [16], [0]),
+    (4, 16, [200], [24]), (5, 352, [2500], [32]), (8, 400, [9000, 17], [8, 24]), (7, 2032, [16], [0]), (1, 2048, [500], [32]),
     (9, 1152, [1024], [16]), (1, 2064, [256], [16]), (1, 1152, [256], [40]),
     (1, 16, [1], [0]), (1, 128, [128], [8]), (1, 1152, [1024, 256, 256], [16, 16, 16]), (2, 5376, [300], [256]),
     (3, 272, [17, 0, 129], [8, 16, 0]), (5, 2064, [257], [72]), (8, 1024, [1152], [64]), (16, 1040, [1000, 8], [128, 256]),
