@@ -111,6 +111,7 @@ constexpr int kFp8GemmThreads = 384;
 constexpr int kFp8Stages = 3;
 constexpr int kFp8BlockBytes = 32768;  // 16 KB of A (or T), up to 16 KB of B (or U)
 constexpr int kFp8StageBytes = 2 * kFp8BlockBytes;
+constexpr int kFp8RangeBlocks = 64;  // blocks of the contraction per range of column sums
 constexpr int kFp8SfSlots = 4;
 constexpr int kFp8SfBytes = 1536;      // four blocks of scales: 128 rows of A, 256 of B
 
@@ -129,7 +130,7 @@ struct Fp8Out {
     int tile_begin;
     // column sums instead of y (kFp8ColSums)
     const __nv_bfloat16 *dy;  // M x N
-    float *sums;              // [ceil(M / 32)][N]: sum over 32 rows of dy (.) (A B^T)
+    float *sums;              // [ranges][ceil(M / 32)][N]: sums over 32 rows of dy (.) (A B^T)
 };
 
 struct Fp8GemmParams {
@@ -142,6 +143,10 @@ struct Fp8GemmParams {
     int nout;
     int M, BN;
     int split;        // CTA pairs that share a tile
+    // Column sums: ranges of the contraction that a tile is summed in, one after
+    // the other.  The tensor cores' sums are cut off, not rounded, at each step,
+    // so their error grows with their length (2e-6 of ds at 20000 columns).
+    int ranges;
     int m_tiles, num_tiles;
     int *status;
     unsigned long long timeout_ns;
@@ -153,7 +158,7 @@ enum Fp8Mode {
     kFp8ColSums       // K-major, the epilogue forms column sums: ds
 };
 
-// Sets BN, split and m_tiles for M rows (set), outputs of N[0..nout) columns and
+// Sets BN, split, ranges (1) and m_tiles for M rows (set), outputs of N[0..nout) columns and
 // a contraction of `blocks` blocks.
 void plan_fp8_gemm(Fp8GemmParams &p, const int *N, int nout, int blocks, bool may_split, int num_sms);
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, Fp8Mode mode, int num_sms, cudaStream_t stream);

@@ -2,6 +2,7 @@
 // the order of the launches.  Contracts in include/wl.h.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 #include <memory>
@@ -154,7 +155,7 @@ Fp8Out &add_out(Fp8GemmParams &g, int N, int part0, int nparts) {
     o.part0 = part0;
     o.nparts = nparts;
     o.tile_begin = g.num_tiles;
-    g.num_tiles += g.m_tiles * ((N + g.BN - 1) / g.BN);
+    g.num_tiles += g.m_tiles * ((N + g.BN - 1) / g.BN);  // times g.ranges, in the end
     return o;
 }
 
@@ -381,8 +382,11 @@ struct BackwardLayout {
     size_t bytes;
 };
 
+// Ranges of the contraction in which ds is summed.
+int sum_ranges(int K) { return std::max(1, (K + kFp8Block * kFp8RangeBlocks - 1) / (kFp8Block * kFp8RangeBlocks)); }
+
 // Sizes alone: a copy of dy is laid out wherever one could be needed.
-BackwardLayout backward_layout(int M, const wl_grad_fp8 *projs, int P, void *ws) {
+BackwardLayout backward_layout(int M, int K, const wl_grad_fp8 *projs, int P, void *ws) {
     BackwardLayout l = {};
     Arena a(ws);
     for (int i = 0; i < P; ++i) {
@@ -391,7 +395,7 @@ BackwardLayout backward_layout(int M, const wl_grad_fp8 *projs, int P, void *ws)
         l.E[i] = a.take<__nv_bfloat16>((size_t)M * projs[i].r);
         l.E_low[i] = a.take<__nv_bfloat16>((size_t)M * projs[i].r);
         l.dy[i] = a.take<__nv_bfloat16>(projs[i].r > 0 ? (size_t)M * round16(projs[i].N) : 0);
-        l.sums[i] = a.take<float>((size_t)((M + 31) / 32) * projs[i].N);
+        l.sums[i] = a.take<float>((size_t)sum_ranges(K) * ((M + 31) / 32) * projs[i].N);
     }
     l.bytes = a.used;
     return l;
@@ -458,7 +462,7 @@ wl_status backward_run(const uint8_t *x_codes, const uint8_t *x_scales, int M, i
     Fp8RowsParams quant = {};
     quant.rows = M;
     Fp8SumParams sums = {};
-    sums.n_rows = (M + 31) / 32;
+    sums.n_rows = sum_ranges(K) * ((M + 31) / 32);
     LowrankParams le, lu, lv;
     init_lowrank(le, dev);
     init_lowrank(lu, dev);
@@ -514,6 +518,8 @@ wl_status backward_run(const uint8_t *x_codes, const uint8_t *x_scales, int M, i
         o.y = bf16(dx);
         if (launch_fp8_gemm(gx, kFp8Transposed, dev.sms, stream) != cudaSuccess) return WL_ERR_CUDA;
     }
+    gs.ranges = sum_ranges(K);
+    gs.num_tiles *= gs.ranges;
     if (launch_fp8_gemm(gs, kFp8ColSums, dev.sms, stream) != cudaSuccess) return WL_ERR_CUDA;
     return from_cuda(launch_fp8_sum_rows(sums, stream));
 }
@@ -663,7 +669,7 @@ void wl_free_fp8_plan(wl_fp8_plan *plan) { delete plan; }
 size_t wl_stacked_backward_fp8_workspace(int M, int K, const wl_grad_fp8 *projs, int P) {
     using namespace wl;
     if (check_sizes(M, K, projs, P) != WL_OK) return 0;
-    return backward_layout(M, projs, P, nullptr).bytes;
+    return backward_layout(M, K, projs, P, nullptr).bytes;
 }
 
 wl_status wl_stacked_backward_fp8(const uint8_t *x_codes, const uint8_t *x_scales, int M, int K,
@@ -672,7 +678,7 @@ wl_status wl_stacked_backward_fp8(const uint8_t *x_codes, const uint8_t *x_scale
     using namespace wl;
     wl_status st = backward_check(x_codes, x_scales, M, K, projs, P, dx);
     if (st != WL_OK) return st;
-    const BackwardLayout l = backward_layout(M, projs, P, workspace);
+    const BackwardLayout l = backward_layout(M, K, projs, P, workspace);
     if (M > 0 && (st = check_workspace(workspace, workspace_bytes, l.bytes)) != WL_OK) return st;
     Device dev;
     if ((st = device_info(&dev.sms, &dev.status)) != WL_OK) return st;

@@ -114,6 +114,7 @@ struct Tile {
     int out, m0, n0;
 };
 __device__ __forceinline__ Tile tile_of(const Fp8GemmParams &p, int t) {
+    t /= p.ranges;
     int o = 0;
     while (o + 1 < p.nout && t >= p.out[o + 1].tile_begin) ++o;
     const int local = t - p.out[o].tile_begin;
@@ -125,12 +126,14 @@ struct Stages {
     int begin, end, low_at;
 };
 
-__device__ __forceinline__ Stages stages_of(const Fp8GemmParams &p, const Fp8Out &o, int pair) {
+// Piece `pair` of p.split, or, for tile t of a product summed in ranges, its range.
+__device__ __forceinline__ Stages stages_of(const Fp8GemmParams &p, const Fp8Out &o, int pair, int t) {
     int total = 0;
     for (int q = 0; q < o.nparts; ++q) total += (p.part[o.part0 + q].nkb + 1) >> 1;
     Stages r;
-    r.begin = total * pair / p.split;
-    r.end = total * (pair + 1) / p.split;
+    const int piece = p.ranges > 1 ? t % p.ranges : pair, pieces = p.ranges > 1 ? p.ranges : p.split;
+    r.begin = total * piece / pieces;
+    r.end = total * (piece + 1) / pieces;
     r.low_at = pair == p.split - 1 ? max(r.begin, total - kLrLead) : -1;  // with the last range
     return r;
 }
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kFp8GemmThreads, 1) fp8_gemm_kernel(const __gr
             };
             const Fp8Out &o = p.out[ti.out];
             ok = for_stages(
-                p, o, stages_of(p, o, pair),
+                p, o, stages_of(p, o, pair, t),
                 [&](int q, int kb, bool two) { return load(&p.tm_a[q], &p.tm_b[q], kb * 128, 128, two, kT, kBBytes); },
                 [&](int q, int j, bool two) { return load(&p.tm_t[q], &p.tm_u[q], j * 64, 64, two, false, kUBytes); });
         }
@@ -343,7 +346,7 @@ __global__ void __launch_bounds__(kFp8GemmThreads, 1) fp8_gemm_kernel(const __gr
                 if (ok && lr_count > 0) ok = warp_wait<true>(l_empty, (lr_count - 1) & 1u, limits);
                 if (!ok) break;
                 tc_fence_after();
-                const Stages range = stages_of(p, o, pair);
+                const Stages range = stages_of(p, o, pair, t);
                 const int lr = range.low_at >= 0 ? lr_blocks(p, o) : 0;
                 int lr_left = lr;
                 uint32_t acc = 0;
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(kFp8GemmThreads, 1) fp8_gemm_kernel(const __gr
         for (int t = cluster; t < p.num_tiles && ok; t += nclusters) {
             const Tile ti = tile_of(p, t);
             const Fp8Out &o = p.out[ti.out];
-            const Stages range = stages_of(p, o, pair);
+            const Stages range = stages_of(p, o, pair, t);
             for (int q = 0, i = 0; q < o.nparts && ok; ++q) {
                 const Fp8Part &pt = p.part[o.part0 + q];
                 // stages i + 2c and i + 2c + 1 take chunk c
@@ -523,7 +526,8 @@ __global__ void __launch_bounds__(kFp8GemmThreads, 1) fp8_gemm_kernel(const __gr
                     }
                     g[0] += __shfl_xor_sync(0xffffffffu, g[0], 16);
                     const int row = (ti.m0 >> 5) + (int)rank * 4 + quarter;
-                    if (lane < 16 && n + lane < o.N && row * 32 < p.M) o.sums[(size_t)row * o.N + n + lane] = g[0];
+                    if (lane < 16 && n + lane < o.N && row * 32 < p.M)
+                        o.sums[((size_t)(t % p.ranges) * ((p.M + 31) >> 5) + row) * o.N + n + lane] = g[0];
                 }
             } else {
                 const bool vec = (o.N & 7) == 0 && (reinterpret_cast<uintptr_t>(o.y) & 15u) == 0;
@@ -674,6 +678,7 @@ void plan_fp8_gemm(Fp8GemmParams &p, const int *N, int nout, int blocks, bool ma
         }
     }
     p.m_tiles = m_tiles;
+    p.ranges = 1;
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, Fp8Mode mode, int num_sms, cudaStream_t stream) {
@@ -693,6 +698,7 @@ cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, Fp8Mode mode, int num_sms, c
         if (e != cudaSuccess) return e;
         done[dev][mode][width].store(true, std::memory_order_release);
     }
+    if (p.ranges > 1 && mode != kFp8ColSums) return cudaErrorInvalidValue;
     // a cut tile has a cluster of its own
     const int clusters = p.split == 1 && num_sms / 2 < p.num_tiles ? num_sms / 2 : p.num_tiles;
     cudaLaunchConfig_t cfg = {};

@@ -192,6 +192,8 @@ def test_forward(M, K, N, r):
     (1, 16, [1], [8]), (1, 128, [128], [0]), (2, 1152, [1024, 256, 256], [16, 16, 16]), (5, 272, [17, 0, 129], [8, 16, 0]),
     (64, 1152, [512, 512], [64, 64]), (127, 528, [130], [40]), (200, 144, [449], [72]), (257, 640, [225, 31], [256, 8]),
     (333, 2000, [301, 264, 77], [40, 0, 8]), (512, 384, [700], [320]), (130, 256, [96], [1024]),
+    # ds summed in ranges of the contraction
+    (70, 20000, [300], [8]), (300, 8208, [130, 500], [0, 16]),
     # dx cut along the contraction
     (150, 304, [4000, 130], [8, 0]), (513, 272, [700, 900, 1300], [16, 0, 72]), (40, 64, [9000], [256]),
     # tiles of 224 and of 128 columns, a second tile per CTA pair
