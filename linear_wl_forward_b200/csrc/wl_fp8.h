@@ -35,6 +35,7 @@ struct Fp8RowsJob {
     uint8_t *codes;
     long long ld_codes;
     uint8_t *scales;
+    __nv_bfloat16 *copy;   // with column scales: a copy of `a`, rows ld_codes elements apart, or nullptr
     long long warp_begin;  // filled by the launcher
 };
 // One matrix, or up to kMaxSeg bf16 ones with column scales, of `rows` rows in

@@ -325,7 +325,7 @@ wl_status forward_plan(wl_fp8_plan &f, const wl_bf16 *x, int M, int K, const wl_
     if (f.lowrank.njobs > 0 && (f.few || (long long)M * K <= 2 << 20)) {
         f.lowrank.quant = LowrankQuant{bf16(x), codes, scales, M, K, l.counters, f.few ? tiles : 0};
     } else {
-        f.quant.job[0] = Fp8RowsJob{x, K, K, nullptr, codes, K, scales, 0};
+        f.quant.job[0] = Fp8RowsJob{x, K, K, nullptr, codes, K, scales, nullptr, 0};
         f.quant.njobs = 1;
         f.quant.rows = M;
         f.quant.zero = l.counters;
@@ -473,12 +473,16 @@ wl_status backward_run(const uint8_t *x_codes, const uint8_t *x_scales, int M, i
         if (q.N == 0) continue;
         const Fp8Mat W{q.codes, q.scales, K, fp8_pitch(K)};
         const bool want_dv = q.dV && K > 0, want_dx = dx && K > 0;
+        __nv_bfloat16 *copy = nullptr;
         if (q.r > 0 && (want_dv || want_dx || q.dU)) {
             const __nv_bfloat16 *dy = bf16(q.dy);
             long long ld = q.N;
-            if (q.N % 8 != 0 || !aligned(q.dy, 16)) {
+            if (q.N % 8 != 0 || !aligned(q.dy, 16)) {  // copied, by the quantiser where it runs
                 ld = round16(q.N);
-                if (launch_fp8_pad_rows(dy, M, q.N, l.dy[i], ld, stream) != cudaSuccess) return WL_ERR_CUDA;
+                if (want_dx)
+                    copy = l.dy[i];
+                else if (launch_fp8_pad_rows(dy, M, q.N, l.dy[i], ld, stream) != cudaSuccess)
+                    return WL_ERR_CUDA;
                 dy = l.dy[i];
             }
             if ((want_dv || want_dx) && (st = add_lowrank(le, kLowrankRows, dy, ld, M, q.N, bf16(q.U), q.r, l.E[i],
@@ -498,7 +502,7 @@ wl_status backward_run(const uint8_t *x_codes, const uint8_t *x_scales, int M, i
         }
         if (want_dx) {
             const long long ldg = round16(q.N);
-            quant.job[quant.njobs++] = Fp8RowsJob{q.dy, q.N, q.N, q.s, l.g_codes[i], ldg, l.g_scales[i], 0};
+            quant.job[quant.njobs++] = Fp8RowsJob{q.dy, q.N, q.N, q.s, l.g_codes[i], ldg, l.g_scales[i], copy, 0};
             if ((st = set_part(gx, parts, Fp8Mat{l.g_codes[i], l.g_scales[i], ldg, fp8_pitch(q.N)}, M, q.N, W, q.N, K, true,
                                l.E[i], bf16(q.V), q.r, K)) != WL_OK)
                 return st;
@@ -545,7 +549,7 @@ wl_status wl_quantize_fp8(const void *a, wl_type type, int rows, int cols, int b
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     if (block_rows == kFp8Block) return from_cuda(launch_fp8_quantize_tiles(a, type, rows, cols, codes, scales, stream));
     Fp8RowsParams p = {};
-    p.job[0] = Fp8RowsJob{a, cols, cols, nullptr, codes, cols, scales, 0};
+    p.job[0] = Fp8RowsJob{a, cols, cols, nullptr, codes, cols, scales, nullptr, 0};
     p.njobs = 1;
     p.rows = rows;
     return from_cuda(launch_fp8_quantize_rows(p, type, stream));

@@ -48,7 +48,12 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constan
     raw.load(a, left, (reinterpret_cast<uintptr_t>(a) & 15u) == 0);
     float v[16];
     raw.unpack(v);
-    if (kColScale) {
+    if constexpr (kColScale) {
+        if (jb.copy && c < jb.ld_codes) {  // aligned rows for the kernels that follow
+            uint4 *dst = reinterpret_cast<uint4 *>(jb.copy + (size_t)row * jb.ld_codes + c);
+            dst[0] = make_uint4(raw.w[0], raw.w[1], raw.w[2], raw.w[3]);
+            dst[1] = make_uint4(raw.w[4], raw.w[5], raw.w[6], raw.w[7]);
+        }
         const float *cs = jb.colscale + c;
         Raw16<float> s;
         s.load(cs, left, (reinterpret_cast<uintptr_t>(cs) & 15u) == 0);
