@@ -60,7 +60,8 @@ cudaError_t launch_fp8_pad_rows(const __nv_bfloat16 *a, int rows, int cols, __nv
 enum LowrankMode {
     kLowrankRows = 0,  // A row-major in i, bf16
     kLowrankCols,      // A row-major in k, bf16
-    kLowrankCodes      // A row-major in k, 8 bits with 1 x 128 blocks along i; B in two bf16 terms
+    kLowrankCodes,     // A row-major in k, 8 bits with 1 x 128 blocks along i; B in two bf16 terms
+    kLowrankFew        // Rows with up to 16 rows: chosen by the plan
 };
 
 // Rows of A per tile that are loaded (Rows mode).
@@ -93,13 +94,14 @@ struct LowrankParams {
     LowrankJob job[kMaxSeg];
     int njobs;
     LowrankQuant quant;
-    int BN, split, tiles, stages, a_bytes, stage_bytes, tmem_cols;  // plan
+    LowrankMode mode;  // plan, with the next line
+    int BN, split, tiles, stages, a_bytes, stage_bytes, tmem_cols;
     int *status;
     unsigned long long timeout_ns;
 };
 
 void plan_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms);
-cudaError_t launch_fp8_lowrank(const LowrankParams &p, LowrankMode mode, cudaStream_t stream);
+cudaError_t launch_fp8_lowrank(const LowrankParams &p, cudaStream_t stream);
 
 // -------------------------------------------------------------------- GEMM ----
 // Tensor-core product over CTA pairs: output tiles of 256 rows x 224, 128 or 64 columns (BN),

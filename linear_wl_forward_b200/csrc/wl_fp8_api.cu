@@ -369,7 +369,7 @@ wl_status forward_launch(wl_fp8_plan &f, const Device &dev, cudaStream_t stream)
     }
     if (f.rows) return from_cuda(launch_fp8_rows(f.short_call, stream));
     if (f.quant.njobs > 0 && launch_fp8_quantize_rows(f.quant, WL_BF16, stream) != cudaSuccess) return WL_ERR_CUDA;
-    if (launch_fp8_lowrank(f.lowrank, kLowrankRows, stream) != cudaSuccess) return WL_ERR_CUDA;
+    if (launch_fp8_lowrank(f.lowrank, stream) != cudaSuccess) return WL_ERR_CUDA;
     return from_cuda(f.few ? launch_fp8_stream(f.stream, stream) : launch_fp8_gemm(f.gemm, kFp8Plain, dev.sms, stream));
 }
 
@@ -513,9 +513,9 @@ wl_status backward_run(const uint8_t *x_codes, const uint8_t *x_scales, int M, i
     plan_fp8_lowrank(lu, kLowrankCols, dev.sms);
     plan_fp8_lowrank(lv, kLowrankCodes, dev.sms);
     if (launch_fp8_quantize_rows(quant, WL_BF16, stream) != cudaSuccess ||
-        launch_fp8_lowrank(le, kLowrankRows, stream) != cudaSuccess ||
-        launch_fp8_lowrank(lu, kLowrankCols, stream) != cudaSuccess ||
-        launch_fp8_lowrank(lv, kLowrankCodes, stream) != cudaSuccess)
+        launch_fp8_lowrank(le, stream) != cudaSuccess ||
+        launch_fp8_lowrank(lu, stream) != cudaSuccess ||
+        launch_fp8_lowrank(lv, stream) != cudaSuccess)
         return WL_ERR_CUDA;
     if (parts > 0) {
         Fp8Out &o = add_out(gx, K, 0, parts);

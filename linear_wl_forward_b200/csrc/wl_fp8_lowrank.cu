@@ -3,6 +3,10 @@
 //   out[i][j] = sum_k A(i, k) B[k][j],   B row-major with r <= 1024 columns
 //
 //   T = x V, E = dy U    A row-major in i (K-major operand)
+//                        (up to 16 rows: on the warp-level MMA, m16n8k16, four
+//                        warps sharing 64 columns -- the tcgen05 MMA has 128
+//                        rows and one issuer, 400 cycles per 64 columns of the
+//                        contraction here against 230 of loads)
 //   dU = dy^T T          A row-major in k (M-major operand): no transposed copy
 //   dV = (x^)^T E        the same, with A in 8 bits: four warps expand a tile's
 //                        codes to bf16 (code * 2^E is exact there) on its way
@@ -52,6 +56,32 @@ constexpr int kMaxSplit = 16;
 __device__ __forceinline__ uint64_t mn_major_desc(uint32_t addr) {
     return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(kBBox >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// 16-byte chunk c of row r of a swizzled tile of 128-byte rows.
+__device__ __forceinline__ uint32_t chunk_addr(uint32_t tile, int r, int c) { return tile + r * 128 + ((c ^ (r & 7)) << 4); }
+
+// acc[n] += A B for 16 rows x 64 contraction columns of A and the 16 columns of
+// B from chunk c0 on.
+__device__ __forceinline__ void few_rows_block(uint32_t a_tile, uint32_t b_tile, int c0, int lane, float (&acc)[2][4]) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        uint32_t a[4], b[4];
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                     : "r"(chunk_addr(a_tile, lane & 15, 2 * s + (lane >> 4)))
+                     : "memory");
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
+                     : "r"(chunk_addr(b_tile, 16 * s + (lane & 15), c0 + (lane >> 4)))
+                     : "memory");
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+            asm volatile(
+                "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                : "+f"(acc[n][0]), "+f"(acc[n][1]), "+f"(acc[n][2]), "+f"(acc[n][3])
+                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[2 * n]), "r"(b[2 * n + 1]));
+    }
 }
 
 // Two E4M3 codes (low byte first) times a power of two, as a pair of bf16.
@@ -116,7 +146,7 @@ __device__ __forceinline__ void quantize_range(const LowrankQuant &q, int c0, in
 
 template <int kMode>
 __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __grid_constant__ LowrankParams p) {
-    constexpr bool kCodes = kMode == kLowrankCodes;
+    constexpr bool kCodes = kMode == kLowrankCodes, kFew = kMode == kLowrankFew, kRows = kFew || kMode == kLowrankRows;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(base + (size_t)p.stages * p.stage_bytes);
@@ -138,7 +168,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
     const int i_tiles = (jb.I + 127) / 128;
     const int i0 = (local % i_tiles) * 128, j0 = (local / i_tiles) * p.BN;
     const int width = min(p.BN, jb.r - j0), n_mma = (width + 15) & ~15, boxes = (width + 63) / 64;
-    const bool quant = kMode == kLowrankRows && p.quant.a != nullptr;
+    const bool quant = kRows && p.quant.a != nullptr;
     int per = (jb.kb + S - 1) / S;
     if (quant) per = (per + 1) & ~1;  // whole 128-column blocks
     const int kb0 = min((int)rank * per, jb.kb), kb1 = min(kb0 + per, jb.kb);
@@ -147,7 +177,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], kFew ? 4 : 1);  // the MMAs' commit, or the warps that read
             mbar_init(&ready[i], kExpanders);
         }
         mbar_init(done, 1);
@@ -158,18 +188,21 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
     // Dependents start once everything before this kernel is complete.
     pdl_wait_primary();
     pdl_launch_dependents();
-    if (kMode == kLowrankRows && p.quant.a)
+    if (kRows && p.quant.a)
         for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < p.quant.n_zero; i += gridDim.x * blockDim.x) p.quant.zero[i] = 0;
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, p.tmem_cols);
-        tmem_relinquish();
+    uint32_t tmem = 0;
+    if (!kFew) {
+        if (warp == 1) {
+            tmem_alloc(tmem_slot, p.tmem_cols);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        tmem = *tmem_slot;
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
 
-    const uint32_t a_bytes = kMode == kLowrankRows ? (uint32_t)p.a_bytes : kATile;
+    const uint32_t a_bytes = kRows ? (uint32_t)p.a_bytes : kATile;
     const uint32_t b_off = a_bytes + (kCodes ? kCodeTile : 0);
     bool ok = true;
     if (warp == 0) {
@@ -182,7 +215,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
                 uint8_t *st = base + (size_t)r.slot * p.stage_bytes;
                 uint64_t *bar = &full[r.slot];
                 mbar_arrive_expect_tx(bar, bytes);
-                if (kMode == kLowrankRows) {
+                if (kRows) {
                     tma_load_2d(st, &jb.tm_a, kb * 64, i0, bar);
                 } else if (kMode == kLowrankCols) {
                     tma_load_2d(st, &jb.tm_a, i0, kb * 64, bar);
@@ -205,7 +238,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
                 mbar_wait(&full[i % p.stages], (i / p.stages) & 1u, p.status, 1000000ull);
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 1 && !kFew) {
         // fp32 sums of bf16 products; A M-major (bit 15) unless its rows run along i; B N-major (bit 16)
         const uint32_t idesc = idesc_bf16_f32(128, n_mma) | (kMode == kLowrankRows ? 0u : 1u << 15) | 1u << 16;
         const uint32_t s0 = smem_addr(base);
@@ -240,7 +273,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
             mbar_wait(done, 0, p.status, kDrainNs);
         }
         __syncwarp();
-    } else {
+    } else if (warp > 1) {
         const int tid = threadIdx.x - 64;
         if (kCodes) {
             // 16 codes of one contraction row per step, two steps of 32 rows per
@@ -287,14 +320,34 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
                 if (++slot == (uint32_t)p.stages) slot = 0, ph ^= 1u;
             }
         }
+        float few[2][4] = {};  // kFew: columns 16 (warp - 2) .. + 15 of 16 rows
+        if (kFew) {
+            Ring r(p.stages);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!(ok = warp_wait(&full[r.slot], r.phase, limits))) break;
+                const uint32_t st = smem_addr(base) + r.slot * p.stage_bytes;
+                few_rows_block(st, st + b_off, 2 * (warp - 2), lane, few);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[r.slot]);
+                r.advance();
+            }
+        }
         if (quant) quantize_range(p.quant, kb0 * 64, min(kb1 * 64, p.quant.cols), unit, gridDim.x / S, tid);
         // MMAs done.  A CTA with an empty range of the contraction has no sums.
-        if (ok && warp < 6 && kb1 > kb0) ok = warp_wait(done, 0, limits);
+        if (!kFew && ok && warp < 6 && kb1 > kb0) ok = warp_wait(done, 0, limits);
         tc_fence_after();
         const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16);
         float *buf = reinterpret_cast<float *>(base);  // [column][row], over the idle stages
-        if (ok && warp < 6)
+        if (kFew) {
+            // through the exchange buffer, split or not (the stages are idle once all four warps are here)
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    buf[((warp - 2) * 16 + n * 8 + 2 * (lane & 3) + (i & 1)) * 128 + (lane >> 2) + 8 * (i >> 1)] = few[n][i];
+        } else if (ok && warp < 6)
             for (int c = 0; c < n_mma; c += 8) {
                 float v[8];
                 if (kb1 > kb0) {
@@ -317,11 +370,11 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (!kFew && warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, p.tmem_cols);
     }
-    if (S > 1) {
+    if (S > 1 || kFew) {
         __syncwarp();
         cluster_sync();  // every CTA's sums are in its shared memory
         if (warp >= 2 && warp < 6 && ok) {
@@ -374,7 +427,8 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
 // 128 x 256 tiles cut in four took 63 us where whole ones take 28).
 static void choose_tiles(LowrankParams &p, int terms, int num_sms) {
     double best = 0;
-    for (int bn = 256; bn >= 64; bn /= 2)
+    const bool few = p.mode == kLowrankFew;
+    for (int bn = few ? 64 : 256; bn >= 64; bn /= 2)
         for (int s = 1; s <= kMaxSplit; s *= 2) {
             long long tiles = 0;
             int kb = 0, widest = 0;
@@ -385,7 +439,8 @@ static void choose_tiles(LowrankParams &p, int terms, int num_sms) {
             }
             if (bn > 64 && bn / 2 >= widest) continue;
             const int cols = std::min(bn, (widest + 15) / 16 * 16);
-            const double block = std::max({2.0 * cols * terms, (p.a_bytes + 128.0 * cols * terms) / 48, 200.0 + 256.0 * terms});
+            const double loads = (p.a_bytes + 128.0 * cols * terms) / 48;
+            const double block = few ? loads : std::max({2.0 * cols * terms, loads, 200.0 + 256.0 * terms});
             const double waves = (double)((tiles * s + num_sms - 1) / num_sms);
             const double cost = waves * (((kb + s - 1) / s) * block + 5000 + (s > 1 ? 1000 + 60.0 * cols : 0));
             if (best == 0 || cost < best) {
@@ -401,6 +456,7 @@ void plan_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms) {
     const int terms = mode == kLowrankCodes ? 2 : 1;
     int rows = 0;
     for (int i = 0; i < p.njobs; ++i) rows = std::max(rows, lowrank_a_rows(p.job[i].I));
+    p.mode = mode == kLowrankRows && rows <= 16 ? kLowrankFew : mode;
     p.a_bytes = mode == kLowrankRows ? rows * 128 : (int)kATile;
     choose_tiles(p, terms, num_sms);
     int widest = 0, longest = 0;
@@ -412,25 +468,27 @@ void plan_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms) {
         widest = std::max(widest, j.r);
         longest = std::max(longest, (j.kb + p.split - 1) / p.split);
     }
-    const int cols = std::min((widest + 15) / 16 * 16, p.BN);
+    const int cols = p.mode == kLowrankFew ? p.BN : std::min((widest + 15) / 16 * 16, p.BN);
     p.stage_bytes = (int)(p.a_bytes + (mode == kLowrankCodes ? kCodeTile : 0) + terms * ((cols + 63) / 64) * kBBox);
     // narrow tiles leave room for a second CTA on the SM, or for the kernel that follows
     p.stages = std::min(kMaxStages, (p.BN > 64 ? 200 * 1024 : p.a_bytes < (int)kATile ? 60 * 1024 : 100 * 1024) / p.stage_bytes);
     p.stages = std::max(2, std::min(p.stages, longest));
-    // the exchange of a split tile reuses the stages
-    while (p.split > 1 && p.stages * p.stage_bytes < cols * 512) ++p.stages;
+    // the exchange of a split tile (and the results of few rows) reuse the stages
+    while ((p.split > 1 || p.mode == kLowrankFew) && p.stages * p.stage_bytes < cols * 512) ++p.stages;
     p.tmem_cols = 32;
     while (p.tmem_cols < cols) p.tmem_cols *= 2;
 }
 
-cudaError_t launch_fp8_lowrank(const LowrankParams &p, LowrankMode mode, cudaStream_t stream) {
+cudaError_t launch_fp8_lowrank(const LowrankParams &p, cudaStream_t stream) {
     if (p.njobs == 0) return cudaSuccess;
+    const LowrankMode mode = p.mode;
     // an MMA reads 128 rows of A, so the last stage's tile may end behind the stages
     const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + std::max<size_t>((3 * kMaxStages + 1) * 8 + 32, kATile);
-    if (p.stages > kMaxStages || smem > 227 * 1024 || (p.quant.a && mode != kLowrankRows)) return cudaErrorInvalidValue;
-    void (*const kernels[3])(LowrankParams) = {lowrank_kernel<kLowrankRows>, lowrank_kernel<kLowrankCols>,
-                                               lowrank_kernel<kLowrankCodes>};
-    static std::atomic<bool> done[64][3] = {};
+    if (p.stages > kMaxStages || smem > 227 * 1024 || (p.quant.a && mode != kLowrankRows && mode != kLowrankFew))
+        return cudaErrorInvalidValue;
+    void (*const kernels[4])(LowrankParams) = {lowrank_kernel<kLowrankRows>, lowrank_kernel<kLowrankCols>,
+                                               lowrank_kernel<kLowrankCodes>, lowrank_kernel<kLowrankFew>};
+    static std::atomic<bool> done[64][4] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
