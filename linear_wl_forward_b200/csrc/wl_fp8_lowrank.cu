@@ -26,7 +26,8 @@
 // are cut instead, to put every SM to work.
 //
 //   warp 0  TMA producer;  warp 1  MMA issuer;  warps 2-5  epilogue;
-//   warps 2-9  expansion of codes, where there are any
+//   warps 2-9  expansion of codes, where there are any;  warps 6-9  quantisation
+//   beside few rows
 #include <algorithm>
 #include <atomic>
 #include <cstring>
@@ -42,8 +43,9 @@ namespace wl {
 
 namespace {
 
-// warps 2.. : four of them run the epilogue; in Codes mode eight expand the codes
-constexpr int threads_of(int mode) { return mode == kLowrankCodes ? 320 : 192; }
+// warps 2-5 run the epilogue (with few rows the products, too); warps 2-9 expand
+// codes, warps 6-9 quantise beside the products of few rows
+constexpr int threads_of(int mode) { return mode == kLowrankCodes || mode == kLowrankFew ? 320 : 192; }
 constexpr int kExpanders = 8;
 constexpr uint32_t kATile = 16384;  // 128 x 64 bf16
 constexpr uint32_t kBBox = 8192;    // 64 x 64 bf16
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
             }
         }
         float few[2][4] = {};  // kFew: columns 16 (warp - 2) .. + 15 of 16 rows
-        if (kFew) {
+        if (kFew && warp < 6) {
             Ring r(p.stages);
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!(ok = warp_wait(&full[r.slot], r.phase, limits))) break;
@@ -332,14 +334,16 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
                 r.advance();
             }
         }
-        if (quant) quantize_range(p.quant, kb0 * 64, min(kb1 * 64, p.quant.cols), unit, gridDim.x / S, tid);
+        // beside the products of few rows (after them: 36.9 us, beside them 35.0)
+        if (quant && (!kFew || warp >= 6))
+            quantize_range(p.quant, kb0 * 64, min(kb1 * 64, p.quant.cols), unit, gridDim.x / S, tid & 127);
         // MMAs done.  A CTA with an empty range of the contraction has no sums.
         if (!kFew && ok && warp < 6 && kb1 > kb0) ok = warp_wait(done, 0, limits);
         tc_fence_after();
         const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16);
         float *buf = reinterpret_cast<float *>(base);  // [column][row], over the idle stages
-        if (kFew) {
+        if (kFew && warp < 6) {
             // through the exchange buffer, split or not (the stages are idle once all four warps are here)
             asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     buf[((warp - 2) * 16 + n * 8 + 2 * (lane & 3) + (i & 1)) * 128 + (lane >> 2) + 8 * (i >> 1)] = few[n][i];
-        } else if (ok && warp < 6)
+        } else if (!kFew && ok && warp < 6)
             for (int c = 0; c < n_mma; c += 8) {
                 float v[8];
                 if (kb1 > kb0) {
@@ -470,8 +474,10 @@ void plan_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms) {
     }
     const int cols = p.mode == kLowrankFew ? p.BN : std::min((widest + 15) / 16 * 16, p.BN);
     p.stage_bytes = (int)(p.a_bytes + (mode == kLowrankCodes ? kCodeTile : 0) + terms * ((cols + 63) / 64) * kBBox);
-    // narrow tiles leave room for a second CTA on the SM, or for the kernel that follows
-    p.stages = std::min(kMaxStages, (p.BN > 64 ? 200 * 1024 : p.a_bytes < (int)kATile ? 60 * 1024 : 100 * 1024) / p.stage_bytes);
+    // Narrow tiles leave room for a second CTA on the SM: 5376 -> 2 x 21504 at rank 256
+    // and 100 tokens takes 77.3 us with 100 KB, 83.8 with 120; 21504 -> 5376 takes
+    // 51.4 us with 100 KB, 52.9 with 60.
+    p.stages = std::min(kMaxStages, (p.BN > 64 ? 200 * 1024 : 100 * 1024) / p.stage_bytes);
     p.stages = std::max(2, std::min(p.stages, longest));
     // the exchange of a split tile (and the results of few rows) reuse the stages
     while ((p.split > 1 || p.mode == kLowrankFew) && p.stages * p.stage_bytes < cols * 512) ++p.stages;
