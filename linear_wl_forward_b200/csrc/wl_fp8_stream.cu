@@ -318,7 +318,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
         for (Segment s; walk.next(p, s); ++count) {
             const Fp8StreamSeg &sg = p.seg[s.seg];
             const uint32_t set = count & 1u;
-            const bool whole = s.u0 == 0 && s.u1 == s.nu;
+            // every rank of a cluster leaves its sums for the exchange, also the one
+            // that has all units of a short tile beside ranks that have none
+            const bool whole = p.cluster == 1 && s.u0 == 0 && s.u1 == s.nu;
             const bool has_z = s.u0 < min(s.u1, sg.kpairs), has_d = s.u1 > max(s.u0, sg.kpairs);  // neither: a rank without units
             bool ok = warp_wait(&acc_full[set], (count >> 1) & 1u, limits);
             {
