@@ -17,6 +17,7 @@
 // applied to its fp32 sums.  Warps take chunks in turn and meet in shared
 // memory in a fixed order.
 #include <algorithm>
+#include <atomic>
 
 #include <cuda_fp16.h>
 
@@ -225,11 +226,13 @@ RowsKernel rows_kernel_of(int blocks) {
 
 int tokens_of(int M) { return M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : 8; }
 
-size_t rows_smem(const Fp8RowsForward &p) {
-    const int Kp = (p.K + 63) & ~63, kb = (p.K + 127) / 128, m = tokens_of(p.M);
-    return (size_t)kTokens * (Kp + 8) * 2 + (size_t)m * Kp * 2 + (size_t)kTokens * kb * 4 + (size_t)kWarps * m * 32 * 4 +
-           (size_t)kWarps * 16 * p.blocks * kTokens * 4;
+constexpr size_t rows_smem(int K, int tokens, int blocks) {
+    const int Kp = (K + 63) & ~63, kb = (K + 127) / 128;
+    return (size_t)kTokens * (Kp + 8) * 2 + (size_t)tokens * Kp * 2 + (size_t)kTokens * kb * 4 + (size_t)kWarps * tokens * 32 * 4 +
+           (size_t)kWarps * 16 * blocks * kTokens * 4;
 }
+constexpr size_t kRowsMaxSmem = rows_smem(kFp8RowsMaxK, kTokens, 4);
+static_assert(kRowsMaxSmem <= 227 * 1024, "shared memory of one CTA");
 }  // namespace
 
 // Calls that take this kernel: what every CTA repeats (x, V) has to stay small
@@ -256,17 +259,26 @@ bool plan_fp8_rows(Fp8RowsForward &p) {
 
 cudaError_t launch_fp8_rows(const Fp8RowsForward &p, cudaStream_t stream) {
     if (p.grid == 0) return cudaSuccess;
-    const size_t smem = rows_smem(p);
-    const RowsKernel kernel = p.M <= 1 ? rows_kernel_of<1>(p.blocks) : p.M <= 2 ? rows_kernel_of<2>(p.blocks)
-                              : p.M <= 4 ? rows_kernel_of<4>(p.blocks) : rows_kernel_of<8>(p.blocks);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const int tokens = tokens_of(p.M), width = tokens == 1 ? 0 : tokens == 2 ? 1 : tokens == 4 ? 2 : 3;
+    const RowsKernel kernel = tokens == 1 ? rows_kernel_of<1>(p.blocks) : tokens == 2 ? rows_kernel_of<2>(p.blocks)
+                              : tokens == 4 ? rows_kernel_of<4>(p.blocks) : rows_kernel_of<8>(p.blocks);
+    // Raised once per device and kernel, to what any call takes: a limit set for
+    // one call would refuse another thread's.
+    static std::atomic<bool> done[64][4][3] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::atomic<bool> &raised = done[dev][width][p.blocks >> 1];
+    if (!raised.load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRowsMaxSmem);
         if (e != cudaSuccess) return e;
+        raised.store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.grid);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = rows_smem(p.K, tokens, p.blocks);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

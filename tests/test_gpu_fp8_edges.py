@@ -1,5 +1,8 @@
 """GPU tests of 8-bit calls at the edges of what their kernels' plans cover."""
+import threading
+
 import pytest
+import torch
 
 import linear_wl_forward_b200 as wl
 from oracle import fp8
@@ -21,3 +24,34 @@ def test_short_projection_beside_a_long_one(M, K, N, r):
     done()
     for p, y in zip(projs, ys):
         within(y, fp8.forward(f64(x), *host(p))[0], "y")
+
+
+def test_short_calls_from_two_host_threads():
+    """Two host threads issue short calls of one kernel that need different
+    amounts of shared memory."""
+    g = gen(3)
+    cases = []
+    for K in (1152, 2048):
+        x, dev = tokens(g, 8, K).cuda(), [cuda(bundle(g, 256, K, 0))]
+        cases.append((x, dev, wl.stacked_forward_fp8(x, dev)[0].clone(), torch.cuda.Stream()))
+    done()
+    failed, start = [], threading.Barrier(len(cases))
+
+    def run(x, dev, want, stream):
+        try:
+            handle, ys = wl.prepare_stacked_fp8(x, dev), None
+            start.wait()
+            for _ in range(4000):
+                ys = handle(stream=stream)
+            stream.synchronize()
+            assert torch.equal(ys[0], want)
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    done()
+    assert not failed, failed
