@@ -460,11 +460,18 @@ class PreparedForwardFp8:
             plan = ctypes.c_void_p()
             _check(lib().wl_plan_stacked_forward_fp8(xp, M, K, arr, len(projs), None, None, _ptr(ws), n,
                                                      ctypes.byref(plan)), "wl_plan_stacked_forward_fp8")
-        self.ys = ys
-        self._keep = (x, projs, ws)
+        # the tensors themselves: the caller's lists may change
+        self._ys = tuple(ys)
+        self._keep = (x, *self._ys, *(t for p in projs for t in p if t is not None))
+        self._ws = ws
         self._device = dev
         self._plan = plan
         self._run = lib().wl_run_fp8_plan
+
+    @property
+    def ys(self):
+        """The outputs that every call writes."""
+        return list(self._ys)
 
     def __call__(self, stream=None):
         import torch
@@ -475,7 +482,7 @@ class PreparedForwardFp8:
         code = self._run(self._plan, _handle_on(self._device, stream) if stream is None else _stream_handle(stream))
         if code:
             _check(code, "wl_run_fp8_plan")
-        return self.ys
+        return list(self._ys)
 
     def __del__(self):
         if self._plan is not None and _lib is not None:
