@@ -601,19 +601,25 @@ class PreparedForward:
         if ys is None:
             ys = [torch.empty(M, W0.shape[0], dtype=torch.bfloat16, device=x.device)
                   for (W0, _, _, _) in projs]
-        self.ys = ys
-        self._keep = (x, projs, ys, prefetch)
+        # the tensors themselves: the caller's lists may change
+        self._ys, prefetch = tuple(ys), tuple(prefetch or ())
+        self._keep = (x, *self._ys, *(t for p in projs for t in p if t is not None), *prefetch)
         self._arr = (_Proj * len(projs))(*[_make_proj(W0, s, U, V, y, M, K)
                                            for (W0, s, U, V), y in zip(projs, ys)])
-        self._rng, self._nrng = prefetch_ranges(prefetch or [])
+        self._rng, self._nrng = prefetch_ranges(prefetch)
         self._args = (_dev_ptr(x, torch.bfloat16, "x", (M, K)), M, K, self._arr, len(projs), PATHS[path])
         self._fn = lib().wl_stacked_forward_prefetch
+
+    @property
+    def ys(self):
+        """The outputs that every call writes."""
+        return list(self._ys)
 
     def __call__(self, stream=None):
         xp, M, K, arr, P, path = self._args
         _check(self._fn(xp, M, K, arr, P, path, self._rng, self._nrng, _stream_handle(stream)),
                "wl_stacked_forward_prefetch")
-        return self.ys
+        return list(self._ys)
 
 
 def prepare_stacked(x, projs, ys=None, path="auto", prefetch=None) -> PreparedForward:

@@ -99,3 +99,18 @@ def test_fp8_handle_keeps_the_tensors_and_not_the_lists(fake):
     assert out == [y] and fake.launched == [5]
     out[0] = None
     assert handle(stream=5) == [y] and handle.ys == [y]
+
+
+def test_bf16_handle_keeps_the_tensors_and_not_the_lists(fake, monkeypatch):
+    monkeypatch.setattr(wl, "prefetch_ranges", lambda items: (None, 0))
+    x, proj, y = call()
+    proj, ahead = [FakeTensor(40, 64), *proj[2:]], FakeTensor(16)
+    tensors, projs, ys, prefetch = [x, *proj, y, ahead], [proj], [y], [ahead]
+    handle = wl.prepare_stacked(x, projs, ys=ys, prefetch=prefetch)
+    for a in (projs, proj, ys, prefetch):
+        a.clear()
+    assert all(any(t is h for h in held(handle)) for t in tensors)
+    out = handle(stream=5)
+    assert out == [y] and fake.launched == [5]
+    out[0] = None
+    assert handle(stream=5) == [y] and handle.ys == [y]
