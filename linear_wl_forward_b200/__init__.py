@@ -443,7 +443,11 @@ class PreparedForwardFp8:
     `stream` (default: torch's current stream), and returns the list of y_p.
     The tensors are kept alive and their storage must not be replaced.  Calls
     of one handle share its workspace, so they must not overlap on the GPU;
-    handles do not share anything."""
+    handles do not share anything.  A handle may be dropped while its calls
+    run: torch's allocator then gives its memory out again only behind them.
+    A graph that captured a call does not keep the handle: it has to live as
+    long as the graph is replayed, as the tensors have to.  A stream given as
+    a raw handle has to outlive the handle's memory."""
 
     _plan = None
 
@@ -464,6 +468,7 @@ class PreparedForwardFp8:
         self._ys = tuple(ys)
         self._keep = (x, *self._ys, *(t for p in projs for t in p if t is not None))
         self._ws = ws
+        self._streams = set()  # that calls ran on
         self._device = dev
         self._plan = plan
         self._run = lib().wl_run_fp8_plan
@@ -479,10 +484,28 @@ class PreparedForwardFp8:
         if self._device.index != torch.cuda.current_device():
             with torch.cuda.device(self._device):
                 return self(stream)
-        code = self._run(self._plan, _handle_on(self._device, stream) if stream is None else _stream_handle(stream))
+        handle = _handle_on(self._device, stream) if stream is None else _stream_handle(stream)
+        if handle not in self._streams:
+            self._use_on(handle, stream)
+        code = self._run(self._plan, handle)
         if code:
             _check(code, "wl_run_fp8_plan")
         return list(self._ys)
+
+    def _use_on(self, handle, stream):
+        """Tells torch's allocator that the handle's memory is used on this
+        stream, whichever streams it was allocated on."""
+        import torch
+
+        if stream is None:
+            stream = torch.cuda.current_stream(self._device)
+        elif isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self._device)
+        elif stream.device != self._device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {self._device}")
+        for t in self._keep if self._ws is None else (*self._keep, self._ws):
+            t.record_stream(stream)
+        self._streams.add(handle)
 
     def __del__(self):
         if self._plan is not None and _lib is not None:

@@ -55,3 +55,37 @@ def test_short_calls_from_two_host_threads():
         t.join()
     done()
     assert not failed, failed
+
+
+@pytest.mark.parametrize("M,K,N,r", [(16, 4112, [600], [64]), (3, 1040, [20000], [8]), (200, 528, [449, 30], [40, 8])])
+def test_handle_dropped_while_its_call_runs(M, K, N, r):
+    """The handle's memory, made on one stream and used on another, is not
+    given out again before the call that uses it has ended."""
+    g = gen(M)
+    x, dev = tokens(g, M, K).cuda(), [cuda(bundle(g, n, K, q)) for n, q in zip(N, r)]
+    want = wl.stacked_forward_fp8(x, dev)
+    ys = [torch.empty_like(y) for y in want]
+    done()
+    for raw in (False, True):
+        side = torch.cuda.Stream()
+        handle = wl.prepare_stacked_fp8(x, dev, ys=ys)
+        size = handle._ws.numel()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # about 10 ms
+        handle(stream=side.cuda_stream if raw else side)
+        del handle
+        junk = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        done()
+        assert all(torch.equal(a, b) for a, b in zip(ys, want)), (raw, len(junk))
+        for y in ys:
+            y.zero_()
+
+
+def test_handle_refuses_a_stream_of_another_device():
+    class Elsewhere:
+        cuda_stream, device = 12345, torch.device("cuda", 7)
+
+    g = gen(0)
+    handle = wl.prepare_stacked_fp8(tokens(g, 3, 64).cuda(), [cuda(bundle(g, 40, 64, 8))])
+    with pytest.raises(ValueError):
+        handle(stream=Elsewhere())

@@ -12,9 +12,13 @@ class FakeTensor:
 
     def __init__(self, *shape):
         self.shape = shape
+        self.streams = []
 
     def data_ptr(self):
         return 1 << 20
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
 
 
 class FakeLib:
@@ -66,6 +70,7 @@ def fake(monkeypatch):
     monkeypatch.setattr(wl, "_ptr_on", lambda device, t, *rest: t.data_ptr())
     monkeypatch.setattr(wl, "_dev_ptr", lambda t, *rest: t.data_ptr())
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: handle)
     return fake
 
 
@@ -99,6 +104,17 @@ def test_fp8_handle_keeps_the_tensors_and_not_the_lists(fake):
     assert out == [y] and fake.launched == [5]
     out[0] = None
     assert handle(stream=5) == [y] and handle.ys == [y]
+
+
+def test_fp8_handle_records_each_stream_once(fake, monkeypatch):
+    x, proj, y = call()
+    ws = FakeTensor(100)
+    monkeypatch.setattr(wl, "_workspace", lambda nbytes, device: ws)
+    handle = wl.prepare_stacked_fp8(x, [proj], ys=[y])
+    for stream in (5, 5, 9, 5, 9):
+        handle(stream=stream)
+    assert fake.launched == [5, 5, 9, 5, 9]
+    assert all(t.streams == [5, 9] for t in (x, *proj, y, ws))
 
 
 def test_bf16_handle_keeps_the_tensors_and_not_the_lists(fake, monkeypatch):
