@@ -151,6 +151,7 @@ struct Fp8GemmParams {
     // so their error grows with their length (2e-6 of ds at 20000 columns).
     int ranges;
     int m_tiles, num_tiles;
+    int early_next;   // the next kernel may start at once; not where it may read `y` before its wait
     int *status;
     unsigned long long timeout_ns;
 };
@@ -204,6 +205,7 @@ struct Fp8StreamParams {
     int pitch;
     int nseg, M;
     int early;  // the weights may be read before the wait for the previous kernel
+    int early_next;  // as in Fp8GemmParams
     // plan
     int Mp, stages, grid, tiles;
     int whole;               // tiles [0, whole) go to one CTA (or cluster) each

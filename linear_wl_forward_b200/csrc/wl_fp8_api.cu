@@ -172,6 +172,7 @@ void init_gemm(Fp8GemmParams &g, int M, const int *N, int nout, int blocks, bool
     std::memset(&g, 0, sizeof g);
     g.M = M;
     plan_fp8_gemm(g, N, nout, blocks, may_split, dev.sms);
+    g.early_next = true;
     g.status = dev.status;
     g.timeout_ns = wait_limit_ns();
 }
@@ -232,6 +233,7 @@ wl_status set_stream(Fp8StreamParams &sp, const Fp8Mat &X, int M, int K, const w
     plan_stream(sp, M, K, N, r, P);
     sp.x_scales = X.scales;
     sp.early = early;
+    sp.early_next = true;
     sp.parts = parts;
     sp.counters = counters;
     sp.status = dev.status;
@@ -625,10 +627,13 @@ wl_status wl_matmul_fp8(const uint8_t *a_codes, const uint8_t *a_scales, const u
         __nv_bfloat16 *T = nullptr;
         Fp8StreamParams sp;
         st = set_stream(sp, Fp8Mat{a_codes, a_scales, K, fp8_pitch(K)}, M, K, &q, &T, 1, l.parts, l.counters, false, dev);
+        // y may be the weights of a bf16 call, which reads those before its wait
+        sp.early_next = false;
         return st != WL_OK ? st : from_cuda(launch_fp8_stream(sp, stream));
     }
     Fp8GemmParams g;
     init_gemm(g, M, &N, 1, (K + kFp8Block - 1) / kFp8Block, true, dev);
+    g.early_next = false;
     if ((st = set_part(g, 0, Fp8Mat{a_codes, a_scales, K, fp8_pitch(K)}, M, K, Fp8Mat{b_codes, b_scales, K, fp8_pitch(K)},
                        N, K, false, nullptr, nullptr, 0, 0)) != WL_OK)
         return st;

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kFp8GemmThreads, 1) fp8_gemm_kernel(const __gr
     constexpr uint32_t kUBytes = kHalf * 128, kBBytes = kT ? kRow * 128 : kUBytes;
     constexpr uint32_t kRegionCols = kBN;  // region r at columns r * kBN
     constexpr uint32_t kSfCol = 2 * kBN;   // two slots of scales, 16 columns apart: A (4 columns), B (8)
-    pdl_launch_dependents();
+    if (p.early_next) pdl_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *sf_base = base + kFp8Stages * kFp8StageBytes;

@@ -109,7 +109,7 @@ struct Walk {
 }  // namespace
 
 __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_constant__ Fp8StreamParams p) {
-    pdl_launch_dependents();
+    if (p.early_next) pdl_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t stages = (uint32_t)p.stages, block_bytes = kWBytes + (uint32_t)p.Mp * 128, stage_bytes = 2 * block_bytes;

@@ -89,3 +89,26 @@ def test_handle_refuses_a_stream_of_another_device():
     handle = wl.prepare_stacked_fp8(tokens(g, 3, 64).cuda(), [cuda(bundle(g, 40, 64, 8))])
     with pytest.raises(ValueError):
         handle(stream=Elsewhere())
+
+
+@pytest.mark.parametrize("M,N,K", [(1024, 1152, 4096), (100, 5376, 2048), (128, 21504, 1152), (4096, 1152, 1152)])
+def test_product_is_the_next_calls_weight(M, N, K):
+    """y = A B^T as W0 of a bf16 call that directly follows: that call reads
+    its weights ahead of its wait for the previous kernel."""
+    g = gen(M)
+    a = tuple(torch.from_numpy(t).cuda() for t in fp8.quantize(f64(tokens(g, M, K)), 1))
+    codes, scales, *_ = bundle(g, N, K, 0)
+    b = (codes.cuda(), scales.cuda())
+    x, s = tokens(g, 1, N).cuda(), torch.ones(M, device="cuda")
+    W = wl.matmul_fp8(a, b)
+    done()
+    want = wl.linear_forward(x, W, s, None, None)
+    y = torch.empty_like(want)
+    for _ in range(10):
+        W.zero_()
+        y.zero_()
+        done()
+        wl.matmul_fp8(a, b, y=W)
+        wl.linear_forward(x, W, s, None, None, y=y)
+        done()
+        assert torch.equal(y, want)
