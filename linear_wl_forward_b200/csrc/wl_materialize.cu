@@ -19,7 +19,8 @@ __global__ void __launch_bounds__(256) materialize_kernel(const __nv_bfloat16 *_
                                                           const __nv_bfloat16 *__restrict__ U,
                                                           const __nv_bfloat16 *__restrict__ V,
                                                           __nv_bfloat16 *__restrict__ Weff, int N, int K, int r) {
-    pdl_launch_dependents();
+    // No early start for the next kernel: a forward reads its weights, which
+    // W_eff may be, before its wait for this one.
     pdl_wait_primary();
     __shared__ float us[kSlice][kTile + 1];  // [j][row n]
     __shared__ float vs[kSlice][kTile + 1];  // [j][column k]
