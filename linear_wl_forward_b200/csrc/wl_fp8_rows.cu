@@ -47,6 +47,14 @@ __device__ __forceinline__ uint32_t f16_pair(uint32_t w, int half) {
     return h;
 }
 
+// The product of two scales as two factors of about the same size: a sum times
+// one of them overflows (or loses bits) only where the result does, while the
+// scales themselves may cancel (weights of 2^118 with tokens of 2^-118).
+__device__ __forceinline__ float2 scale_halves(uint32_t a, uint32_t b) {
+    const uint32_t e = a == 255 || b == 255 ? 510 : a + b;  // a NaN scale makes both NaN
+    return make_float2(scale_value(e >> 1), scale_value(e - (e >> 1)));
+}
+
 }  // namespace
 
 // kM: tokens rounded up to 1, 2, 4 or 8;  kBlocks: 16-row blocks per CTA.
@@ -59,8 +67,8 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
     const int ldh = Kp + 8;                                       // halves; rows 16 bytes off 128, for the lanes' reads
     __half *xh = reinterpret_cast<__half *>(smem);                // [kTokens][ldh]
     __nv_bfloat16 *xb = reinterpret_cast<__nv_bfloat16 *>(xh + kTokens * ldh);  // [kM][Kp]
-    float *sx = reinterpret_cast<float *>(xb + kM * Kp);          // [kTokens][kb]
-    float *tp = sx + kTokens * kb;                                // [kWarps][kM][32], then T in [0]
+    uint32_t *sx = reinterpret_cast<uint32_t *>(xb + kM * Kp);    // [kTokens][kb] scale bytes
+    float *tp = reinterpret_cast<float *>(sx + kTokens * kb);                                // [kWarps][kM][32], then T in [0]
     float *zp = tp + kWarps * kM * 32;                            // [kWarps][16 kBlocks][kTokens]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -115,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
                 xd[1] = make_uint4(raw.w[4], raw.w[5], raw.w[6], raw.w[7]);
             }
         }
-        if ((threadIdx.x & 7) == 0) sx[m * kb + (c >> 7)] = scale_value((uint32_t)(E + 127));
+        if ((threadIdx.x & 7) == 0) sx[m * kb + (c >> 7)] = (uint32_t)(E + 127);
     }
     __syncthreads();
 
@@ -165,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
         const uint4 *bx = reinterpret_cast<const uint4 *>(xh + g * ldh + c * 64 + t * 16);
         const uint4 b0 = bx[0], b1 = bx[1];
         const uint32_t xb8[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-        const float f0 = sx[2 * t * kb + (c >> 1)], f1 = sx[(2 * t + 1) * kb + (c >> 1)];
+        const uint32_t e0 = sx[2 * t * kb + (c >> 1)], e1 = sx[(2 * t + 1) * kb + (c >> 1)];
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
             const uint32_t lo[4] = {wc[b][0].x, wc[b][0].y, wc[b][0].z, wc[b][0].w};
@@ -175,11 +183,12 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
             for (int i = 0; i < 4; ++i)
                 mma_f16(d, f16_pair(lo[i], 0), f16_pair(hi[i], 0), f16_pair(lo[i], 1), f16_pair(hi[i], 1), xb8[2 * i], xb8[2 * i + 1]);
             const int row = min(n0 + b * 16, sg.N - 1);
-            const float fw = scale_value(__ldg(sg.w_scales + (size_t)(row >> 7) * p.pitch + (c >> 1)));
-            z[b][0] = fmaf(d[0] * fw, f0, z[b][0]);
-            z[b][1] = fmaf(d[1] * fw, f1, z[b][1]);
-            z[b][2] = fmaf(d[2] * fw, f0, z[b][2]);
-            z[b][3] = fmaf(d[3] * fw, f1, z[b][3]);
+            const uint32_t ew = __ldg(sg.w_scales + (size_t)(row >> 7) * p.pitch + (c >> 1));
+            const float2 f0 = scale_halves(ew, e0), f1 = scale_halves(ew, e1);
+            z[b][0] = fmaf(d[0] * f0.x, f0.y, z[b][0]);
+            z[b][1] = fmaf(d[1] * f1.x, f1.y, z[b][1]);
+            z[b][2] = fmaf(d[2] * f0.x, f0.y, z[b][2]);
+            z[b][3] = fmaf(d[3] * f1.x, f1.y, z[b][3]);
         }
     }
 #pragma unroll

@@ -112,3 +112,20 @@ def test_product_is_the_next_calls_weight(M, N, K):
         wl.linear_forward(x, W, s, None, None, y=y)
         done()
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("M", [1, 3, 8, 40, 200])
+@pytest.mark.parametrize("up", [60, -100, 118, -118, 119])
+def test_scales_that_cancel(M, up):
+    """Large weights with small tokens and the other way round: each product
+    is of ordinary size, whatever its two scales are."""
+    N, K = 200, 640
+    g = gen(M + up)
+    sign = torch.tensor([1.0, -1.0, 1.0, -1.0, 1.0]).repeat_interleave(128)
+    x = (torch.randn(M, K, generator=g) * torch.exp2(-up * sign)).bfloat16()
+    w = torch.randn(N, K, generator=g).double() * torch.exp2(up * sign.double())
+    codes, scales = fp8.quantize(w.numpy(), 128)
+    p = (torch.from_numpy(codes), torch.from_numpy(scales), torch.ones(N), None, None)
+    y, = wl.stacked_forward_fp8(x.cuda(), [cuda(p)])
+    done()
+    within(y, fp8.forward(f64(x), *host(p))[0], "y")
