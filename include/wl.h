@@ -316,6 +316,7 @@ wl_status wl_quantize_fp8(const void *a, wl_type type, int rows, int cols, int b
 wl_status wl_matmul_fp8(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *b_codes,
                         const uint8_t *b_scales, wl_bf16 *y, int M, int N, int K,
                         void *workspace, size_t workspace_bytes, void *stream);
+/* 0 for sizes that the product refuses. */
 size_t wl_matmul_fp8_workspace(int M, int N, int K);
 
 /* One projection of an 8-bit call: W0 as an fp8 matrix with 128 x 128 blocks. */

@@ -593,7 +593,11 @@ MatmulLayout matmul_layout(int M, int N, int K, void *ws) {
 
 extern "C" {
 
-size_t wl_matmul_fp8_workspace(int M, int N, int K) { return wl::matmul_layout(M, N, K, nullptr).bytes; }
+size_t wl_matmul_fp8_workspace(int M, int N, int K) {
+    using namespace wl;
+    if (M > kMaxSize || N > kMaxSize || K > kMaxSize || K % 16 != 0) return 0;  // refused
+    return matmul_layout(M, N, K, nullptr).bytes;
+}
 
 wl_status wl_matmul_fp8(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *b_codes,
                         const uint8_t *b_scales, wl_bf16 *y, int M, int N, int K, void *workspace,
