@@ -283,6 +283,8 @@ def _ptr_on(device, t, dtype, name, shape):
             return t.data_ptr()
     except AttributeError:
         pass
+    if t is None:
+        raise TypeError(f"{name} must be a CUDA tensor")
     _dev_ptr(t, dtype, name, shape)  # says what is wrong
     raise ValueError(f"{name} is on {t.device}, expected {device}")
 

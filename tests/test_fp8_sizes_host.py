@@ -1,5 +1,7 @@
-"""CPU tests of the 8-bit operators' sizes: workspaces of calls that are refused."""
+"""CPU tests of the 8-bit operators' refusals: workspaces of refused sizes, and
+arguments that are no tensors."""
 import pytest
+import torch
 
 import linear_wl_forward_b200 as wl
 from linear_wl_forward_b200 import build as wlbuild
@@ -17,3 +19,8 @@ def test_refused_products_need_no_workspace(L):
                     (-1, 40000, 4096), (3, -1, 4096), (3, 40000, -16), (3, (1 << 30) + 1, 4096)):
         assert L.wl_matmul_fp8_workspace(M, N, K) == 0, (M, N, K)
     assert L.wl_matmul_fp8_workspace(3, 40000, 4096) > 0
+
+
+def test_none_where_a_tensor_is_needed():
+    with pytest.raises(TypeError, match="T must be a CUDA tensor"):
+        wl._ptr_on(torch.device("cuda", 0), None, torch.bfloat16, "T", (3, 8))

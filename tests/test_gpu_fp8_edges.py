@@ -144,3 +144,15 @@ def test_short_call_keeps_its_delta_in_fp32():
     y, = wl.stacked_forward_fp8(x.cuda(), [cuda((torch.from_numpy(codes), torch.from_numpy(scales), torch.ones(N), U.bfloat16(), V.bfloat16()))])
     done()
     assert (y == 1).all()
+
+
+def test_none_where_a_tensor_is_needed():
+    g = gen(0)
+    x, (codes, scales, s, U, V) = tokens(g, 4, 64).cuda(), cuda(bundle(g, 40, 64, 8))
+    for call in (lambda: wl.stacked_forward_fp8(x, [(codes, scales, None, U, V)]),
+                 lambda: wl.stacked_forward_fp8(x, [(codes, None, s, U, V)]),
+                 lambda: wl.matmul_fp8(wl.quantize_fp8(x), (codes, None)),
+                 lambda: wl.stacked_backward_fp8(wl.Fp8Checkpoint(*wl.quantize_fp8(x), [None]), [x[:, :40].contiguous()],
+                                                 [(codes, scales, s, U, V)])):
+        with pytest.raises(TypeError):
+            call()
