@@ -130,3 +130,70 @@ def backward(x_codes, x_scales, dys, Ts, projs):
             dV = (v, U16 * np.abs(v) + (1 + U16) * (np.abs(X).T @ eE + 2 * (M + 8) * U32 * vmag))
         per.append((ds, dU, dV))
     return (dx, U16 * np.abs(dx) + (1 + U16) * (err + 2 * terms * U32 * mag)), per
+
+
+# ------------------------------------------------------------------- norms ----
+# The bounds above grow with the number of terms and end as large as the values
+# themselves (K = 20000).  These hold the Frobenius norm of an output's error,
+# and see a single 128-column block that is left out of a long contraction.
+#   * half a bf16 step of each element of the output: U16 of its norm;
+#   * a bf16 operand's rounding E -> E + e, |e| <= U16 |E|, carried through B:
+#     ||e B||_F <= U16 ||E||_F ||B||_2;
+#   * fp32 sums on the tensor cores: a step adds 32 (8 bits) or 16 (bf16) terms
+#     and is off by at most 2^-23 of the partial sum, whose norm over the matrix
+#     stays below twice the result's: 2^-22 of it per step.
+STEP = 2.0 ** -22
+
+
+def norm(a):
+    return float(np.linalg.norm(a))
+
+
+def forward_norm(x, codes, scales, s, U, V):
+    """(y, bound on the norm of its error) of one projection."""
+    x = np.asarray(x, np.float64)
+    X, W = dequantize(*quantize(x, 1), 1), dequantize(codes, scales, 128)
+    y = np.asarray(s, np.float64) * (X @ W.T)
+    tol = STEP * (x.shape[1] / 32) * norm(y)
+    if U is not None:
+        T, U = x @ np.asarray(V, np.float64), np.asarray(U, np.float64)
+        y = y + T @ U.T
+        tol += (U16 + STEP * (x.shape[1] + U.shape[1]) / 16) * norm(T) * np.linalg.norm(U, 2)
+    return y, U16 * norm(y) + (1 + U16) * tol
+
+
+def ds_norm(x_codes, x_scales, dy, codes, scales, run):
+    """(ds, bound on the norm of its error) with sums of at most `run` columns on
+    the tensor cores: each z = x^ W^T is off by STEP per step of its runs, which
+    dy carries (Cauchy-Schwarz over the tokens), and the fp32 sums over runs and
+    tokens by one unit per term."""
+    X, W = dequantize(x_codes, x_scales, 1), dequantize(codes, scales, 128)
+    dy, z = np.asarray(dy, np.float64), X @ W.T
+    c = STEP * (run / 32) + (dy.shape[0] + X.shape[1] / run + 2) * U32
+    return (dy * z).sum(0), c * norm(np.linalg.norm(dy, axis=0) * np.linalg.norm(z, axis=0))
+
+
+def dx_norm(dys, projs):
+    """(dx, bound on the norm of its error)."""
+    dx, tol = 0.0, 0.0
+    for (codes, scales, s, U, V), dy in zip(projs, dys):
+        W, dy = dequantize(codes, scales, 128), np.asarray(dy, np.float64)
+        g = (np.asarray(s, np.float32) * dy.astype(np.float32)).astype(np.float64)
+        d = dequantize(*quantize(g, 1), 1) @ W
+        dx, tol = dx + d, tol + STEP * (dy.shape[1] / 32) * norm(d)
+        if U is not None:
+            U, V = np.asarray(U, np.float64), np.asarray(V, np.float64)
+            E = dy @ U
+            dx = dx + E @ V.T
+            tol += (U16 + STEP * (dy.shape[1] + U.shape[1]) / 16) * norm(E) * np.linalg.norm(V, 2)
+    return dx, U16 * norm(dx) + (1 + U16) * tol
+
+
+def dv_norm(x_codes, x_scales, dy, U):
+    """(dV, bound on the norm of its error): E takes part in two bf16 terms,
+    which leave at most U16^2 of it."""
+    X, dy, U = dequantize(x_codes, x_scales, 1), np.asarray(dy, np.float64), np.asarray(U, np.float64)
+    E = dy @ U
+    v = X.T @ E
+    tol = (U16 * U16 + STEP * (dy.shape[1] + X.shape[0]) / 16) * np.linalg.norm(X, 2) * norm(E)
+    return v, U16 * norm(v) + (1 + U16) * tol
