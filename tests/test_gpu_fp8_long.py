@@ -89,3 +89,19 @@ def test_ds_is_summed_in_ranges(M):
     _, [(ds, _, _)] = wl.stacked_backward_fp8(ckpt, [torch.ones(M, N, dtype=torch.bfloat16, device="cuda")], [dev], need_dx=False)
     done()
     assert (ds == 256.0 * M).all(), ds
+
+
+@pytest.mark.parametrize("M,N", [(2, 300), (40, 600), (200, 300), (700, 5000)])
+def test_dv_takes_e_in_two_terms(M, N):
+    """E = 257 and -256 in two tokens with x = 1: dV = 1, and 0 if E were rounded to bf16."""
+    K, r = 272, 8
+    x, dy, U = torch.zeros(M, K), torch.zeros(M, N), torch.zeros(N, r)
+    x[0], x[M - 1] = 1, 1
+    dy[0, :257], dy[M - 1, :256] = 1, -1
+    U[:, ::2] = 1
+    g = gen(0)
+    codes, scales, s, _, V = cuda(bundle(g, N, K, r))
+    ckpt = wl.Fp8Checkpoint(*wl.quantize_fp8(x.bfloat16().cuda()), [torch.zeros(M, r, dtype=torch.bfloat16, device="cuda")])
+    _, [(ds, dU, dV)] = wl.stacked_backward_fp8(ckpt, [dy.bfloat16().cuda()], [(codes, scales, s, U.bfloat16().cuda(), V)])
+    done()
+    assert (dV[:, ::2] == 1).all() and (dV[:, 1::2] == 0).all()
