@@ -9,8 +9,9 @@
 //                        contraction here against 230 of loads)
 //   dU = dy^T T          A row-major in k (M-major operand): no transposed copy
 //   dV = (x^)^T E        the same, with A in 8 bits: four warps expand a tile's
-//                        codes to bf16 (code * 2^E is exact there) on its way
-//                        to the MMA; E comes as two bf16 terms (high and low
+//                        codes to bf16 on its way to the MMA (code * 2^E is
+//                        exact for E >= -124; below, its lowest bits are
+//                        rounded to multiples of bf16's 2^-133); E comes as two bf16 terms (high and low
 //                        part), so that dV's error is its own rounding, at
 //                        twice the MMAs of a product that is small beside
 //                        the M x N x K ones

@@ -1,6 +1,7 @@
 """GPU tests of the 8-bit operators on long contractions and small terms, where
 the element-wise bounds of the oracle are as large as the values: exact
 integers, norms of the errors, and sums that a lost term shows in."""
+import numpy as np
 import pytest
 import torch
 
@@ -105,3 +106,31 @@ def test_dv_takes_e_in_two_terms(M, N):
     _, [(ds, dU, dV)] = wl.stacked_backward_fp8(ckpt, [dy.bfloat16().cuda()], [(codes, scales, s, U.bfloat16().cuda(), V)])
     done()
     assert (dV[:, ::2] == 1).all() and (dV[:, 1::2] == 0).all()
+
+
+@pytest.mark.parametrize("M", [5, 60, 200])
+def test_dv_of_the_smallest_scales(M):
+    """Codes whose values lie below 2^-126 down to 2^-136: bf16 holds multiples
+    of 2^-133, so an expanded code is off by at most 2^-134."""
+    K, N, r = 272, 130, 8
+    g = gen(M)
+    codes = torch.randint(0, 256, (M, K), generator=g).to(torch.uint8)
+    codes[(codes & 127) == 127] = 3
+    scales = torch.full((M, 4), 127, dtype=torch.uint8)
+    scales[:, :3] = torch.randint(0, 8, (M, 3), generator=g).to(torch.uint8)
+    wc, wsc, s, U, V = bundle(g, N, K, r)
+    U = (U.float() * 2.0 ** 60).bfloat16()
+    dy = (torch.randn(M, N, generator=g) * 2.0 ** 60).bfloat16()
+    ckpt = wl.Fp8Checkpoint(codes.cuda(), scales.cuda(), [torch.zeros(M, r, dtype=torch.bfloat16, device="cuda")])
+    _, [(ds, dU, dV)] = wl.stacked_backward_fp8(ckpt, [dy.cuda()], [cuda((wc, wsc, s, U, V))], need_dx=False)
+    done()
+    value, tol = fp8.dv_norm(codes.numpy(), scales.numpy(), f64(dy), f64(U))
+    E = f64(dy) @ f64(U)
+    near(dV, (value, tol + 2.0 ** -134 * np.sqrt(M * K) * fp8.norm(E)), "dV")
+    # where every value is at least 2^-127 no bits are lost
+    big = scales.clone()
+    big[:, :3] = 9
+    ckpt = wl.Fp8Checkpoint(codes.cuda(), big.cuda(), ckpt.T)
+    _, [(ds, dU, dV)] = wl.stacked_backward_fp8(ckpt, [dy.cuda()], [cuda((wc, wsc, s, U, V))], need_dx=False)
+    done()
+    near(dV, fp8.dv_norm(codes.numpy(), big.numpy(), f64(dy), f64(U)), "dV")
