@@ -1,4 +1,5 @@
 """GPU tests of 8-bit calls at the edges of what their kernels' plans cover."""
+import ctypes
 import threading
 
 import numpy as np
@@ -156,3 +157,32 @@ def test_none_where_a_tensor_is_needed():
                                                  [(codes, scales, s, U, V)])):
         with pytest.raises(TypeError):
             call()
+
+
+@pytest.mark.parametrize("M,K,N,r", [(3, 1152, [1024, 256], [16, 0]), (16, 4112, [600], [64]), (200, 528, [449, 30], [40, 8])])
+def test_plan_with_a_checkpoint(M, K, N, r):
+    """The C plan that also leaves the checkpoint, run twice, against the call."""
+    g = gen(M)
+    dev = [cuda(bundle(g, n, K, q)) for n, q in zip(N, r)]
+    x = tokens(g, M, K).cuda()
+    L, u8, bf16 = wl.lib(), torch.uint8, torch.bfloat16
+    ys = [torch.empty(M, n, dtype=bf16, device="cuda") for n in N]
+    T = [torch.empty(M, q, dtype=bf16, device="cuda") if q else None for q in r]
+    codes, scales = torch.empty(M, K, dtype=u8, device="cuda"), torch.empty(M, wl.fp8_scale_pitch(K), dtype=u8, device="cuda")
+    xp, _, _, arr = wl._forward_fp8_args(x, dev, ys, T)
+    n = L.wl_stacked_forward_fp8_workspace(M, K, arr, len(dev))
+    ws, plan = torch.empty(n, dtype=u8, device="cuda"), ctypes.c_void_p()
+    assert L.wl_plan_stacked_forward_fp8(xp, M, K, arr, len(dev), codes.data_ptr(), scales.data_ptr(), ws.data_ptr(), n,
+                                         ctypes.byref(plan)) == 0
+    try:
+        for _ in range(2):
+            x.copy_(tokens(g, M, K))
+            ws.fill_(255)
+            assert L.wl_run_fp8_plan(plan, torch.cuda.current_stream().cuda_stream) == 0
+            want, ckpt = wl.stacked_forward_fp8(x, dev, checkpoint=True)
+            done()
+            assert all(torch.equal(a, b) for a, b in zip(ys, want))
+            assert torch.equal(codes, ckpt.codes) and torch.equal(scales, ckpt.scales)
+            assert all(a is b is None or torch.equal(a, b) for a, b in zip(T, ckpt.T))
+    finally:
+        L.wl_free_fp8_plan(plan)
