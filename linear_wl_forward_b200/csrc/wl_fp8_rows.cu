@@ -50,9 +50,10 @@ __device__ __forceinline__ uint32_t f16_pair(uint32_t w, int half) {
 // The product of two scales as two factors of about the same size: a sum times
 // one of them overflows (or loses bits) only where the result does, while the
 // scales themselves may cancel (weights of 2^118 with tokens of 2^-118).
-__device__ __forceinline__ float2 scale_halves(uint32_t a, uint32_t b) {
-    const uint32_t e = a == 255 || b == 255 ? 510 : a + b;  // a NaN scale makes both NaN
-    return make_float2(scale_value(e >> 1), scale_value(e - (e >> 1)));
+__device__ __forceinline__ float2 scale_halves(uint32_t w, uint32_t x) {
+    const uint32_t e = w + x, h = e >> 1;
+    // the tokens' scales were made here: only the weights' can be NaN
+    return make_float2(scale_value(w == 255 ? 255 : h), scale_value(e - h));
 }
 
 }  // namespace
@@ -68,7 +69,7 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
     __half *xh = reinterpret_cast<__half *>(smem);                // [kTokens][ldh]
     __nv_bfloat16 *xb = reinterpret_cast<__nv_bfloat16 *>(xh + kTokens * ldh);  // [kM][Kp]
     uint32_t *sx = reinterpret_cast<uint32_t *>(xb + kM * Kp);    // [kTokens][kb] scale bytes
-    float *tp = reinterpret_cast<float *>(sx + kTokens * kb);                                // [kWarps][kM][32], then T in [0]
+    float *tp = reinterpret_cast<float *>(sx + kTokens * kb);     // [kWarps][kM][32], then T in [0]
     float *zp = tp + kWarps * kM * 32;                            // [kWarps][16 kBlocks][kTokens]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -77,10 +78,14 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
     const Fp8RowsSeg &sg = p.seg[sp];
     const int n0 = ((int)blockIdx.x - sg.cta_begin) * 16 * kBlocks;
 
-    // Weights of a chunk: 16 bytes of rows g and g + 8 of every block.
+    // Weights of a chunk: 16 bytes of rows g and g + 8 of every block, and the
+    // scale (a CTA's 16, 32 or 64 rows, from a multiple of that, have one).
     uint4 w[kBlocks][2];
+    uint32_t ew = 127;
+    const uint8_t *w_scales = sg.w_scales + (size_t)(n0 >> 7) * p.pitch;
     auto load_chunk = [&](int c) {
         const int k = c * 64 + t * 16;
+        if (c * 64 < K) ew = __ldg(w_scales + (c >> 1));
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
@@ -169,11 +174,12 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
         uint4 wc[kBlocks][2];
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) wc[b][0] = w[b][0], wc[b][1] = w[b][1];
+        const uint32_t e = ew;
         if (c + kWarps < chunks) load_chunk(c + kWarps);
         const uint4 *bx = reinterpret_cast<const uint4 *>(xh + g * ldh + c * 64 + t * 16);
         const uint4 b0 = bx[0], b1 = bx[1];
         const uint32_t xb8[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-        const uint32_t e0 = sx[2 * t * kb + (c >> 1)], e1 = sx[(2 * t + 1) * kb + (c >> 1)];
+        const float2 f0 = scale_halves(e, sx[2 * t * kb + (c >> 1)]), f1 = scale_halves(e, sx[(2 * t + 1) * kb + (c >> 1)]);
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
             const uint32_t lo[4] = {wc[b][0].x, wc[b][0].y, wc[b][0].z, wc[b][0].w};
@@ -182,9 +188,6 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 mma_f16(d, f16_pair(lo[i], 0), f16_pair(hi[i], 0), f16_pair(lo[i], 1), f16_pair(hi[i], 1), xb8[2 * i], xb8[2 * i + 1]);
-            const int row = min(n0 + b * 16, sg.N - 1);
-            const uint32_t ew = __ldg(sg.w_scales + (size_t)(row >> 7) * p.pitch + (c >> 1));
-            const float2 f0 = scale_halves(ew, e0), f1 = scale_halves(ew, e1);
             z[b][0] = fmaf(d[0] * f0.x, f0.y, z[b][0]);
             z[b][1] = fmaf(d[1] * f1.x, f1.y, z[b][1]);
             z[b][2] = fmaf(d[2] * f0.x, f0.y, z[b][2]);
