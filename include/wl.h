@@ -337,8 +337,7 @@ typedef struct {
  * quantised in blocks of 1 x 128 (x^), and for each projection
  *   T_p = x V_p,   y_p = s_p (.) (x^ W0_p^T) + T_p U_p^T,
  * with fp32 accumulation; T is formed from x itself (bf16) and rounded to
- * bf16 as an operand of the second product (short calls without a checkpoint
- * keep it in fp32); y is rounded once to bf16.
+ * bf16 as an operand of the second product; y is rounded once to bf16.
  *   x_codes, x_scales : where the quantised x is left (M x K codes and
  *     M x WL_FP8_SCALE_PITCH(K) scales), or both NULL.  Together with the
  *     projections' T they are the 8-bit checkpoint that

@@ -200,12 +200,14 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
         for (int i = 0; i < 4; ++i)
             zp[(warp * 16 * kBlocks + b * 16 + (i >> 1) * 8 + g) * kTokens + 2 * t + (i & 1)] = z[b][i];
     __syncthreads();
-    if (sg.r > 0) {  // T, which stays in fp32: no tensor core takes it
+    if (sg.r > 0) {
+        // T, rounded to bf16 as the tensor-core kernels take it, so that a call with
+        // a checkpoint and the same one without differ by the order of sums alone
         for (int i = threadIdx.x; i < kM * 32; i += kThreads) {
             float v = 0.f;
 #pragma unroll
             for (int q = 0; q < kWarps; ++q) v += tp[q * kM * 32 + i];
-            tp[i] = v;
+            tp[i] = __bfloat162float(__float2bfloat16_rn(v));
         }
         __syncthreads();
     }
