@@ -11,6 +11,10 @@
 namespace wl {
 
 constexpr int kFp8Block = 128;  // columns (and, for weights, rows) per scale
+// The plans estimate a call's cycles.  An SM was measured to take 46 bytes per
+// cycle into shared memory in the long GEMM; the rates in the estimates are the
+// ones whose choices were fastest for each kernel, and hold its other costs too.
+constexpr double kFp8GemmFill = 42, kFp8StreamFill = 42, kFp8LowrankFill = 48;
 
 inline int fp8_pitch(int cols) { return WL_FP8_SCALE_PITCH(cols); }
 

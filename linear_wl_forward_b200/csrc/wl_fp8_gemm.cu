@@ -653,7 +653,7 @@ GemmKernel kernel_of(int bn) {
 
 // The tile width and cut with the least estimated cycles: waves of tiles over
 // the CTA pairs, a block of the contraction at the slowest of the MMAs (2 cycles
-// per column), the loads (42 bytes per cycle) and the issue (330 cycles), about
+// per column), the loads (kFp8GemmFill) and the issue (330 cycles), about
 // 5000 cycles to start and drain a tile, and for a cut tile, all pairs of whose
 // clusters have to be resident, 3000 and 25 per column for the exchange.
 // 512 x 1152 over 8192: 12 whole tiles of 224 columns take 37 us.
@@ -665,7 +665,7 @@ void plan_fp8_gemm(Fp8GemmParams &p, const int *N, int nout, int blocks, bool ma
     for (int bn : {224, 128, 64}) {
         long long tiles = 0;
         for (int i = 0; i < nout; ++i) tiles += (long long)m_tiles * ((N[i] + bn - 1) / bn);
-        const double block = std::max({2.0 * bn, (16384 + 64.0 * bn) / 42, 330.0});
+        const double block = std::max({2.0 * bn, (16384 + 64.0 * bn) / kFp8GemmFill, 330.0});
         for (int s = 1; s <= 8; ++s) {
             if (s > 1 && (!may_split || tiles > kResident[s - 1] || blocks < 4 * s)) break;
             const double cost = (double)((tiles + pairs - 1) / pairs) * ((blocks + s - 1) / s * block + 5000) +

@@ -8,13 +8,13 @@
 //                        rows and one issuer, 400 cycles per 64 columns of the
 //                        contraction here against 230 of loads)
 //   dU = dy^T T          A row-major in k (M-major operand): no transposed copy
-//   dV = (x^)^T E        the same, with A in 8 bits: four warps expand a tile's
+//   dV = (x^)^T E        the same, with A in 8 bits: eight warps expand a tile's
 //                        codes to bf16 on its way to the MMA (code * 2^E is
 //                        exact for E >= -124; below, its lowest bits are
-//                        rounded to multiples of bf16's 2^-133); E comes as two bf16 terms (high and low
-//                        part), so that dV's error is its own rounding, at
-//                        twice the MMAs of a product that is small beside
-//                        the M x N x K ones
+//                        rounded to multiples of bf16's 2^-133); E comes as
+//                        two bf16 terms (high and low part), so that dV's
+//                        error is its own rounding, at twice the MMAs of a
+//                        product that is small beside the M x N x K ones
 //
 // B is read as it lies (N-major operand, boxes of 64 columns x 64 rows).
 // A CTA owns 128 rows x up to 256 columns of one product and a range of the
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1) lowrank_kernel(const __g
 
 // Tile width and split of the contraction, by an estimate of a call's cycles:
 // waves of CTAs, each with its blocks of the contraction at the slowest of the
-// MMAs (2 cycles per column), the loads (48 bytes per cycle and SM) and the
+// MMAs (2 cycles per column), the loads (kFp8LowrankFill) and the
 // issuing thread (450 cycles), plus 5000 for the start and the drain and, with
 // a split, the exchange of 128 x BN sums (60 cycles per column; measured:
 // 128 x 256 tiles cut in four took 63 us where whole ones take 28).
@@ -444,7 +444,7 @@ static void choose_tiles(LowrankParams &p, int terms, int num_sms) {
             }
             if (bn > 64 && bn / 2 >= widest) continue;
             const int cols = std::min(bn, (widest + 15) / 16 * 16);
-            const double loads = (p.a_bytes + 128.0 * cols * terms) / 48;
+            const double loads = (p.a_bytes + 128.0 * cols * terms) / kFp8LowrankFill;
             const double block = few ? loads : std::max({2.0 * cols * terms, loads, 200.0 + 256.0 * terms});
             const double waves = (double)((tiles * s + num_sms - 1) / num_sms);
             const double cost = waves * (((kb + s - 1) / s) * block + 5000 + (s > 1 ? 1000 + 60.0 * cols : 0));
@@ -475,9 +475,12 @@ void plan_fp8_lowrank(LowrankParams &p, LowrankMode mode, int num_sms) {
     }
     const int cols = p.mode == kLowrankFew ? p.BN : std::min((widest + 15) / 16 * 16, p.BN);
     p.stage_bytes = (int)(p.a_bytes + (mode == kLowrankCodes ? kCodeTile : 0) + terms * ((cols + 63) / 64) * kBBox);
-    // Narrow tiles leave room for a second CTA on the SM: 5376 -> 2 x 21504 at rank 256
-    // and 100 tokens takes 77.3 us with 100 KB, 83.8 with 120; 21504 -> 5376 takes
-    // 51.4 us with 100 KB, 52.9 with 60.
+    // Narrow tiles leave room for a second CTA on the SM where stages are large:
+    // 5376 -> 2 x 21504 at rank 256 and 100 tokens takes 77.3 us with 100 KB, 83.8
+    // with 120; 21504 -> 5376 takes 51.4 us with 100 KB, 52.9 with 60.  The stages of
+    // up to 16 tokens (10 KB) fill the 100 KB, and with the tail behind them an SM
+    // holds one such CTA; 92 KB, which would admit two, are slower (21504 -> 5376 at
+    // one token 31.9 us against 31.5) and 123 KB no faster.
     p.stages = std::min(kMaxStages, (p.BN > 64 ? 200 * 1024 : 100 * 1024) / p.stage_bytes);
     p.stages = std::max(2, std::min(p.stages, longest));
     // the exchange of a split tile (and the results of few rows) reuse the stages

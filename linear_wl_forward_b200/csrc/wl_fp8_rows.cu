@@ -32,7 +32,11 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kTokens = 8;  // the MMA's N
-constexpr int kAhead = 9;   // rows of V in flight per thread (all of them at 1152 x 16)
+// Rows of V in flight per thread: 9 cover 1152 x 16 in one go, and the fewer
+// passes are worth the registers where T is most of the call (1536 x 1152, rank
+// 16, one token: 5.9, 5.7, 5.3 and 5.6 us with 4, 6, 9 and 12; 9000 x 640, rank
+// 8, which needs three: 5.0, 5.1, 5.4 and 5.6).
+constexpr int kAhead = 9;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(

@@ -18,8 +18,8 @@
 // each tile to a cluster (up to 16 CTAs), whose sums meet over distributed
 // shared memory, again in rank order.
 //
-//   warp 0  TMA producer (up to 6 stages of two blocks; weights are fetched before the wait
-//           for the kernel that makes x and T)
+//   warp 0  TMA producer (up to 6 stages of two blocks; without a rank-r launch
+//           in front, weights are fetched before the wait for the kernel that makes x)
 //   warp 1  MMA issuer;  warp 2  scales;  warps 4-7  epilogue
 #include <algorithm>
 #include <atomic>
@@ -163,8 +163,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_stream_kernel(const __grid_co
 
     if (warp == 0) {
         // ------------------------------------------------------ producer ----
-        // weights of the first `stages` units, then (x and T made) their
-        // operands, then the rest in order
+        // early: weights of the first `stages` units, then (x made) their operands,
+        // then the rest in order; else everything in order once x and T are made
         const uint32_t head = p.early ? stages : 0;
         uint32_t issued = 0;
         bool ok = true;
@@ -460,9 +460,10 @@ static int fp8_stream_stage(const Fp8StreamParams &p) { return 2 * ((int)kWBytes
 
 // More tiles than SMs: whole ones for every CTA, the rest cut.  Fewer: the
 // cluster size with the least estimated cycles among those that are resident
-// at once, a unit coming at 42 bytes per cycle and SM, or in 1400 cycles when
-// all SMs stream, and the exchange taking about 4000 and 30 per token.
-// (5376 x 21504 at one token: 42 tiles whole 37 us, cut over 148 CTAs with
+// at once, a unit coming at kFp8StreamFill (at 46 bytes per cycle 21504 -> 5376 at
+// rank 256 and one token would take clusters of two: 32.9 us against 31.5), or in
+// 1400 cycles when all SMs stream, and the exchange taking about 4000 and 30 per
+// token.  (5376 x 21504 at one token: 42 tiles whole 37 us, cut over 148 CTAs with
 // their parts in memory 31, in clusters of three 22.)
 void plan_fp8_stream(Fp8StreamParams &p) {
     constexpr int kSms = kFp8StreamMaxGrid;
@@ -490,7 +491,7 @@ void plan_fp8_stream(Fp8StreamParams &p) {
         double least = 0;
         for (int c = 1; c <= kFp8StreamMaxCluster && c <= longest; ++c) {
             if (tiles > kResident[c - 1]) continue;
-            const double unit = std::max(fp8_stream_stage(p) / 42.0, 1400.0 * c * tiles / kSms);
+            const double unit = std::max(fp8_stream_stage(p) / kFp8StreamFill, 1400.0 * c * tiles / kSms);
             const double cost = (longest + c - 1) / c * unit + (c > 1 ? 4000 + 30.0 * p.M : 0);
             if (least == 0 || cost < least) {
                 least = cost;
@@ -511,7 +512,9 @@ void plan_fp8_stream(Fp8StreamParams &p) {
         const long long share = std::max(2, longest / (p.M <= 16 ? 8 : 4));
         p.cut_ctas = (int)std::min<long long>(kSms, std::max<long long>(1, (units - p.cut_unit) / share));
     }
-    // up to 32 tokens 150 KB hold enough in flight and leave room for the rank-r kernel beside
+    // Up to 32 tokens 150 KB hold enough in flight, and more stages gain nothing or
+    // lose: 5376 -> 2 x 21504 at one token takes 46.0 us with 150 KB and 49.2 with
+    // 200 (39.9 and 42.3 without ranks), 21504 -> 5376 31.5 and 31.3.
     p.stages = std::min(6, ((p.Mp <= 32 ? 150 : 200) * 1024) / fp8_stream_stage(p));
 }
 
