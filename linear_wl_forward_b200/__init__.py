@@ -248,6 +248,18 @@ def _handle_on(device, stream):
     return None
 
 
+def _torch_stream(stream, device):
+    """The torch stream of a torch stream or raw handle on `device`."""
+    import torch
+
+    if not isinstance(stream, int):
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        return stream
+    # ExternalStream takes 0, the default stream's handle, for "a new stream"
+    return torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+
+
 class _On:
     """Makes `device` current and, when a stream (torch stream or raw handle)
     is given, that stream too, so that what the call allocates belongs to the
@@ -265,11 +277,7 @@ class _On:
         with contextlib.ExitStack() as stack:
             stack.enter_context(torch.cuda.device(device))
             if stream is not None:
-                if isinstance(stream, int):
-                    stream = torch.cuda.ExternalStream(stream, device=device)
-                elif stream.device != device:
-                    raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-                stack.enter_context(torch.cuda.stream(stream))
+                stack.enter_context(torch.cuda.stream(_torch_stream(stream, device)))
             self.stack = stack.pop_all()
 
     def __exit__(self, *exc):
@@ -499,12 +507,7 @@ class PreparedForwardFp8:
         stream, whichever streams it was allocated on."""
         import torch
 
-        if stream is None:
-            stream = torch.cuda.current_stream(self._device)
-        elif isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=self._device)
-        elif stream.device != self._device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {self._device}")
+        stream = torch.cuda.current_stream(self._device) if stream is None else _torch_stream(stream, self._device)
         for t in self._keep if self._ws is None else (*self._keep, self._ws):
             t.record_stream(stream)
         self._streams.add(handle)

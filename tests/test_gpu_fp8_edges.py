@@ -171,3 +171,30 @@ def test_plan_with_a_checkpoint(M, K, N, r):
             assert all(a is b is None or torch.equal(a, b) for a, b in zip(T, ckpt.T))
     finally:
         L.wl_free_fp8_plan(plan)
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_raw_handle_of_the_default_stream(M):
+    """stream=0 is the default stream: behind what runs there already, and
+    ahead of what comes after."""
+    K, N, r = 1040, 300, 16
+    g = gen(M)
+    dev, x = [cuda(bundle(g, N, K, r))], tokens(g, M, K).cuda()
+    dy = (1e-3 * torch.randn(M, N, generator=g)).bfloat16().cuda()
+    want, ckpt = wl.stacked_forward_fp8(x, dev, checkpoint=True)
+    plain = wl.stacked_forward_fp8(x, dev)
+    wdx, wper = wl.stacked_backward_fp8(ckpt, [dy], dev)
+    handle = wl.prepare_stacked_fp8(torch.zeros_like(x), dev)
+    late = handle._keep[0]
+    done()
+    assert torch.cuda.current_stream().cuda_stream == 0
+    torch.cuda._sleep(20_000_000)
+    late.copy_(x)
+    codes, scales = wl.quantize_fp8(late, stream=0)
+    ys, saved = wl.stacked_forward_fp8(late, dev, checkpoint=True, stream=0)
+    dx, per = wl.stacked_backward_fp8(saved, [dy], dev, stream=0)
+    got = handle(stream=0)
+    copies = [t.clone() for t in (codes, scales, ys[0], dx, *per[0], got[0])]
+    done()
+    for a, b in zip(copies, (ckpt.codes, ckpt.scales, want[0], wdx, *wper[0], plain[0])):
+        assert torch.equal(a, b)

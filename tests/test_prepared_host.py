@@ -1,5 +1,6 @@
-"""CPU tests of what the prepared calls hold on to: a library and tensors that
-stand in for the real ones, so that no GPU is touched."""
+"""CPU tests of what the prepared calls hold on to, and of the streams that the
+8-bit calls run on: a library and tensors that stand in for the real ones, so
+that no GPU is touched."""
 import pytest
 
 import linear_wl_forward_b200 as wl
@@ -130,3 +131,22 @@ def test_bf16_handle_keeps_the_tensors_and_not_the_lists(fake, monkeypatch):
     assert out == [y] and fake.launched == [5]
     out[0] = None
     assert handle(stream=5) == [y] and handle.ys == [y]
+
+
+def test_raw_handle_0_is_the_default_stream(monkeypatch):
+    import torch
+
+    device = torch.device("cuda", 3)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: ("external", handle, device))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: ("default", device))
+    entered = []
+
+    class Enter(Nothing):
+        def __init__(self, what):
+            entered.append(what)
+
+    monkeypatch.setattr(torch.cuda, "device", Enter)
+    monkeypatch.setattr(torch.cuda, "stream", Enter)
+    for handle, want in ((0, ("default", device)), (5, ("external", 5, device))):
+        with wl._On(device, handle):
+            assert entered[-1] == want
