@@ -126,8 +126,9 @@ typedef enum {
  * and starts streaming W0, U, V and s while the previous kernel in the stream
  * still runs (x, y and the scratch are touched only after that kernel has
  * finished).  So W0, s, U and V must not be the outputs of the immediately
- * preceding forward or backward call of this library on the same stream;
- * outputs of any other kernel are safe. */
+ * preceding forward or backward call of this library on the same stream, nor
+ * of an earlier one with only such calls in between; outputs of any other
+ * kernel are safe. */
 wl_status wl_linear_forward(const wl_bf16 *x, const wl_bf16 *W0, const float *s,
                             const wl_bf16 *U, const wl_bf16 *V, wl_bf16 *y,
                             int M, int N, int K, int r, void *stream);
